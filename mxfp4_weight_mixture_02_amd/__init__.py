@@ -7,3 +7,4 @@ from .native import (Dims, MoeLayer, Mxfp4Error, SavedState, Workspace, lib,  # 
                      mxfp4_dequantize, mxfp4_moe_backward, mxfp4_moe_backward_dx, mxfp4_moe_forward,
                      mxfp4_moe_forward_noalloc, mxfp4_quantize, mxfp8_quantize,
                      workspace_bytes)
+from .ops import RouteOptions, Routing, moe_route, moe_route_backward  # noqa: F401

@@ -13,10 +13,11 @@
 #include <mutex>
 #include <vector>
 
+#include "abi_util.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
-namespace {
+namespace mxmoe {
 
 thread_local char g_err[512] = "";
 
@@ -33,7 +34,16 @@ int ok() {
   return MXFP4_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace mxmoe
+
+namespace {
+
+using mxmoe::aligned;
+using mxmoe::fail;
+using mxmoe::g_err;
+using mxmoe::hip_status;
+using mxmoe::launch_timed;
+using mxmoe::ok;
 
 constexpr size_t ALIGN = 256;
 // Routed-row count up to which the forward takes the decode kernels.
@@ -196,11 +206,6 @@ int check_weights(const mxfp4_moe_weights* w, const mxfp4_moe_dims& d) {
   return MXFP4_OK;
 }
 
-int hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(MXFP4_EHIP, "%s: %s", what, hipGetErrorString(e));
-  return MXFP4_OK;
-}
-
 // Optional per-kernel event timing (mxfp4_moe_kernel_timing).
 struct KernelTimer {
   struct Pending {
@@ -250,31 +255,33 @@ struct KernelTimer {
 };
 KernelTimer g_timer;
 
-// Enqueue one kernel; with timing on, bracket it with events on stream s.
-template <class F>
-int launch_timed(F&& enqueue, const char* name, hipStream_t s) {
-  hipEvent_t e0 = nullptr, e1 = nullptr;
-  const bool on = g_timer.on;
-  if (on) {
-    std::lock_guard<std::mutex> g(g_timer.mu);
-    e0 = g_timer.take();
-    e1 = g_timer.take();
-    if (e0) (void)hipEventRecord(e0, s);
-  }
-  int rc = hip_status(enqueue(), name);
-  if (on && e0 && e1) {
-    (void)hipEventRecord(e1, s);
-    std::lock_guard<std::mutex> g(g_timer.mu);
-    g_timer.pending.push_back({name, e0, e1});
-  }
-  return rc;
+}  // namespace
+
+namespace mxmoe {
+
+hipEvent_t timing_begin(hipStream_t s) {
+  if (!g_timer.on) return nullptr;
+  std::lock_guard<std::mutex> g(g_timer.mu);
+  hipEvent_t e0 = g_timer.take();
+  if (e0) (void)hipEventRecord(e0, s);
+  return e0;
 }
 
-#define LAUNCH(call, name)                                            \
-  do {                                                                \
-    int rc_ = launch_timed([&]() { return (call); }, name, s);        \
-    if (rc_ != MXFP4_OK) return rc_;                                  \
-  } while (0)
+void timing_end(hipEvent_t e0, const char* name, hipStream_t s) {
+  if (!e0) return;
+  std::lock_guard<std::mutex> g(g_timer.mu);
+  hipEvent_t e1 = g_timer.take();
+  if (!e1) {
+    g_timer.pool.push_back(e0);
+    return;
+  }
+  (void)hipEventRecord(e1, s);
+  g_timer.pending.push_back({name, e0, e1});
+}
+
+}  // namespace mxmoe
+
+namespace {
 
 // Validation shared by the two forward entry points (everything but the
 // scratch memory).

@@ -1,0 +1,34 @@
+// Launchers of the routing kernels (gate.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mxmoe {
+
+struct RouteArgs {
+  int64_t T;
+  int E, k;
+  int groups, top_groups;   // top_groups == groups: no groups
+  int sigmoid, top2, renorm;
+  float scale;
+  const float* logits;      // [T, E]
+  const float* bias;        // [E] or nullptr
+  int32_t* topk_idx;        // [T, k]
+  float* topk_w;            // [T, k]
+  int32_t* offsets;         // [E + 1]
+  int32_t* sorted_rows;     // [T * k]
+};
+
+// The choice and each workgroup's histogram [gate_blocks(T), E]; then in
+// place the rows of earlier workgroups, with the totals [E]; then offsets
+// and permutation.
+int64_t gate_blocks(int64_t T);
+hipError_t launch_gate(const RouteArgs& a, int32_t* hist, hipStream_t s);
+hipError_t launch_gate_prefix(const RouteArgs& a, int32_t* hist, int32_t* total, hipStream_t s);
+hipError_t launch_gate_scatter(const RouteArgs& a, const int32_t* base, const int32_t* total,
+                               hipStream_t s);
+hipError_t launch_gate_bwd(const RouteArgs& a, const int32_t* idx, const float* dw, float* dlogits,
+                           hipStream_t s);
+
+}  // namespace mxmoe

@@ -1,0 +1,151 @@
+"""Routing on the GPU against its float64 definition.
+
+Integers are equal.  A weight is an fp64 value rounded once to fp32 (2^-24
+relative; the fp64 steps add about 1e-15), a gradient the same: 1e-7
+relative, plus 1e-12 times the largest term of a sum for cancellation."""
+import numpy as np
+import pytest
+import torch
+
+import route_ref as ref
+from mxfp4_weight_mixture_02_amd import RouteOptions, moe_route, moe_route_backward
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+OPTIONS = [
+    RouteOptions(),
+    RouteOptions(renorm=False, scale=2.5),
+    RouteOptions(score="sigmoid", scale=2.5),
+    RouteOptions(score="sigmoid", renorm=False),
+]
+GROUPED = [
+    RouteOptions(score="sigmoid", groups=8, top_groups=4, group_score="top2", scale=2.5),
+    RouteOptions(groups=4, top_groups=2, renorm=False),
+    RouteOptions(score="sigmoid", groups=2, top_groups=1),
+]
+
+
+def _check(x, k, o, bias=None):
+    print("route", x.shape, k, o, bias is not None, flush=True)
+    t = torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(DEV)
+    b = None if bias is None else torch.from_numpy(np.asarray(bias, np.float32)).to(DEV)
+    r = moe_route(t, k, o, bias=b)
+    idx, w, off, rows = ref.route(np.asarray(x, np.float32), k, o, bias)
+    assert np.array_equal(r.topk_idx.cpu().numpy(), idx)
+    assert np.array_equal(r.expert_offsets.cpu().numpy(), off)
+    assert np.array_equal(r.sorted_rows.cpu().numpy(), rows)
+    np.testing.assert_allclose(r.topk_w.cpu().numpy(), w, rtol=1e-7, atol=1e-45)
+    return r
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (3, 5, 5), (7, 64, 4), (17, 65, 8), (64, 32, 4),
+                                   (129, 128, 4), (1000, 200, 7), (4097, 256, 8), (513, 16, 1)])
+@pytest.mark.parametrize("o", range(len(OPTIONS)))
+def test_sizes(T, E, k, o):
+    r = np.random.default_rng(T * 1000 + E)
+    bias = r.normal(size=E).astype(np.float32) * 0.05 if o % 2 else None
+    _check(r.normal(size=(T, E)) * 2, k, OPTIONS[o], bias)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (33, 8, 2), (70, 24, 3), (515, 256, 8), (9, 120, 8)])
+@pytest.mark.parametrize("o", range(len(GROUPED)))
+def test_groups(T, E, k, o):
+    r = np.random.default_rng(T * 7 + E)
+    per = E // GROUPED[o].groups
+    _check(r.normal(size=(T, E)), min(k, GROUPED[o].top_groups * per), GROUPED[o], r.normal(size=E) * 0.1)
+
+
+def test_one_expert_per_group_and_64_groups():
+    r = np.random.default_rng(0)
+    _check(r.normal(size=(21, 64)), 8, RouteOptions(groups=64, top_groups=9, group_score="top2"))
+    _check(r.normal(size=(21, 192)), 8, RouteOptions(groups=64, top_groups=3, group_score="top2"))
+
+
+def test_ties_masks_and_non_finite():
+    """Equal logits, rows of -inf, lowest values, +-inf and NaN, alone and mixed."""
+    r = np.random.default_rng(1)
+    lowest = np.finfo(np.float32).min
+    x = r.integers(-2, 3, size=(64, 96)).astype(np.float32)   # many ties
+    x[1] = -np.inf
+    x[2] = lowest
+    x[3, 5:] = -np.inf
+    x[4, 5:] = lowest
+    x[5] = -np.inf
+    x[5, 70] = 3.0
+    x[6, 10] = np.nan
+    x[7] = np.nan
+    x[8, 3] = np.inf
+    x[9] = 200.0
+    x[10] = -800.0          # sigmoid: 0 in fp64
+    x[11] = -90.0           # sigmoid: a denormal in fp32, a number in fp64
+    x[12, ::2] = -np.inf
+    x[12, 1::2] = np.nan
+    x[13] = -0.0
+    x[13, 4] = 0.0
+    for o in OPTIONS + [RouteOptions(score="sigmoid", groups=8, top_groups=2, group_score="top2"),
+                        RouteOptions(groups=8, top_groups=3)]:
+        _check(x, 8, o)
+        _check(x, 8, o, r.normal(size=96) * 0.1)
+
+
+def test_every_token_to_the_same_experts():
+    x = np.zeros((3000, 40), np.float32)
+    x[:, 7] = 1
+    r = _check(x, 3, RouteOptions())
+    assert r.expert_offsets.cpu().tolist()[0:3] == [0, 3000, 6000]
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (5, 7, 3), (66, 64, 4), (130, 129, 8), (1001, 128, 4)])
+@pytest.mark.parametrize("o", range(len(OPTIONS)))
+def test_gradient(T, E, k, o):
+    print("route grad", T, E, k, o, flush=True)
+    r = np.random.default_rng(T + E)
+    x = (r.normal(size=(T, E)) * 2).astype(np.float32)
+    dw = r.normal(size=(T, k)).astype(np.float32)
+    idx = np.stack([r.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    g = moe_route_backward(*(torch.from_numpy(v).to(DEV) for v in (x, idx, dw)), OPTIONS[o]).cpu().numpy()
+    want = ref.dlogits(x, idx, dw, OPTIONS[o])
+    np.testing.assert_allclose(g, want, rtol=1e-7, atol=1e-12 * max(1e-20, np.abs(dw).max() * OPTIONS[o].scale))
+
+
+def test_gradient_edges():
+    """Scores of 0, a repeated index, and indices outside the experts (skipped)."""
+    x = np.zeros((4, 6), np.float32)
+    x[0] = -800.0
+    x[1, 2:] = -np.inf
+    idx = np.array([[0, 1], [0, 1], [3, 3], [2, 5]], np.int32)
+    dw = np.array([[1, 2], [3, -1], [0.5, 0.25], [1, 1]], np.float32)
+    for o in OPTIONS:
+        t = [torch.from_numpy(v).to(DEV) for v in (x, idx, dw)]
+        np.testing.assert_allclose(moe_route_backward(*t, o).cpu().numpy(), ref.dlogits(x, idx, dw, o),
+                                   rtol=1e-7, atol=1e-11)
+        bad = idx.copy()
+        bad[3] = [-1, 6]
+        t[1] = torch.from_numpy(bad).to(DEV)
+        assert torch.all(moe_route_backward(*t, o)[3] == 0)
+
+
+def test_runs_repeat_and_replay():
+    """The same bits twice, from another stream, and from a captured graph
+    replayed on new logits."""
+    o = GROUPED[0]
+    g = torch.Generator(device=DEV).manual_seed(0)
+    xs = [torch.randn(700, 256, device=DEV, generator=g) for _ in range(3)]
+    want = [moe_route(x, 8, o) for x in xs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = moe_route(xs[0], 8, o)
+    side.synchronize()
+    assert all(torch.equal(getattr(other, n), getattr(want[0], n)) for n in vars(other))
+    x = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = moe_route(x, 8, o)
+    for i in (0, 1, 2, 1):
+        x.copy_(xs[i])
+        moe_route(xs[2], 8, o)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(getattr(got, n), getattr(want[i], n)) for n in vars(got))
