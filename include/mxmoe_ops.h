@@ -73,6 +73,87 @@ int mxmoe_route_backward(const mxmoe_route_opts* opts, int64_t T, int32_t E, int
                          const float* logits, const int32_t* topk_idx, const float* dw,
                          float* dlogits, void* stream);
 
+/* ------------------------------------------------- 8-bit dense products */
+
+/* An 8-bit matrix of `rows` rows and K columns:
+ *  codes   uint8 [rows, Kp], Kp = K rounded up to 128: OCP E4M3, the bytes
+ *          past K zero; 16-byte aligned
+ *  scales  uint8 UE8M0 (value 2^(s - 127)), K block by K block of 128:
+ *          block_rows == 1:   [Kp / 128, rows rounded up to 16], one scale
+ *                             for 1 x 128 elements, 16-byte aligned; the
+ *                             bytes past `rows` are not used
+ *          block_rows == 128: [Kp / 128, ceil(rows / 128)], one scale for
+ *                             128 x 128 elements
+ * Scale of a block: the smallest 2^e with its largest finite magnitude at
+ * most 448 * 2^e, e in [-127, 127] (all zeros: -127).  Element: the nearest
+ * E4M3 value to x / 2^e, ties to even; a non-finite x has the NaN code.
+ * rows and K are >= 1, K <= 2^22, rows < 2^31. */
+
+/* Quantizers.  x [rows, K], dtype MXMOE_F32 or MXMOE_BF16 (any alignment of
+ * the dtype's; 16 bytes and K % 8 == 0 run faster).  block_rows 1 or 128. */
+#define MXMOE_F32 0
+#define MXMOE_BF16 1
+int mxmoe_fp8_quantize(const void* x, int dtype, int64_t rows, int64_t K, int block_rows,
+                       uint8_t* codes, uint8_t* scales, void* stream);
+/* The transpose of x as an 8-bit matrix of K rows and `rows` columns with
+ * block_rows 1 (blocks run along x's rows); rows <= 2^22. */
+int mxmoe_fp8_quantize_t(const void* x, int dtype, int64_t rows, int64_t K, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+/* The transpose of an 8-bit matrix with block_rows 128, exactly: codes_t
+ * [K, rows rounded up to 128], scales_t [ceil(rows / 128), Kp / 128]. */
+int mxmoe_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                        uint8_t* codes_t, uint8_t* scales_t, void* stream);
+
+/* out [M, N] = X W^T + bias for 8-bit X [M, K] (block_rows 1) and W [N, K]
+ * (block_rows w_block_rows).  Products and sums in fp32 on the block-scaled
+ * matrix cores; bias bf16 [N] or NULL; out bf16 or fp32 (out_dtype), 16-byte
+ * aligned, rounded once. */
+int mxmoe_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes,
+                     const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                     int w_block_rows, const uint16_t* bias, int out_dtype, void* out,
+                     void* stream);
+/* The same from bf16 rows x [M, K], which are quantized with block_rows 1
+ * (in the product's own launch for few rows, else into the workspace), and
+ * W with block_rows 128.  A linear layer's input gradient is this product
+ * of dy [M, N] with the transposed W. */
+int mxmoe_fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const uint8_t* w_codes,
+                     const uint8_t* w_scales, const uint16_t* bias, int out_dtype, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream);
+/* The weights' gradient of a linear layer: dw fp32 [N, K] = dy^T x with dy
+ * bf16 [M, N] and x bf16 [M, K], both quantized in blocks of 128 tokens of
+ * one column.  M <= 2^22. */
+int mxmoe_fp8_linear_dw(int64_t M, int64_t N, int64_t K, const uint16_t* dy, const uint16_t* x,
+                        float* dw, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace of mxmoe_fp8_linear (dw 0) or mxmoe_fp8_linear_dw (dw
+ * 1); 0 if a size is out of range. */
+size_t mxmoe_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int dw);
+
+/* ------------------------------------------- 8-bit activation checkpoints */
+
+/* The clamped SwiGLU of mxfp4_moe.h on rows h bf16 [R, 2I] (gate 2j, up
+ * 2j + 1), with an 8-bit checkpoint of h: codes uint8 [R, 2I] (OCP E4M3) and
+ * scales uint8 [R, 2I / 32] (UE8M0, scale rule as above with blocks of 32).
+ * A code is the nearest whose value lies on the same side of the clamp
+ * bounds as the element (gate: above limit or not; up: above limit, below
+ * -limit or neither), so a backward pass from the checkpoint takes the
+ * forward's clamp decisions.  Non-finite elements have the NaN code.
+ * R >= 1, I % 16 == 0, alpha finite, limit > 0 and finite; tensors 16-byte
+ * aligned; R * 2I < 2^41. */
+
+/* a bf16 [R, I] out (NULL: the checkpoint alone). */
+int mxmoe_swiglu8_forward(const uint16_t* h, int64_t R, int64_t I, float alpha, float limit,
+                          uint16_t* a, uint8_t* codes, uint8_t* scales, void* stream);
+/* dh bf16 [R, 2I] = the derivative at the checkpoint's values times da bf16
+ * [R, I] (no gradient beyond a clamp bound); a bf16 [R, I], the activation
+ * of the checkpoint's values, or NULL. */
+int mxmoe_swiglu8_backward(const uint8_t* codes, const uint8_t* scales, const uint16_t* da,
+                           int64_t R, int64_t I, float alpha, float limit, uint16_t* dh,
+                           uint16_t* a, void* stream);
+/* h bf16 [R, 2I], the checkpoint's values (exact unless below bf16's
+ * subnormals), and their activation a bf16 [R, I]; either may be NULL. */
+int mxmoe_swiglu8_restore(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t I,
+                          float alpha, float limit, uint16_t* h, uint16_t* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

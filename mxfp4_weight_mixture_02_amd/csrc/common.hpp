@@ -118,6 +118,37 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float da, float al
   *du = (uc == u) ? ds * gc : 0.0f;
 }
 
+// Scale exponent of an E4M3 block whose largest finite magnitude has these
+// bits: the smallest e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), at least
+// -127.  And 2^-e, for e in [-127, 120] (an fp32 amax gives no larger e).
+__device__ __forceinline__ int e4m3_exponent(uint32_t amax_bits) {
+  const int E = (int)(amax_bits >> 23);
+  return E == 0 ? -127 : max(E - 135 + ((amax_bits & 0x7FFFFFu) > 0x600000u), -127);
+}
+__device__ __forceinline__ float e4m3_inverse(int e) {
+  return __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// A value's part in its block's largest magnitude (bits; 0 if non-finite),
+// and the value itself with every non-finite one a NaN, which the conversion
+// gives the NaN code.
+__device__ __forceinline__ bool non_finite(float v) {
+  return (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+  return non_finite(v) ? 0u : __float_as_uint(v) & 0x7FFFFFFFu;
+}
+__device__ __forceinline__ float nan_unless_finite(float v) {
+  return non_finite(v) ? __uint_as_float(0x7FC00000u) : v;
+}
+
+// Four values (at most 448 in magnitude) as E4M3 codes, nearest, ties to
+// even: gfx950's conversion instruction.
+__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
 // Global and LDS pointer types of the global -> LDS load builtin.
 typedef __attribute__((address_space(1))) const void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;

@@ -6,7 +6,9 @@
 #include <hip/hip_runtime.h>
 
 #include "abi_util.hpp"
+#include "fp8.hpp"
 #include "gate.hpp"
+#include "swiglu8.hpp"
 
 namespace {
 
@@ -73,6 +75,64 @@ mxmoe::RouteArgs route_args(const mxmoe_route_opts& o, int64_t T, int32_t E, int
   return a;
 }
 
+constexpr int64_t FP8_MAX_K = int64_t(1) << 22;
+
+// An 8-bit matrix of `rows` rows and K columns: sizes that the kernels'
+// 32-bit offsets within a tile and block counts hold.
+int check_fp8(int64_t rows, int64_t K, const char* what) {
+  if (rows < 1 || K < 1)
+    return fail(MXFP4_EINVAL, "%s: sizes must be >= 1 (%lld x %lld)", what, (long long)rows,
+                (long long)K);
+  if (rows >= (int64_t(1) << 31) || K > FP8_MAX_K)
+    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld (rows must be < 2^31, K <= 2^22)", what,
+                (long long)rows, (long long)K);
+  // one workgroup for 16 rows of a K block
+  if ((rows + 15) / 16 * ((K + 63) / 64) >= (int64_t(1) << 31))
+    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld is too large", what, (long long)rows,
+                (long long)K);
+  return MXFP4_OK;
+}
+
+int check_dtype(int dtype, const void* p, const char* what) {
+  if (dtype != MXMOE_F32 && dtype != MXMOE_BF16)
+    return fail(MXFP4_EINVAL, "%s: dtype %d unknown", what, dtype);
+  if (!aligned(p, dtype == MXMOE_F32 ? 4 : 2)) return fail(MXFP4_EINVAL, "%s is misaligned", what);
+  return MXFP4_OK;
+}
+
+int check_product(int64_t M, int64_t N, int64_t K) {
+  int rc = check_fp8(M, K, "X");
+  if (!rc) rc = check_fp8(N, K, "W");
+  if (!rc && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 31))
+    rc = fail(MXFP4_EUNSUPPORTED, "M=%lld N=%lld: too many tiles", (long long)M, (long long)N);
+  return rc;
+}
+
+// Workspace of a product: X's codes and scales, then (dw) W's.
+struct Fp8Layout {
+  size_t xs, w, ws, total;
+};
+Fp8Layout fp8_layout(int64_t M, int64_t N, int64_t K, bool w) {
+  Fp8Layout L;
+  const size_t kb = (size_t)mxmoe::fp8_pitch(K) / 128;
+  L.xs = up((size_t)M * mxmoe::fp8_pitch(K), ALIGN);
+  L.w = L.xs + up(kb * mxmoe::fp8_scale_pitch(M), ALIGN);
+  L.ws = L.w + (w ? up((size_t)N * mxmoe::fp8_pitch(K), ALIGN) : 0);
+  L.total = L.ws + (w ? up(kb * mxmoe::fp8_scale_pitch(N), ALIGN) : 0);
+  return L;
+}
+
+int check_swiglu8(int64_t R, int64_t I, float alpha, float limit) {
+  if (R < 1 || I < 1)
+    return fail(MXFP4_EINVAL, "R and I must be >= 1 (R=%lld I=%lld)", (long long)R, (long long)I);
+  if (I % 16) return fail(MXFP4_EUNSUPPORTED, "I=%lld is not a multiple of 16", (long long)I);
+  if (I >= (int64_t(1) << 32) || R >= (int64_t(1) << 40) / I)
+    return fail(MXFP4_EUNSUPPORTED, "R=%lld I=%lld is too large", (long long)R, (long long)I);
+  if (!finite(alpha) || !finite(limit) || !(limit > 0.0f))
+    return fail(MXFP4_EINVAL, "alpha must be finite and limit finite and > 0");
+  return MXFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -122,6 +182,170 @@ int mxmoe_route_backward(const mxmoe_route_opts* opts, int64_t T, int32_t E, int
   hipStream_t s = static_cast<hipStream_t>(stream);
   LAUNCH(mxmoe::launch_gate_bwd(route_args(*opts, T, E, k, logits, nullptr), topk_idx, dw, dlogits, s),
          "gate_bwd");
+  return ok();
+}
+
+int mxmoe_fp8_quantize(const void* x, int dtype, int64_t rows, int64_t K, int block_rows,
+                       uint8_t* codes, uint8_t* scales, void* stream) {
+  int rc = check_fp8(rows, K, "x");
+  if (rc) return rc;
+  if (!x || !codes || !scales) return fail(MXFP4_EINVAL, "x, codes and scales are required");
+  rc = check_dtype(dtype, x, "x");
+  if (rc) return rc;
+  if (block_rows != 1 && block_rows != 128)
+    return fail(MXFP4_EINVAL, "block_rows=%d must be 1 or 128", block_rows);
+  if (!aligned(codes, 16) || !aligned(scales, 16))
+    return fail(MXFP4_EINVAL, "codes and scales must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (block_rows == 1)
+    LAUNCH(mxmoe::launch_fp8_quantize_rows(x, dtype == MXMOE_F32, rows, K, codes, scales, s),
+           "fp8_quantize_rows");
+  else
+    LAUNCH(mxmoe::launch_fp8_quantize_blocks(x, dtype == MXMOE_F32, rows, K, codes, scales, s),
+           "fp8_quantize_blocks");
+  return ok();
+}
+
+int mxmoe_fp8_quantize_t(const void* x, int dtype, int64_t rows, int64_t K, uint8_t* codes,
+                         uint8_t* scales, void* stream) {
+  int rc = check_fp8(K, rows, "x transposed");
+  if (rc) return rc;
+  if (!x || !codes || !scales) return fail(MXFP4_EINVAL, "x, codes and scales are required");
+  rc = check_dtype(dtype, x, "x");
+  if (rc) return rc;
+  if (!aligned(codes, 16) || !aligned(scales, 16))
+    return fail(MXFP4_EINVAL, "codes and scales must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_fp8_quantize_cols(x, dtype == MXMOE_F32, rows, K, codes, scales, s),
+         "fp8_quantize_cols");
+  return ok();
+}
+
+int mxmoe_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                        uint8_t* codes_t, uint8_t* scales_t, void* stream) {
+  int rc = check_fp8(rows, K, "w");
+  if (!rc) rc = check_fp8(K, rows, "w transposed");
+  if (rc) return rc;
+  if (!codes || !scales || !codes_t || !scales_t)
+    return fail(MXFP4_EINVAL, "codes, scales, codes_t and scales_t are required");
+  if (!aligned(codes, 16) || !aligned(codes_t, 16))
+    return fail(MXFP4_EINVAL, "codes and codes_t must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_fp8_transpose(codes, scales, rows, K, codes_t, scales_t, s), "fp8_transpose");
+  return ok();
+}
+
+int mxmoe_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes,
+                     const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                     int w_block_rows, const uint16_t* bias, int out_dtype, void* out,
+                     void* stream) {
+  int rc = check_product(M, N, K);
+  if (rc) return rc;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !out)
+    return fail(MXFP4_EINVAL, "codes, scales and out are required");
+  if (w_block_rows != 1 && w_block_rows != 128)
+    return fail(MXFP4_EINVAL, "w_block_rows=%d must be 1 or 128", w_block_rows);
+  rc = check_dtype(out_dtype, out, "out");
+  if (rc) return rc;
+  if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 16) ||
+      (w_block_rows == 1 && !aligned(w_scales, 16)) || !aligned(out, 16) || !aligned(bias, 2))
+    return fail(MXFP4_EINVAL, "codes, scales of rows and out must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const mxmoe::Fp8Gemm g{M, N, K, x_codes, x_scales, w_codes, w_scales, w_block_rows == 1, bias,
+                         out, out_dtype == MXMOE_F32};
+  LAUNCH(mxmoe::launch_fp8_gemm(g, s), "fp8_matmul");
+  return ok();
+}
+
+size_t mxmoe_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int dw) {
+  if ((dw ? check_product(N, K, M) : check_product(M, N, K)) != MXFP4_OK) return 0;
+  ok();
+  return dw ? fp8_layout(N, K, M, true).total : fp8_layout(M, N, K, false).total;
+}
+
+int mxmoe_fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const uint8_t* w_codes,
+                     const uint8_t* w_scales, const uint16_t* bias, int out_dtype, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_product(M, N, K);
+  if (rc) return rc;
+  if (!x || !w_codes || !w_scales || !out)
+    return fail(MXFP4_EINVAL, "x, w_codes, w_scales and out are required");
+  rc = check_dtype(out_dtype, out, "out");
+  if (!rc) rc = check_dtype(MXMOE_BF16, x, "x");
+  if (rc) return rc;
+  if (!aligned(w_codes, 16) || !aligned(out, 16) || !aligned(bias, 2))
+    return fail(MXFP4_EINVAL, "w_codes and out must be 16-byte aligned");
+  const Fp8Layout L = fp8_layout(M, N, K, false);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const mxmoe::Fp8Gemm g{M, N, K, ws, ws + L.xs, w_codes, w_scales, 0, bias, out,
+                         out_dtype == MXMOE_F32};
+  if (mxmoe::fp8_fused_fits(M, K)) {
+    LAUNCH(mxmoe::launch_fp8_fused(g, x, s), "fp8_linear");
+    return ok();
+  }
+  LAUNCH(mxmoe::launch_fp8_quantize_rows(x, 0, M, K, ws, ws + L.xs, s), "fp8_quantize_rows");
+  LAUNCH(mxmoe::launch_fp8_gemm(g, s), "fp8_matmul");
+  return ok();
+}
+
+int mxmoe_fp8_linear_dw(int64_t M, int64_t N, int64_t K, const uint16_t* dy, const uint16_t* x,
+                        float* dw, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_product(N, K, M);
+  if (rc) return rc;
+  if (!dy || !x || !dw) return fail(MXFP4_EINVAL, "dy, x and dw are required");
+  if (!aligned(dy, 2) || !aligned(x, 2) || !aligned(dw, 16))
+    return fail(MXFP4_EINVAL, "dw must be 16-byte, dy and x 2-byte aligned");
+  const Fp8Layout L = fp8_layout(N, K, M, true);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  LAUNCH(mxmoe::launch_fp8_quantize_cols(dy, 0, M, N, ws, ws + L.xs, s), "fp8_quantize_cols");
+  LAUNCH(mxmoe::launch_fp8_quantize_cols(x, 0, M, K, ws + L.w, ws + L.ws, s), "fp8_quantize_cols");
+  const mxmoe::Fp8Gemm g{N, K, M, ws, ws + L.xs, ws + L.w, ws + L.ws, 1, nullptr, dw, 1};
+  LAUNCH(mxmoe::launch_fp8_gemm(g, s), "fp8_matmul");
+  return ok();
+}
+
+int mxmoe_swiglu8_forward(const uint16_t* h, int64_t R, int64_t I, float alpha, float limit,
+                          uint16_t* a, uint8_t* codes, uint8_t* scales, void* stream) {
+  const int rc = check_swiglu8(R, I, alpha, limit);
+  if (rc) return rc;
+  if (!h || !codes || !scales) return fail(MXFP4_EINVAL, "h, codes and scales are required");
+  if (!aligned(h, 16) || !aligned(a, 16) || !aligned(codes, 16))
+    return fail(MXFP4_EINVAL, "h, a and codes must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_swiglu8_fwd(h, R * I / 4, alpha, limit, a, codes, scales, s), "swiglu8_fwd");
+  return ok();
+}
+
+int mxmoe_swiglu8_backward(const uint8_t* codes, const uint8_t* scales, const uint16_t* da,
+                           int64_t R, int64_t I, float alpha, float limit, uint16_t* dh,
+                           uint16_t* a, void* stream) {
+  const int rc = check_swiglu8(R, I, alpha, limit);
+  if (rc) return rc;
+  if (!codes || !scales || !da || !dh)
+    return fail(MXFP4_EINVAL, "codes, scales, da and dh are required");
+  if (!aligned(codes, 16) || !aligned(da, 16) || !aligned(dh, 16) || !aligned(a, 16))
+    return fail(MXFP4_EINVAL, "codes, da, dh and a must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_swiglu8_bwd(codes, scales, da, R * I / 4, alpha, limit, dh, a, s), "swiglu8_bwd");
+  return ok();
+}
+
+int mxmoe_swiglu8_restore(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t I,
+                          float alpha, float limit, uint16_t* h, uint16_t* a, void* stream) {
+  const int rc = check_swiglu8(R, I, alpha, limit);
+  if (rc) return rc;
+  if (!codes || !scales || (!h && !a))
+    return fail(MXFP4_EINVAL, "codes, scales and one of h and a are required");
+  if (!aligned(codes, 16) || !aligned(h, 16) || !aligned(a, 16))
+    return fail(MXFP4_EINVAL, "codes, h and a must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_swiglu8_restore(codes, scales, R * I / 4, alpha, limit, h, a, s), "swiglu8_restore");
   return ok();
 }
 

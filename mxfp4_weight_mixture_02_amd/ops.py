@@ -40,8 +40,22 @@ def lib() -> ctypes.CDLL:
         L.mxmoe_route_workspace_bytes.argtypes = [i64, i32, i32]
         L.mxmoe_route.argtypes = [opts, i64, i32, i32] + [vp] * 7 + [sz, vp]
         L.mxmoe_route_backward.argtypes = [opts, i64, i32, i32] + [vp] * 5
-        for n in ("route", "route_backward"):
-            getattr(L, "mxmoe_" + n).restype = ctypes.c_int
+        ci, f32 = ctypes.c_int, ctypes.c_float
+        L.mxmoe_fp8_linear_workspace_bytes.restype = sz
+        L.mxmoe_fp8_linear_workspace_bytes.argtypes = [i64, i64, i64, ci]
+        L.mxmoe_fp8_quantize.argtypes = [vp, ci, i64, i64, ci, vp, vp, vp]
+        L.mxmoe_fp8_quantize_t.argtypes = [vp, ci, i64, i64, vp, vp, vp]
+        L.mxmoe_fp8_transpose.argtypes = [vp, vp, i64, i64, vp, vp, vp]
+        L.mxmoe_fp8_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, ci, vp, ci, vp, vp]
+        L.mxmoe_fp8_linear.argtypes = [i64, i64, i64, vp, vp, vp, vp, ci, vp, vp, sz, vp]
+        L.mxmoe_fp8_linear_dw.argtypes = [i64, i64, i64, vp, vp, vp, vp, sz, vp]
+        L.mxmoe_swiglu8_forward.argtypes = [vp, i64, i64, f32, f32, vp, vp, vp, vp]
+        L.mxmoe_swiglu8_backward.argtypes = [vp, vp, vp, i64, i64, f32, f32, vp, vp, vp]
+        L.mxmoe_swiglu8_restore.argtypes = [vp, vp, i64, i64, f32, f32, vp, vp, vp]
+        for n in ("route", "route_backward", "fp8_quantize", "fp8_quantize_t", "fp8_transpose",
+                  "fp8_matmul", "fp8_linear", "fp8_linear_dw", "swiglu8_forward",
+                  "swiglu8_backward", "swiglu8_restore"):
+            getattr(L, "mxmoe_" + n).restype = ci
         _lib = L
     return _lib
 
@@ -155,3 +169,214 @@ def moe_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, dw: torch.T
     _call("mxmoe_route_backward", dev, options.struct, T, E, k, _p(logits), _p(topk_idx), _p(dw),
           _p(out))
     return out
+
+
+# ------------------------------------------------------ 8-bit dense products
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _up(n, m):
+    return (n + m - 1) // m * m
+
+
+@dataclass
+class Fp8Matrix:
+    """A [rows, K] matrix in 8-bit floating point (E4M3) with one power-of-two
+    scale for each block of block_rows x 128 (layouts in mxmoe_ops.h)."""
+    codes: torch.Tensor      # uint8 [rows, K rounded up to 128], zeros past K
+    scales: torch.Tensor     # uint8 [K blocks, rows rounded up to 16 | row blocks of 128]
+    K: int
+    block_rows: int          # 1 or 128
+
+    @property
+    def rows(self):
+        return self.codes.shape[0]
+
+    @staticmethod
+    def empty(rows, K, block_rows, device):
+        if block_rows not in (1, 128):
+            raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+        if rows < 1 or K < 1:
+            raise ValueError(f"an 8-bit matrix has at least one element, got {rows} x {K}")
+        Kp = _up(K, 128)
+        side = _up(rows, 16) if block_rows == 1 else _up(rows, 128) // 128
+        u8 = dict(dtype=torch.uint8, device=device)
+        return Fp8Matrix(torch.empty((rows, Kp), **u8), torch.empty((Kp // 128, side), **u8), K, block_rows)
+
+    def check_shapes(self, name="matrix"):
+        if self.codes.dim() != 2 or self.block_rows not in (1, 128) or self.K < 1:
+            raise ValueError(f"{name}: codes must be [rows, K rounded up to 128], block_rows 1 or 128")
+        Kp = _up(self.K, 128)
+        side = _up(self.rows, 16) if self.block_rows == 1 else _up(self.rows, 128) // 128
+        _shape(self.codes, (self.rows, Kp), torch.uint8, name + ".codes")
+        _shape(self.scales, (Kp // 128, side), torch.uint8, name + ".scales")
+
+
+def _matrix(x, name):
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(x.shape)}")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be fp32 or bf16, got {x.dtype}")
+    return x.shape
+
+
+def fp8_quantize(x: torch.Tensor, block_rows: int = 1) -> Fp8Matrix:
+    """fp32 or bf16 x [rows, K] in blocks of block_rows x 128."""
+    rows, K = _matrix(x, "x")
+    dev = _same_device(x=x)
+    q = Fp8Matrix.empty(rows, K, block_rows, dev)
+    _call("mxmoe_fp8_quantize", dev, _p(x), _DTYPES[x.dtype], rows, K, block_rows, _p(q.codes), _p(q.scales))
+    return q
+
+
+def fp8_quantize_t(x: torch.Tensor) -> Fp8Matrix:
+    """x's transpose [K, rows] in blocks of 128 of x's rows, one column each."""
+    rows, K = _matrix(x, "x")
+    dev = _same_device(x=x)
+    q = Fp8Matrix.empty(K, rows, 1, dev)
+    _call("mxmoe_fp8_quantize_t", dev, _p(x), _DTYPES[x.dtype], rows, K, _p(q.codes), _p(q.scales))
+    return q
+
+
+def fp8_transpose(w: Fp8Matrix) -> Fp8Matrix:
+    """The transpose of a matrix with 128 x 128 blocks, exactly."""
+    w.check_shapes("w")
+    if w.block_rows != 128:
+        raise ValueError("only a matrix with block_rows 128 can be transposed exactly")
+    dev = _same_device(codes=w.codes, scales=w.scales)
+    t = Fp8Matrix.empty(w.K, w.rows, 128, dev)
+    _call("mxmoe_fp8_transpose", dev, _p(w.codes), _p(w.scales), w.rows, w.K, _p(t.codes), _p(t.scales))
+    return t
+
+
+def _out(M, N, dtype, dev):
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be fp32 or bf16, got {dtype}")
+    return torch.empty((M, N), dtype=dtype, device=dev)
+
+
+def fp8_matmul(x: Fp8Matrix, w: Fp8Matrix, bias: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """x [M, K] (block_rows 1) times w [N, K] (either block shape) transposed,
+    plus bias bf16 [N]: [M, N] in dtype."""
+    x.check_shapes("x")
+    w.check_shapes("w")
+    if x.block_rows != 1:
+        raise ValueError("x needs block_rows 1")
+    if x.K != w.K:
+        raise ValueError(f"x has K={x.K}, w K={w.K}")
+    M, N = x.rows, w.rows
+    _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
+    dev = _same_device(x=x.codes, x_scales=x.scales, w=w.codes, w_scales=w.scales, bias=bias)
+    out = _out(M, N, dtype, dev)
+    _call("mxmoe_fp8_matmul", dev, M, N, x.K, _p(x.codes), _p(x.scales), _p(w.codes), _p(w.scales),
+          w.block_rows, _p(bias), _DTYPES[dtype], _p(out))
+    return out
+
+
+def fp8_linear(x: torch.Tensor, w: Fp8Matrix, bias: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """bf16 x [M, K] rounded to E4M3 with a scale for each 128 elements of a
+    row, times w [N, K] (128 x 128 blocks) transposed, plus bias: [M, N]."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
+    w.check_shapes("w")
+    if w.block_rows != 128:
+        raise ValueError("w needs block_rows 128")
+    M, N, K = x.shape[0], w.rows, w.K
+    _shape(x, (M, K), torch.bfloat16, "x")
+    _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
+    dev = _same_device(x=x, w=w.codes, w_scales=w.scales, bias=bias)
+    nbytes = _bytes_needed("mxmoe_fp8_linear_workspace_bytes", M, N, K, 0)
+    out = _out(M, N, dtype, dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _call("mxmoe_fp8_linear", dev, M, N, K, _p(x), _p(w.codes), _p(w.scales), _p(bias), _DTYPES[dtype],
+          _p(out), _p(ws), nbytes)
+    return out
+
+
+def fp8_linear_dx(dy: torch.Tensor, w_t: Fp8Matrix, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The input's gradient of fp8_linear: bf16 dy [M, N], rounded as x is,
+    times w, given transposed (w_t = fp8_transpose(w), [K, N])."""
+    return fp8_linear(dy, w_t, dtype=dtype)
+
+
+def fp8_linear_dw(dy: torch.Tensor, x: torch.Tensor) -> torch.Tensor:
+    """The weights' gradient of a linear layer, fp32 [N, K] = dy^T x, with
+    bf16 dy [M, N] and x [M, K] rounded in blocks of 128 tokens."""
+    if dy.dim() != 2 or x.dim() != 2:
+        raise ValueError(f"dy and x must be 2-D, got {tuple(dy.shape)} and {tuple(x.shape)}")
+    (M, N), K = dy.shape, x.shape[1]
+    _shape(dy, (M, N), torch.bfloat16, "dy")
+    _shape(x, (M, K), torch.bfloat16, "x")
+    dev = _same_device(dy=dy, x=x)
+    nbytes = _bytes_needed("mxmoe_fp8_linear_workspace_bytes", M, N, K, 1)
+    dw = torch.empty((N, K), dtype=torch.float32, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _call("mxmoe_fp8_linear_dw", dev, M, N, K, _p(dy), _p(x), _p(dw), _p(ws), nbytes)
+    return dw
+
+
+# ------------------------------------------------- 8-bit activation checkpoints
+
+@dataclass
+class SwigluCheckpoint:
+    """The clamped SwiGLU's input h [R, 2I] in MXFP8, and its constants."""
+    codes: torch.Tensor      # uint8 [R, 2I]
+    scales: torch.Tensor     # uint8 [R, 2I / 32]
+    alpha: float = 1.702
+    limit: float = 7.0
+
+    def check_shapes(self):
+        if self.codes.dim() != 2 or self.codes.shape[1] % 32:
+            raise ValueError(f"codes must be [R, 2I], 2I a multiple of 32, got {tuple(self.codes.shape)}")
+        R, C = self.codes.shape
+        _shape(self.codes, (R, C), torch.uint8, "codes")
+        _shape(self.scales, (R, C // 32), torch.uint8, "scales")
+        return R, C // 2
+
+
+def _swiglu_rows(h):
+    if h.dim() != 2 or h.shape[1] % 32:
+        raise ValueError(f"h must be [R, 2I], 2I a multiple of 32, got {tuple(h.shape)}")
+    _shape(h, tuple(h.shape), torch.bfloat16, "h")
+    return h.shape[0], h.shape[1] // 2
+
+
+def swiglu_mxfp8(h: torch.Tensor, alpha: float = 1.702, limit: float = 7.0, activation: bool = True):
+    """The clamped SwiGLU of bf16 rows h [R, 2I] (gates even, ups odd) and an
+    8-bit checkpoint of h: (a bf16 [R, I], checkpoint).  With activation
+    False, (None, checkpoint)."""
+    R, I = _swiglu_rows(h)
+    dev = _same_device(h=h)
+    u8 = dict(dtype=torch.uint8, device=dev)
+    c = SwigluCheckpoint(torch.empty((R, 2 * I), **u8), torch.empty((R, I // 16), **u8), alpha, limit)
+    a = torch.empty((R, I), dtype=torch.bfloat16, device=dev) if activation else None
+    _call("mxmoe_swiglu8_forward", dev, _p(h), R, I, alpha, limit, _p(a), _p(c.codes), _p(c.scales))
+    return a, c
+
+
+def swiglu_mxfp8_backward(saved: SwigluCheckpoint, da: torch.Tensor, activation: bool = True):
+    """(dh bf16 [R, 2I], a): the derivative at the checkpoint's values times
+    da bf16 [R, I], and their activation (None with activation False)."""
+    R, I = saved.check_shapes()
+    _shape(da, (R, I), torch.bfloat16, "da")
+    dev = _same_device(codes=saved.codes, scales=saved.scales, da=da)
+    dh = torch.empty((R, 2 * I), dtype=torch.bfloat16, device=dev)
+    a = torch.empty((R, I), dtype=torch.bfloat16, device=dev) if activation else None
+    _call("mxmoe_swiglu8_backward", dev, _p(saved.codes), _p(saved.scales), _p(da), R, I, saved.alpha,
+          saved.limit, _p(dh), _p(a))
+    return dh, a
+
+
+def swiglu_mxfp8_restore(saved: SwigluCheckpoint):
+    """(h bf16 [R, 2I], a bf16 [R, I]): the checkpoint's values and their
+    activation."""
+    R, I = saved.check_shapes()
+    dev = _same_device(codes=saved.codes, scales=saved.scales)
+    h = torch.empty((R, 2 * I), dtype=torch.bfloat16, device=dev)
+    a = torch.empty((R, I), dtype=torch.bfloat16, device=dev)
+    _call("mxmoe_swiglu8_restore", dev, _p(saved.codes), _p(saved.scales), R, I, saved.alpha, saved.limit,
+          _p(h), _p(a))
+    return h, a
