@@ -73,6 +73,34 @@ int mxmoe_route_backward(const mxmoe_route_opts* opts, int64_t T, int32_t E, int
                          const float* logits, const int32_t* topk_idx, const float* dw,
                          float* dlogits, void* stream);
 
+/* Router logits as the expert block forms them: fp32 [T, E] = x W_r^T + b_r
+ * with x bf16 [T, H], router_w fp32 [E, H], router_b fp32 [E] or NULL,
+ * products summed in fp64 and rounded once.  H % 32 == 0, H <= 5120, E <=
+ * 256, T * H < 2^31; x and router_w 16-byte aligned. */
+int mxmoe_router_logits(int64_t T, int64_t H, int32_t E, const uint16_t* x, const float* router_w,
+                        const float* router_b, float* logits, void* stream);
+
+/* The expert block (mxfp4_moe_forward) on a given routing: `saved` names
+ * its topk_idx, topk_w, expert_offsets and sorted_rows as mxmoe_route fills
+ * them (inputs, read as they are: offsets must end at T * k, sorted_rows
+ * must be a permutation grouped by expert); h, a (and lora_v, lora_vg with
+ * the adapters) are outputs, or all NULL for inference.  router_w may be
+ * NULL.  workspace: mxfp4_moe_workspace_bytes of MXFP4_WS_FORWARD_SAVED or
+ * (without h) MXFP4_WS_FORWARD. */
+int mxmoe_forward_routed(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w, const uint16_t* x,
+                         uint16_t* out, const mxfp4_moe_saved* saved, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Its backward: everything mxfp4_moe_backward computes for the gradients
+ * that grads names, except that dX holds no router term; dw fp32 [T, k] is
+ * the gradient of topk_w instead (the input of mxmoe_route_backward).
+ * router_w may be NULL.  workspace: MXFP4_WS_BACKWARD, or
+ * MXFP4_WS_BACKWARD_FULL if grads names dW_gu, dW_dn, db_gu or db_dn. */
+int mxmoe_backward_routed(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w,
+                          const mxfp4_moe_saved* saved, const uint16_t* x, const uint16_t* dy,
+                          const mxfp4_moe_grads* grads, float* dw, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------- 8-bit dense products */
 
 /* An 8-bit matrix of `rows` rows and K columns:

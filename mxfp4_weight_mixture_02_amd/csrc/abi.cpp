@@ -4,6 +4,7 @@
 // invalid call leaves the stream untouched ("Integrate finegrained kernels
 // ...": guards refuse before the kernel is reached rather than fall back).
 #include "mxfp4_moe.h"
+#include "mxmoe_ops.h"
 
 #include <hip/hip_runtime.h>
 
@@ -175,7 +176,8 @@ T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-int check_weights(const mxfp4_moe_weights* w, const mxfp4_moe_dims& d) {
+// routed: the routing comes from outside, so router_w may be NULL.
+int check_weights(const mxfp4_moe_weights* w, const mxfp4_moe_dims& d, bool routed = false) {
   if (!w) return fail(MXFP4_EINVAL, "weights is NULL");
   if (lora_dn(d)) {
     if (!w->lora_A || !w->lora_B)
@@ -196,7 +198,7 @@ int check_weights(const mxfp4_moe_weights* w, const mxfp4_moe_dims& d) {
   } else if (w->lora_gu_A || w->lora_gu_B) {
     return fail(MXFP4_EINVAL, "lora_gu_A/lora_gu_B given but gate_up is not a lora target");
   }
-  if (!w->router_w || !w->gu_codes || !w->gu_scales || !w->dn_codes || !w->dn_scales)
+  if ((!w->router_w && !routed) || !w->gu_codes || !w->gu_scales || !w->dn_codes || !w->dn_scales)
     return fail(MXFP4_EINVAL, "router_w, gu_codes, gu_scales, dn_codes and dn_scales are required");
   if (!aligned(w->router_w, 16) || !aligned(w->gu_codes, 16) || !aligned(w->dn_codes, 16) ||
       !aligned(w->gu_scales, 16) || !aligned(w->dn_scales, 16))
@@ -286,14 +288,18 @@ namespace {
 // Validation shared by the two forward entry points (everything but the
 // scratch memory).
 int check_forward(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w, const uint16_t* x,
-                  const uint16_t* out, const mxfp4_moe_saved* saved) {
+                  const uint16_t* out, const mxfp4_moe_saved* saved, bool routed = false) {
   int rc = check_dims(dims);
   if (rc) return rc;
-  rc = check_weights(w, *dims);
+  rc = check_weights(w, *dims, routed);
   if (rc) return rc;
   const mxfp4_moe_dims& d = *dims;
   if (!x || !out) return fail(MXFP4_EINVAL, "x and out are required");
   if (!aligned(x, 16) || !aligned(out, 16)) return fail(MXFP4_EINVAL, "x and out must be 16-byte aligned");
+  if (routed && (!saved || !saved->topk_idx || !saved->topk_w || !saved->expert_offsets ||
+                 !saved->sorted_rows))
+    return fail(MXFP4_EINVAL, "the routing (topk_idx, topk_w, expert_offsets, sorted_rows) is required");
+  if (routed && !saved->h && !saved->a && !saved->lora_v && !saved->lora_vg) return MXFP4_OK;
   if (saved) {
     if (!saved->topk_idx || !saved->topk_w || !saved->expert_offsets || !saved->sorted_rows ||
         !saved->h || !saved->a)
@@ -309,10 +315,11 @@ int check_forward(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w, const 
 }
 
 // The forward's launches on stream s, with the workspace laid out by
-// layout(d, mode) at `workspace` (validated by the caller).
+// layout(d, mode) at `workspace` (validated by the caller).  routing: the
+// routing to run on, as its first four buffers (nullptr: from the logits).
 int enqueue_forward(const mxfp4_moe_dims& d, const mxfp4_moe_weights* w, const uint16_t* x,
                     uint16_t* out, const mxfp4_moe_saved* saved, void* workspace,
-                    hipStream_t s) {
+                    hipStream_t s, const mxfp4_moe_saved* routing = nullptr) {
   const int mode = saved ? MXFP4_WS_FORWARD_SAVED : MXFP4_WS_FORWARD;
   const Layout L = layout(d, mode);
   const int T = (int)d.T, H = (int)d.H, I = (int)d.I, E = d.E, k = d.k;
@@ -323,6 +330,11 @@ int enqueue_forward(const mxfp4_moe_dims& d, const mxfp4_moe_weights* w, const u
   int32_t* sorted_rows = saved ? saved->sorted_rows : at<int32_t>(workspace, L.sorted_rows);
   uint16_t* a = saved ? saved->a : at<uint16_t>(workspace, L.a);
   uint16_t* h = saved ? saved->h : nullptr;
+  if (routing) {
+    topk_w = routing->topk_w;
+    offsets = routing->expert_offsets;
+    sorted_rows = routing->sorted_rows;
+  }
   int32_t* blk_hist = at<int32_t>(workspace, L.blk_hist);
   mxmoe::Tile* tiles = at<mxmoe::Tile>(workspace, L.tiles);
   int32_t* num_tiles = at<int32_t>(workspace, L.num_tiles);
@@ -333,7 +345,11 @@ int enqueue_forward(const mxfp4_moe_dims& d, const mxfp4_moe_weights* w, const u
   const int maxt = mxmoe::max_tiles(R, E, mxmoe::MT);
 
   float* logits = at<float>(workspace, L.logits);
-  if (mxmoe::plan_fits(d.T, E, k)) {
+  if (routing) {
+    LAUNCH(mxmoe::launch_build_tiles(offsets, E, mxmoe::MT, nullptr, nullptr, mxmoe::MT, tiles,
+                                     num_tiles, s),
+           "fwd_tiles");
+  } else if (mxmoe::plan_fits(d.T, E, k)) {
     // partial logits over many CUs, then one workgroup for the logits,
     // top-k, offsets, permutation and tiles
     double* part = at<double>(workspace, L.logit_part);
@@ -516,15 +532,17 @@ namespace {
 
 // The backward of both entry points: dX and the adapter gradients, and with
 // mode MXFP4_WS_BACKWARD_FULL the base-weight and bias gradients g names.
+// With dw_out the routing came from outside: its weights' gradients go
+// there, and dX gets no router term.
 int backward_impl(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w,
                   const mxfp4_moe_saved* saved, const uint16_t* x, const uint16_t* dy,
                   const mxfp4_moe_grads& g, int mode, void* workspace, size_t workspace_bytes,
-                  void* stream) {
+                  void* stream, float* dw_out = nullptr) {
   uint16_t* dx = g.dx;
   float *dA = g.dA, *dB = g.dB, *dA_gu = g.dA_gu, *dB_gu = g.dB_gu;
   int rc = check_dims(dims);
   if (rc) return rc;
-  rc = check_weights(w, *dims);
+  rc = check_weights(w, *dims, dw_out != nullptr);
   if (rc) return rc;
   const mxfp4_moe_dims& d = *dims;
   if (!saved || !saved->topk_idx || !saved->topk_w || !saved->expert_offsets ||
@@ -626,7 +644,8 @@ int backward_impl(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w,
                                    num_tiles, maxt, H, I, lora_guAt, lora_dvg, r, dxr, s),
          "bwd_gate_up");
   LAUNCH(mxmoe::launch_bwd_combine(dy, dxr, dw_part, mxmoe::bwd_down_ntiles(I), saved->topk_idx,
-                                   saved->topk_w, w->dn_bias, w->router_w, d.T, H, k, dx, s),
+                                   saved->topk_w, w->dn_bias, w->router_w, d.T, H, k, dx, dw_out,
+                                   s),
          "bwd_combine");
   if (full) {
     // base-weight and bias gradients (dh still in the workspace):
@@ -680,6 +699,47 @@ int mxfp4_moe_backward(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w,
   if (!grads) return fail(MXFP4_EINVAL, "grads is NULL");
   return backward_impl(dims, w, saved, x, dy, *grads, MXFP4_WS_BACKWARD_FULL, workspace,
                        workspace_bytes, stream);
+}
+
+int mxmoe_forward_routed(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w, const uint16_t* x,
+                         uint16_t* out, const mxfp4_moe_saved* saved, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  int rc = check_forward(dims, w, x, out, saved, true);
+  if (rc) return rc;
+  const mxfp4_moe_saved* state = saved->h ? saved : nullptr;
+  const Layout L = layout(*dims, state ? MXFP4_WS_FORWARD_SAVED : MXFP4_WS_FORWARD);
+  if (!workspace || workspace_bytes < L.total)
+    return fail(MXFP4_EWORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, L.total);
+  if (!aligned(workspace, ALIGN)) return fail(MXFP4_EINVAL, "workspace must be 256-byte aligned");
+  return enqueue_forward(*dims, w, x, out, state, workspace, static_cast<hipStream_t>(stream), saved);
+}
+
+int mxmoe_backward_routed(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w,
+                          const mxfp4_moe_saved* saved, const uint16_t* x, const uint16_t* dy,
+                          const mxfp4_moe_grads* grads, float* dw, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (!grads || !dw) return fail(MXFP4_EINVAL, "grads and dw are required");
+  if (!aligned(dw, 4)) return fail(MXFP4_EINVAL, "dw must be 4-byte aligned");
+  const bool base = grads->dW_gu || grads->dW_dn || grads->db_gu || grads->db_dn;
+  return backward_impl(dims, w, saved, x, dy, *grads,
+                       base ? MXFP4_WS_BACKWARD_FULL : MXFP4_WS_BACKWARD, workspace,
+                       workspace_bytes, stream, dw);
+}
+
+int mxmoe_router_logits(int64_t T, int64_t H, int32_t E, const uint16_t* x, const float* router_w,
+                        const float* router_b, float* logits, void* stream) {
+  if (T < 1 || H < 1 || E < 1) return fail(MXFP4_EINVAL, "T, H and E must be >= 1");
+  if (H % 32 || H > 5120 || E > 256)
+    return fail(MXFP4_EUNSUPPORTED, "H must be a multiple of 32 up to 5120, E <= 256 (H=%lld E=%d)",
+                (long long)H, E);
+  if (T >= (int64_t(1) << 31) / H)
+    return fail(MXFP4_EUNSUPPORTED, "T*H elements exceed int32 (T=%lld H=%lld)", (long long)T, (long long)H);
+  if (!x || !router_w || !logits) return fail(MXFP4_EINVAL, "x, router_w and logits are required");
+  if (!aligned(x, 16) || !aligned(router_w, 16) || !aligned(router_b, 4) || !aligned(logits, 4))
+    return fail(MXFP4_EINVAL, "x and router_w must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_logits(x, router_w, router_b, (int)T, (int)H, E, logits, s), "router_logits");
+  return ok();
 }
 
 int mxfp4_quantize(const float* w, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,

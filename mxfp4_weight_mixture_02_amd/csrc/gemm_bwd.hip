@@ -755,13 +755,16 @@ __global__ __launch_bounds__(GTHR) __attribute__((amdgpu_waves_per_eu(2, 2))) vo
 // reduction); then dX[t] = sum_j dxr[(t,j)] + dl_j Wr[e_j].  The bias dot
 // reads dY and the slots' bias rows in 16-byte pieces, one batch of k + 1
 // loads per piece (2-byte loads in a "load, use" loop paid a memory round
-// trip per element group), and the dw partials go through LDS.
-template <int K>
+// trip per element group), and the dw partials go through LDS.  ROUTED (the
+// routing came from outside): dw goes to dw_out [T, K] and the router term
+// is left to the caller.
+template <int K, bool ROUTED>
 __global__ __launch_bounds__(256) void bwd_combine_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ dxr,
     const float* __restrict__ dw_part, int n_dw_part, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ topk_w, const uint16_t* __restrict__ dn_bias,
-    const float* __restrict__ router_w, int H, uint16_t* __restrict__ dx) {
+    const float* __restrict__ router_w, int H, uint16_t* __restrict__ dx,
+    float* __restrict__ dw_out) {
   __shared__ float red[4][K];
   __shared__ float dl[K];
   __shared__ int32_t ex[K];
@@ -814,7 +817,10 @@ __global__ __launch_bounds__(256) void bwd_combine_kernel(
       w[j] = topk_w[t * K + j];
       sw += w[j] * s;
     }
-    for (int j = 0; j < K; ++j) dl[j] = w[j] * (dw[j] - sw);
+    for (int j = 0; j < K; ++j) {
+      dl[j] = w[j] * (dw[j] - sw);
+      if (ROUTED) dw_out[t * K + j] = dw[j];
+    }
   }
   __syncthreads();
   // dX piece c (8 columns) from the slots' dxr pieces v, in slot order
@@ -822,6 +828,10 @@ __global__ __launch_bounds__(256) void bwd_combine_kernel(
     f32x4 r[K][2];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
+      if (ROUTED) {
+        r[j][0] = r[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        continue;
+      }
       const f32x4* rw = reinterpret_cast<const f32x4*>(router_w + (int64_t)ex[j] * H) + 2 * c;
       r[j][0] = rw[0];
       r[j][1] = rw[1];
@@ -829,7 +839,7 @@ __global__ __launch_bounds__(256) void bwd_combine_kernel(
     float s[8] = {};
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      const float d = dl[j];
+      const float d = ROUTED ? 0.0f : dl[j];
 #pragma unroll
       for (int m = 0; m < 8; ++m)
         s[m] += bf16_to_f32((uint16_t)(v[j][m >> 1] >> (16 * (m & 1)))) + d * r[j][m >> 2][m & 3];
@@ -887,12 +897,18 @@ hipError_t launch_bwd_gate_up(const uint16_t* dh, const uint8_t* codes, const ui
 hipError_t launch_bwd_combine(const uint16_t* dy, const uint16_t* dxr, const float* dw_part,
                               int n_dw_part, const int32_t* topk_idx, const float* topk_w,
                               const uint16_t* dn_bias, const float* router_w, int64_t T, int H,
-                              int k, uint16_t* dx, hipStream_t s) {
+                              int k, uint16_t* dx, float* dw_out, hipStream_t s) {
   if (n_dw_part > 20 || H % 8) return hipErrorInvalidValue;
 #define BWD_COMBINE(KK)                                                                        \
   case KK:                                                                                     \
-    hipLaunchKernelGGL(bwd_combine_kernel<KK>, dim3((unsigned)T), dim3(256), 0, s, dy, dxr,    \
-                       dw_part, n_dw_part, topk_idx, topk_w, dn_bias, router_w, H, dx);        \
+    if (dw_out)                                                                                \
+      hipLaunchKernelGGL((bwd_combine_kernel<KK, true>), dim3((unsigned)T), dim3(256), 0, s, dy, \
+                         dxr, dw_part, n_dw_part, topk_idx, topk_w, dn_bias, router_w, H, dx,  \
+                         dw_out);                                                              \
+    else                                                                                       \
+      hipLaunchKernelGGL((bwd_combine_kernel<KK, false>), dim3((unsigned)T), dim3(256), 0, s, dy, \
+                         dxr, dw_part, n_dw_part, topk_idx, topk_w, dn_bias, router_w, H, dx,  \
+                         dw_out);                                                              \
     break;
   switch (k) {
     BWD_COMBINE(1) BWD_COMBINE(2) BWD_COMBINE(3) BWD_COMBINE(4)

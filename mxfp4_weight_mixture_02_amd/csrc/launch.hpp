@@ -45,7 +45,8 @@ hipError_t launch_scatter(const int32_t* topk_idx, const int32_t* blk_base, int 
                           int32_t* sorted_rows, hipStream_t s);
 int max_tiles(int64_t R, int E, int mt);
 // tile lists from the offsets: at most mt rows per tile, dealt to the XCDs
-// (the backward GEMMs' order), and with tiles2 at most mt2 rows in expert order
+// (the backward GEMMs' order), and with tiles2 at most mt2 rows in expert
+// order; without tiles the second list alone
 hipError_t launch_build_tiles(const int32_t* offsets, int E, int mt, Tile* tiles,
                               int32_t* num_tiles, int mt2, Tile* tiles2, int32_t* num_tiles2,
                               hipStream_t s);
@@ -111,7 +112,9 @@ hipError_t launch_bwd_gate_up(const uint16_t* dh, const uint8_t* codes, const ui
 hipError_t launch_bwd_combine(const uint16_t* dy, const uint16_t* dxr, const float* dw_part,
                               int n_dw_part, const int32_t* topk_idx, const float* topk_w,
                               const uint16_t* dn_bias, const float* router_w, int64_t T, int H,
-                              int k, uint16_t* dx, hipStream_t s);
+                              int k, uint16_t* dx, float* dw_out, hipStream_t s);
+// (with dw_out [T, k]: the routing weights' gradients go there, and dx gets
+// no router term)
 
 // lora.hip
 // out [R, r] fp32 = scale * src rows . M_e rows (M: [E, r, C] bf16)

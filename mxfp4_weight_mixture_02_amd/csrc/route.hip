@@ -819,7 +819,7 @@ __global__ __launch_bounds__(256) void tiles_kernel(const int32_t* __restrict__ 
   // memory would pay a round trip per expert)
   for (int e = tid; e <= E; e += 256) offs[e] = offsets[e];
   __syncthreads();
-  write_dealt_tiles(offs, E, mt, start, tiles, num_tiles);
+  if (tiles) write_dealt_tiles(offs, E, mt, start, tiles, num_tiles);
   if (tiles2) write_tiles(offs, E, mt2, start, tiles2, num_tiles2);
 }
 

@@ -172,7 +172,7 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.floa
 @dataclass
 class MoeLayer:
     """Device tensors of one layer (layouts as in include/mxfp4_moe.h)."""
-    router_w: torch.Tensor            # fp32 [E, H]
+    router_w: torch.Tensor | None     # fp32 [E, H] (None: routed calls only)
     router_b: torch.Tensor | None     # fp32 [E]
     gu_codes: torch.Tensor            # uint8 [E, 2I, H/2]
     gu_scales: torch.Tensor           # uint8 [E, 2I, H/32]
@@ -219,13 +219,14 @@ class MoeLayer:
         return Dims(T, self.H, self.I, self.E, self.k, self.alpha, self.limit, self.lora_rank,
                     self.lora_scale, self.lora_targets, ACT_FORMATS[self.act_format])
 
-    def check_shapes(self):
-        """Every parameter's shape and dtype against E, H, I (and the rank)."""
+    def check_shapes(self, routed=False):
+        """Every parameter's shape and dtype against E, H, I (and the rank);
+        with ``routed`` the router's weights may be absent."""
         if self.gu_codes.dim() != 3 or min(self.gu_codes.shape) < 1:
             raise ValueError(f"gu_codes must be [E, 2I, H/2], got {tuple(self.gu_codes.shape)}")
         E, H, I = self.E, self.H, self.I
         u8, bf = torch.uint8, torch.bfloat16
-        _shape(self.router_w, (E, H), torch.float32, "router_w")
+        _shape(self.router_w, (E, H), torch.float32, "router_w", optional=routed)
         _shape(self.router_b, (E,), torch.float32, "router_b", optional=True)
         _shape(self.gu_codes, (E, 2 * I, H // 2), u8, "gu_codes")
         _shape(self.gu_scales, (E, 2 * I, H // 32), u8, "gu_scales")
@@ -250,8 +251,8 @@ class MoeLayer:
             _shape(self.lora_gu_A, (E, r, H), bf, "lora_gu_A")
             _shape(self.lora_gu_B, (E, 2 * I, r), bf, "lora_gu_B")
 
-    def weights(self):
-        self.check_shapes()
+    def weights(self, routed=False):
+        self.check_shapes(routed)
         _dev(self.router_w, torch.float32, "router_w")
         _dev(self.router_b, torch.float32, "router_b")
         for n in ("gu_codes", "gu_scales", "dn_codes", "dn_scales"):
@@ -307,6 +308,10 @@ class SavedState:
         _shape(self.lora_vg, (R, r), torch.float32, "saved.lora_vg",
                optional=(layer.lora_gu_A is None))
 
+    def restore(self):
+        """This state itself (SavedState8 makes its bf16 activations here)."""
+        return self
+
     def struct(self):
         for n, _ in Saved._fields_:
             t = getattr(self, n)
@@ -345,10 +350,16 @@ def workspace_bytes(layer: MoeLayer, T: int, mode: int) -> int:
     return n
 
 
-def mxfp4_moe_forward(layer: MoeLayer, x: torch.Tensor, saved: SavedState | bool | None = None,
+def mxfp4_moe_forward(layer: MoeLayer, x: torch.Tensor, saved: SavedState | bool | str | None = None,
                       out: torch.Tensor | None = None, workspace: Workspace | None = None):
     """Expert-block forward.  ``saved=True`` allocates and fills the state
-    the backward needs.  Returns (out, saved)."""
+    the backward needs; ``saved="mxfp8"`` returns it with 8-bit activations
+    (SavedState8, a third of the bytes).  Returns (out, saved)."""
+    if isinstance(saved, str):
+        from .ops import SavedState8
+        SavedState8.check_format(saved)
+        out, state = mxfp4_moe_forward(layer, x, True, out, workspace)
+        return out, SavedState8.pack(layer, state)
     layer.check_shapes()
     if x.dim() != 2:
         raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
@@ -408,7 +419,8 @@ def mxfp4_moe_backward_dx(layer: MoeLayer, saved: SavedState, dy: torch.Tensor,
                           x: torch.Tensor | None = None, dA_gu: torch.Tensor | None = None,
                           dB_gu: torch.Tensor | None = None):
     """dX (and the adapter gradients, overwritten) for the loss sum(dy * out).
-    ``x`` (the forward's input) is needed only with the gate_up adapter.
+    ``x`` (the forward's input) is needed only with the gate_up adapter.  A
+    SavedState8 is restored first.
     Returns (dx, dA, dB), plus (dA_gu, dB_gu) when the layer has a gate_up
     adapter."""
     layer.check_shapes()
@@ -419,6 +431,7 @@ def mxfp4_moe_backward_dx(layer: MoeLayer, saved: SavedState, dy: torch.Tensor,
     if dx is not None:
         _shape(dx, (T, layer.H), torch.bfloat16, "dx")
     saved.check_shapes(layer, T)
+    saved = saved.restore()
     grads = {}
     for name, base, on in (("dA", layer.lora_A, True), ("dB", layer.lora_B, True),
                            ("dA_gu", layer.lora_gu_A, True), ("dB_gu", layer.lora_gu_B, True)):
@@ -475,6 +488,7 @@ def mxfp4_moe_backward(layer: MoeLayer, saved: SavedState, x: torch.Tensor, dy: 
     _shape(dy, (T, layer.H), torch.bfloat16, "dy")
     _shape(x, (T, layer.H), torch.bfloat16, "x")
     saved.check_shapes(layer, T)
+    saved = saved.restore()
     _dev(dy, torch.bfloat16, "dy")
     _dev(x, torch.bfloat16, "x")
     E, H, I = layer.E, layer.H, layer.I
