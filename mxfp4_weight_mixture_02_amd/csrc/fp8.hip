@@ -311,53 +311,96 @@ __device__ __forceinline__ void fp8_store(const Fp8Gemm& g, int64_t m, int64_t n
 
 constexpr int FP8_RSRC_W3 = 0x00020000;   // raw buffer, untyped
 
-template <int WN_, int WM_, int FN_, int FM_>
+// A workgroup's tile: WN x WM waves of (16 FN) x (16 FM), and NST LDS stages.
+// A stage holds one K block: BN rows of W and BM rows of X (128 bytes each),
+// X's BM scale bytes (room for 256) and W's scales (256 bytes).
+template <int WN_, int WM_, int FN_, int FM_, int NST_>
 struct Fp8Tile {
-  static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_;
+  static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, NST = NST_;
   static constexpr int NW = WN * WM;          // waves
   static constexpr int BN = WN * FN * 16, BM = WM * FM * 16;
-  static constexpr int STAGE = (BN + BM) * 128;
+  static constexpr int SX = (BN + BM) * 128, SW = SX + 256, STAGE = SW + 256;
   static constexpr int LOADS = (BN + BM) / 8 / NW;   // 1 KB copies per wave and step
-  static_assert(LOADS <= 8 && LOADS * NW * 8 == BN + BM, "Fp8Wave::off");
+  static_assert(LOADS <= 8 && LOADS * NW * 8 == BN + BM && NW % 2 == 0, "copies");
+  static_assert(BN <= 256 && BM <= 256 && NST >= 2 && NST * STAGE <= 160 * 1024, "LDS");
+  static_assert((NST - 1) * (LOADS + 1) < 64, "vector-memory counter");
+  static constexpr bool SPREAD = 2 * NST * STAGE > 160 * 1024;   // one workgroup on a CU
+  // scale bytes of X are read four at a time, or with F_M % 4 one by one
+  static constexpr int XW = FM % 4 ? FM : FM / 4;
 };
+
+// Copy from global memory to LDS: 16, 4 or 1 bytes a lane from base + off +
+// soff to LDS address lds + (16, 4, 4) * lane.  As assembly, because the
+// compiler makes every later LDS read wait for every such copy in flight
+// that it cannot prove to go elsewhere, and with a ring of stages it can
+// prove nothing.  The kernel waits itself (fp8_wait) before it reads a
+// stage.  A copy has no output register; its address is read at issue.
+template <int BYTES>
+__device__ __forceinline__ void lds_copy(u32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
+  if (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory");
+  else if (BYTES == 4)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory");
+}
+// Raw buffer of `bytes` bytes at p (a wave-uniform pointer).
+__device__ __forceinline__ u32x4 buffer_of(const uint8_t* p, int64_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)FP8_RSRC_W3};
+}
 
 // A wave's part of a tile's main loop.
 struct Fp8Wave {
-  __amdgpu_buffer_rsrc_t rw, rx;
+  u32x4 rw, rx, rs;            // W's and X's rows of the tile, and this wave's scales
   uint32_t off[8];             // this lane's 16 bytes of each copy, at K block 0
-  const uint8_t *sx, *sw;      // this lane's scale bytes, at K block 0
-  int64_t sxp, swp;            // and their step from K block to K block
+  uint32_t soff, sstep;        // its scale copy, and the step to the next K block
+  uint32_t lds;                // LDS address of the stages
   int wave, woff, xoff, s0;    // fragment addresses in a stage: row, first chunk
+  int sxoff, swoff;            // scale addresses in a stage
 };
 
-// Copies of K block kb into a stage: this wave's 1 KB pieces; piece p is
-// rows 8 p .. 8 p + 7 of the W tile, then of the X tile.
-template <class T>
-__device__ __forceinline__ void fp8_copy(const Fp8Wave& g, uint8_t* __restrict__ st, int kb) {
-#pragma unroll
-  for (int i = 0; i < T::LOADS; ++i) {
-    const int p = g.wave * T::LOADS + i;
-    if (p < T::BN / 8)   // uniform
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(g.rw, (lptr_t)(st + p * 1024), 16, g.off[i], kb * 128, 0, 0);
-    else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(g.rx, (lptr_t)(st + p * 1024), 16, g.off[i], kb * 128, 0, 0);
+// Copies of K block kb into the stage at LDS offset st: this wave's 1 KB
+// pieces (piece p is rows 8 p .. 8 p + 7 of the W tile, then of the X tile)
+// and the scales of X (even waves) or W (odd waves; all of them write the
+// same bytes, so that every wave has as many copies in flight).
+template <class T, bool WROWS>
+__device__ __forceinline__ void fp8_copy_piece(const Fp8Wave& g, uint32_t st, int kb, int i) {
+  if (i < T::LOADS) {
+    const int p = g.wave * T::LOADS + i;   // uniform
+    lds_copy<16>(p < T::BN / 8 ? g.rw : g.rx, g.lds + st + p * 1024, g.off[i], kb * 128);
+  } else if ((g.wave & 1) == 0) {
+    lds_copy<4>(g.rs, g.lds + st + T::SX, g.soff, kb * g.sstep);
+  } else if (WROWS) {
+    lds_copy<4>(g.rs, g.lds + st + T::SW, g.soff, kb * g.sstep);
+  } else {
+    lds_copy<1>(g.rs, g.lds + st + T::SW, g.soff, kb * g.sstep);
   }
 }
-
-struct Fp8Scales {
-  uint32_t x[2], w[2];
-};
-
 template <class T, bool WROWS>
-__device__ __forceinline__ void fp8_scales(const Fp8Wave& g, int kb, Fp8Scales& s) {
+__device__ __forceinline__ void fp8_copy(const Fp8Wave& g, uint32_t st, int kb) {
 #pragma unroll
-  for (int i = 0; i < T::FM / 4; ++i) s.x[i] = *reinterpret_cast<const uint32_t*>(g.sx + kb * g.sxp + 4 * i);
-  if (WROWS) {
-#pragma unroll
-    for (int i = 0; i < T::FN / 4; ++i) s.w[i] = *reinterpret_cast<const uint32_t*>(g.sw + kb * g.swp + 4 * i);
-  } else {
-    s.w[0] = g.sw[kb * g.swp];
-  }
+  for (int i = 0; i <= T::LOADS; ++i) fp8_copy_piece<T, WROWS>(g, st, kb, i);
+}
+
+// Wait until at most `blocks` K blocks' copies of this wave are under way,
+// and for all its LDS reads.
+template <class T>
+__device__ __forceinline__ void fp8_wait(int blocks) {
+  // a constant for every count that a ring of up to 4 stages has
+  if (blocks <= 0)
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+  else if (blocks == 1 || T::NST <= 2)
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(T::LOADS + 1, 0));
+  else if (blocks == 2 || T::NST <= 3)
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * (T::LOADS + 1), 0));
+  else
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * (T::LOADS + 1), 0));
 }
 
 __device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p, int s0) {
@@ -366,60 +409,106 @@ __device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p, int s0) {
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// One K block: wait for this wave's copies of it, meet the other waves
-// (which also ends their reads of the other stage), start the next block's
-// copies there, multiply.  cur and nxt do not overlap: the compiler need
-// not wait for the copies before it reads cur.
+// A K block's scales of this lane's rows: words of four bytes, or bytes.
+template <class T>
+struct Fp8Scales {
+  uint32_t x[T::XW], w[T::FN / 4];
+};
+template <class T, bool WROWS>
+__device__ __forceinline__ Fp8Scales<T> fp8_scales(const Fp8Wave& g, const uint8_t* st) {
+  Fp8Scales<T> s;
+#pragma unroll
+  for (int i = 0; i < T::XW; ++i)
+    s.x[i] = T::FM % 4 ? st[g.sxoff + i] : *reinterpret_cast<const uint32_t*>(st + g.sxoff + 4 * i);
+#pragma unroll
+  for (int i = 0; i < (WROWS ? T::FN / 4 : 1); ++i)
+    s.w[i] = *reinterpret_cast<const uint32_t*>(st + g.swoff + 4 * i);
+  return s;
+}
+
+// The K loop: wait for the block's copies, meet the others (which ends their
+// reads of the previous block's stage), start the copies of block kb + NST -
+// 1 there, multiply.  bf16 results on the scaled matrix core, fp32 results
+// as bf16 products (twice the matrix time).
 template <class T, bool WROWS, bool F32>
-__device__ __forceinline__ void fp8_step(const Fp8Wave& g, const uint8_t* __restrict__ cur,
-                                         uint8_t* __restrict__ nxt, int kb, int kblocks,
-                                         Fp8Scales& sc, f32x4 (&acc)[T::FN][T::FM]) {
-  constexpr int FN = T::FN, FM = T::FM;
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-  barrier_only();
-  const Fp8Scales c = sc;
-  if (kb + 1 < kblocks) {
-    fp8_copy<T>(g, nxt, kb + 1);
-    fp8_scales<T, WROWS>(g, kb + 1, sc);
-  }
-  if (F32) {
-    bf16x8 b[FM][4];
+__device__ __forceinline__ void fp8_loop(const Fp8Wave& g, int kblocks, const uint8_t* lds,
+                                         f32x4 (&acc)[T::FN][T::FM]) {
+  constexpr int FN = T::FN, FM = T::FM, LAST = T::NST * T::STAGE;
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
-      fp8_to_bf16(fp8_frag(cur + g.xoff + j * 128, g.s0), byte_of(c.x[j >> 2], j & 3), b[j]);
+  for (int k = 0; k < T::NST - 1; ++k)
+    if (k < kblocks) fp8_copy<T, WROWS>(g, k * T::STAGE, k);
+  int st = 0;
+  for (int kb = 0; kb < kblocks; ++kb) {
+    fp8_wait<T>(min(T::NST - 1, kblocks - kb) - 1);
+    barrier_only();
+    const uint32_t prev = st == 0 ? LAST - T::STAGE : st - T::STAGE;
+    const bool more = kb + T::NST - 1 < kblocks;
+    // A copy instruction holds its wave until the CU's memory pipe takes it
+    // (17 cycles each).  With one workgroup on a CU they are spread over the
+    // rows of products (256 x 256 tiles -3%); with two, which fill each
+    // other's gaps, they go first (128 x 128 tiles: spread +7%).
+    constexpr int PER = T::SPREAD ? (T::LOADS + FN) / FN : T::LOADS + 1;
+    auto copies = [&](int i) {
+      if (more) {
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      bf16x8 a[4];
-      fp8_to_bf16(fp8_frag(cur + g.woff + i * 128, g.s0), WROWS ? byte_of(c.w[i >> 2], i & 3) : c.w[0], a);
+        for (int c = i * PER; c < (i + 1) * PER && c <= T::LOADS; ++c)
+          fp8_copy_piece<T, WROWS>(g, prev, kb + T::NST - 1, c);
+      }
+    };
+    const uint8_t* cur = lds + st;
+    if (!T::SPREAD) copies(0);
+    const Fp8Scales<T> c = fp8_scales<T, WROWS>(g, cur);
+    if (F32) {
+      bf16x8 b[FM][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int j = 0; j < FM; ++j)
+        fp8_to_bf16(fp8_frag(cur + g.xoff + j * 2048, g.s0), byte_of(c.x[FM % 4 ? j : j >> 2], FM % 4 ? 0 : j & 3), b[j]);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        bf16x8 a[4];
+        fp8_to_bf16(fp8_frag(cur + g.woff + i * 2048, g.s0),
+                    byte_of(c.w[WROWS ? i >> 2 : 0], WROWS ? i & 3 : 0), a);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int j = 0; j < FM; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s], b[j][s], acc[i][j], 0, 0, 0);
+        if (T::SPREAD) copies(i);
+      }
+    } else {
+      i32x8 b[FM];
+#pragma unroll
+      for (int j = 0; j < FM; ++j) b[j] = fp8_frag(cur + g.xoff + j * 2048, g.s0);
+      i32x8 a[2];
+      a[0] = fp8_frag(cur + g.woff, g.s0);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        // one workgroup: the next row's fragment is read a row ahead
+        if (T::SPREAD && i + 1 < FN) a[(i + 1) & 1] = fp8_frag(cur + g.woff + (i + 1) * 2048, g.s0);
+        if (!T::SPREAD && i > 0) a[i & 1] = fp8_frag(cur + g.woff + i * 2048, g.s0);
+        if (T::SPREAD) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < FM; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s], b[j][s], acc[i][j], 0, 0, 0);
+          acc[i][j] = fp8_mfma(a[i & 1], b[j], acc[i][j], WROWS ? i & 3 : 0, (int)c.w[WROWS ? i >> 2 : 0],
+                               FM % 4 ? 0 : j & 3, (int)c.x[FM % 4 ? j : j >> 2]);
+        if (T::SPREAD) {
+          __builtin_amdgcn_sched_barrier(0);
+          copies(i);
+        }
+      }
     }
-    return;
-  }
-  i32x8 b[FM];
-#pragma unroll
-  for (int j = 0; j < FM; ++j) b[j] = fp8_frag(cur + g.xoff + j * 128, g.s0);
-#pragma unroll
-  for (int i = 0; i < FN; ++i) {
-    const i32x8 a = fp8_frag(cur + g.woff + i * 128, g.s0);
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-      acc[i][j] = fp8_mfma(a, b[j], acc[i][j], WROWS ? i & 3 : 0, (int)c.w[WROWS ? i >> 2 : 0], j & 3,
-                           (int)c.x[j >> 2]);
+    st = st + T::STAGE == LAST ? 0 : st + T::STAGE;
   }
 }
 
-// One BN x BM tile per workgroup, WN x WM waves of (16 FN) x (16 FM); K in
-// steps of one scale block (128), two LDS stages.  LDS rows are 128 bytes in
-// 16-byte chunks; chunk c of a row whose fragment row is r sits at slot c ^
-// (r % 8), so 8 consecutive lanes' reads cover all banks.
-template <int WN, int WM, int FN, int FM, bool WROWS, bool F32>
-__global__ __launch_bounds__(64 * WN * WM) void fp8_gemm_kernel(Fp8Gemm g, int ntiles, int mtiles) {
-  using T = Fp8Tile<WN, WM, FN, FM>;
-  __shared__ __align__(1024) uint8_t lds[2 * T::STAGE];
+// One BN x BM tile per workgroup; K in steps of one scale block (128).  In
+// LDS an operand's 16-row fragments follow each other, a row is 128 bytes in
+// 16-byte chunks, and chunk c of fragment row r sits at slot c ^ (r / 2 % 8):
+// the rows that a read touches in one cycle spread over all banks.
+template <class T, bool WROWS, bool F32>
+__global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int ntiles, int mtiles) {
+  constexpr int FN = T::FN, FM = T::FM, WM = T::WM;
+  __shared__ __align__(1024) uint8_t lds[T::NST * T::STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
   Fp8Wave v;
   v.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -441,43 +530,45 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_gemm_kernel(Fp8Gemm g, int n
   // copies: lane l brings slot l % 8 of row l / 8 of a piece.  Rows past the
   // matrix repeat its last row (their results are dropped).
   const int nrows = (int)min((int64_t)T::BN, g.N - n0), mrows = (int)min((int64_t)T::BM, g.M - m0);
-  v.rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.w + n0 * pitch), (short)0,
-                                           (int)(nrows * pitch), FP8_RSRC_W3);
-  v.rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.x + m0 * pitch), (short)0,
-                                           (int)(mrows * pitch), FP8_RSRC_W3);
+  v.rw = buffer_of(g.w + n0 * pitch, nrows * pitch);
+  v.rx = buffer_of(g.x + m0 * pitch, mrows * pitch);
+  v.lds = (uint32_t)(uintptr_t)(lptr_t)lds;
 #pragma unroll
   for (int i = 0; i < T::LOADS; ++i) {
     const int p = v.wave * T::LOADS + i;
     const bool isw = p < T::BN / 8;
-    const int row = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);
-    const int fr = isw ? fp8_pi((row % (16 * FN)) / FN) : (row % (16 * FM)) / FM;
+    const int at = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);   // LDS row of the operand
+    const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
+    const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
     v.off[i] = (uint32_t)min(row, (isw ? nrows : mrows) - 1) * (uint32_t)pitch +
-               (((lane & 7) ^ (fr & 7)) << 4);
+               (((lane & 7) ^ ((fr >> 1) & 7)) << 4);
+  }
+  // scale copies: four bytes a lane of a K block's row of scales, or with
+  // 128-row blocks of W one byte a lane, from the tile's first on (within
+  // the row of scales; lanes past the tile bring bytes that are not read)
+  {
+    const int64_t swp = WROWS ? fp8_scale_pitch(g.N) : (g.N + 127) / 128, sxp = fp8_scale_pitch(g.M);
+    const bool isw = v.wave & 1;
+    const int64_t sp = isw ? swp : sxp, at = isw ? (WROWS ? n0 : n0 / 128) : m0;
+    const int left = (int)min(sp - at, (int64_t)256);   // >= 16, or >= 1 of single bytes
+    v.soff = (isw && !WROWS) ? min(lane, left - 1) : min(4 * lane, left - 4);
+    v.sstep = (uint32_t)sp;
+    v.rs = buffer_of((isw ? g.sw : g.sx) + at, (kblocks - 1) * sp + left);
   }
   const int wn = v.wave / WM, wm = v.wave % WM;
   const int r = lane & 15, q = lane >> 4;
-  // scales: X's FM bytes of this lane's rows; W's one byte of the wave's
-  // 128-row block, or its FN rows' bytes
-  const int64_t nw0 = n0 + wn * 16 * FN;
-  v.sxp = fp8_scale_pitch(g.M);
-  v.sx = g.sx + min(m0 + wm * 16 * FM + r * FM, v.sxp - FM);
-  v.swp = WROWS ? fp8_scale_pitch(g.N) : (g.N + 127) / 128;
-  v.sw = g.sw + (WROWS ? min(nw0 + fp8_pi(r) * FN, v.swp - FN) : min(nw0 / 128, v.swp - 1));
-  v.woff = (wn * 16 * FN + fp8_pi(r) * FN) * 128;
-  v.xoff = T::BN * 128 + (wm * 16 * FM + r * FM) * 128;
-  v.s0 = ((2 * q) ^ (r & 7)) << 4;
+  v.woff = (wn * 16 * FN + r) * 128;
+  v.xoff = (T::BN + wm * 16 * FM + r) * 128;
+  v.s0 = ((2 * q) ^ ((r >> 1) & 7)) << 4;
+  v.sxoff = T::SX + wm * 16 * FM + r * FM;
+  v.swoff = T::SW + (WROWS ? wn * 16 * FN + fp8_pi(r) * FN : wn * 16 * FN / 128 * 4);
   f32x4 acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  Fp8Scales sc;
-  fp8_copy<T>(v, lds, 0);
-  fp8_scales<T, WROWS>(v, 0, sc);
-  for (int kb = 0; kb < kblocks; kb += 2) {
-    fp8_step<T, WROWS, F32>(v, lds, lds + T::STAGE, kb, kblocks, sc, acc);
-    if (kb + 1 < kblocks) fp8_step<T, WROWS, F32>(v, lds + T::STAGE, lds, kb + 1, kblocks, sc, acc);
-  }
+  fp8_loop<T, WROWS, F32>(v, kblocks, lds, acc);
+  const int64_t nw0 = n0 + wn * 16 * FN;
   const bool wide = g.N % FN == 0;
 #pragma unroll
   for (int j = 0; j < FM; ++j)
@@ -490,13 +581,15 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_gemm_kernel(Fp8Gemm g, int n
     }
 }
 
-// Few rows: a workgroup takes 16 rows of W and its NW waves split the K
-// blocks; every wave streams its part of W straight into fragments (a lane
-// 32 bytes of its row, a wave 16 whole 128-byte lines) and the partial sums
-// meet in LDS in wave order.  FUSED: X comes as bf16 and is rounded to E4M3
-// in the lane that feeds it to the matrix core: the lane's 32 elements, the
-// block's largest magnitude from the four lanes that share the row.
-constexpr int SK_NW = 8, SK_CH = 4;   // waves; K blocks in flight per wave
+// Few rows: a workgroup takes 16 rows of W and its waves split the K blocks;
+// every wave streams its part of W straight into fragments (a lane 32 bytes
+// of its row, a wave 16 whole 128-byte lines) and the partial sums meet in
+// LDS in wave order.  All loads of SK_CH K blocks are issued before the
+// first product, X's before W's, so a chunk costs one memory round trip.
+// FUSED: X comes as bf16 and is rounded to E4M3 in the lane that feeds it to
+// the matrix core: the lane's 32 elements, the block's largest magnitude
+// from the four lanes that share the row.
+constexpr int SK_NW = 8, SK_CH = 3;   // waves; K blocks in flight per wave
 
 template <int FM, bool WROWS, bool F32, bool FUSED, bool VEC>
 __global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g, const uint16_t* __restrict__ xb) {
@@ -516,24 +609,42 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g, const
 #pragma unroll
   for (int j = 0; j < FM; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int c0 = b0; c0 < b1; c0 += SK_CH) {
-    u32x4 lo[SK_CH], hi[SK_CH];
-    uint32_t s[SK_CH];
+    // blocks past the wave's last repeat it and are not multiplied
+    u32x4 wl[SK_CH], wh[SK_CH], xr[SK_CH][FM][FUSED ? 4 : 2];
+    uint32_t s[SK_CH], sx[SK_CH][FM];
 #pragma unroll
     for (int u = 0; u < SK_CH; ++u) {
       const int64_t kb = min(c0 + u, b1 - 1);
-      lo[u] = gload16(w + kb * 128);
-      hi[u] = gload16(w + kb * 128 + 16);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        const int64_t m = min((int64_t)(16 * j + r), g.M - 1);
+        if (FUSED && VEC) {
+          const int64_t k0 = kb * 128 + 32 * q;
+#pragma unroll
+          for (int p = 0; p < 4; ++p)   // past K: the row's last elements, zeroed below
+            xr[u][j][p] = gload16(xb + m * g.K + min(k0 + 8 * p, g.K - 8));
+        } else if (!FUSED) {
+          xr[u][j][0] = gload16(g.x + m * pitch + kb * 128 + 32 * q);
+          xr[u][j][1] = gload16(g.x + m * pitch + kb * 128 + 32 * q + 16);
+          sx[u][j] = g.sx[kb * sxp + m];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < SK_CH; ++u) {
+      const int64_t kb = min(c0 + u, b1 - 1);
+      wl[u] = gload16(w + kb * 128);
+      wh[u] = gload16(w + kb * 128 + 16);
       s[u] = sw[kb * swp];
     }
 #pragma unroll
     for (int u = 0; u < SK_CH; ++u) {
-      if (c0 + u >= b1) break;
+      if (c0 + u >= b1) continue;
       const int64_t kb = c0 + u;
-      const i32x8 a = {(int)lo[u][0], (int)lo[u][1], (int)lo[u][2], (int)lo[u][3],
-                       (int)hi[u][0], (int)hi[u][1], (int)hi[u][2], (int)hi[u][3]};
+      const i32x8 a = {(int)wl[u][0], (int)wl[u][1], (int)wl[u][2], (int)wl[u][3],
+                       (int)wh[u][0], (int)wh[u][1], (int)wh[u][2], (int)wh[u][3]};
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
-        const int64_t m = min((int64_t)(16 * j + r), g.M - 1);
         i32x8 b;
         uint32_t sb;
         if (FUSED) {
@@ -542,7 +653,16 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g, const
           uint32_t top = 0;
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            load8<false, VEC>(xb, m * g.K + k0 + 8 * p, g.K - k0 - 8 * p, v[p]);
+            if (VEC) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t h = xr[u][j][p][i >> 1];
+                v[p][i] = k0 + 8 * p < g.K ? __uint_as_float((i & 1) ? h & 0xFFFF0000u : h << 16) : 0.0f;
+              }
+            } else {
+              const int64_t m = min((int64_t)(16 * j + r), g.M - 1);
+              load8<false, false>(xb, m * g.K + k0 + 8 * p, g.K - k0 - 8 * p, v[p]);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = max(top, finite_bits(v[p][i]));
           }
@@ -559,10 +679,9 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g, const
           }
           sb = (uint32_t)(e + 127);
         } else {
-          const u32x4 xl = gload16(g.x + m * pitch + kb * 128 + 32 * q);
-          const u32x4 xh = gload16(g.x + m * pitch + kb * 128 + 32 * q + 16);
+          const u32x4 xl = xr[u][j][0], xh = xr[u][j][1];
           b = i32x8{(int)xl[0], (int)xl[1], (int)xl[2], (int)xl[3], (int)xh[0], (int)xh[1], (int)xh[2], (int)xh[3]};
-          sb = g.sx[kb * sxp + m];
+          sb = sx[u][j];
         }
         if (F32) {
           bf16x8 av[4], bv[4];
@@ -638,21 +757,21 @@ hipError_t launch_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int
   return hipGetLastError();
 }
 
-template <int WN, int WM, int FN, int FM>
+template <int WN, int WM, int FN, int FM, int NST>
 static hipError_t gemm_tile(const Fp8Gemm& g, hipStream_t s) {
-  using T = Fp8Tile<WN, WM, FN, FM>;
+  using T = Fp8Tile<WN, WM, FN, FM, NST>;
   const int64_t nt = (g.N + T::BN - 1) / T::BN, mt = (g.M + T::BM - 1) / T::BM;
   const dim3 grid((unsigned)(nt * mt)), block(64 * T::NW);
   if (g.w_rows) {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, FN, FM, true, true>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, true>), grid, block, 0, s, g, (int)nt, (int)mt);
     else
-      hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, FN, FM, true, false>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, false>), grid, block, 0, s, g, (int)nt, (int)mt);
   } else {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, FN, FM, false, true>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, true>), grid, block, 0, s, g, (int)nt, (int)mt);
     else
-      hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, FN, FM, false, false>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, false>), grid, block, 0, s, g, (int)nt, (int)mt);
   }
   return hipGetLastError();
 }
@@ -675,14 +794,36 @@ static hipError_t skinny(const Fp8Gemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+static const float FP8_T16[5] = {1.30f, 1.15f, 0.75f, 1.05f, 0.65f};
+static const float FP8_T32[5] = {2.33f, 1.96f, 1.30f, 1.70f, 1.02f};
+
+static int64_t tiles(const Fp8Gemm& g, int64_t bn, int64_t bm) {
+  return ((g.N + bn - 1) / bn) * ((g.M + bm - 1) / bm);
+}
+static float rounds(const Fp8Gemm& g, int64_t bn, int64_t bm, int64_t slots) {
+  return (float)((tiles(g, bn, bm) + slots - 1) / slots);
+}
+
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
   if (g.M <= 16) return skinny<1>(g, s);
   if (g.M <= 32) return skinny<2>(g, s);
   if (g.M <= 64) return skinny<4>(g, s);
-  // 256 x 256 tiles once they fill the 256 CUs, else 128 x 128
-  const int64_t big = ((g.N + 255) / 256) * ((g.M + 255) / 256);
-  if (big >= 256) return gemm_tile<2, 4, 8, 4>(g, s);
-  return gemm_tile<2, 2, 4, 4>(g, s);
+  // Tile: the least time by rounds of the 256 CUs.  A round of a tile takes
+  // a time in proportion to its K blocks and about four more (launch, first
+  // copies, stores); the factors are measured (us for a K block on one
+  // round of 5760 x 2880): bf16 results 1.30, 1.15, 0.75 and, with two
+  // workgroups on a CU, 1.05 (one: 0.65); fp32 results 2.33, 1.96, 1.30,
+  // 1.70 (1.02).  2047 x 5760 x 2880: 256 x 256 40.1 us, 256 x 192 36.3, 128
+  // x 192 46.0, 128 x 128 43.8; 2048 x 2880 x 5760: 66.2, 58.7, 41.7, 41.9.
+  const float* us = g.out_f32 ? FP8_T32 : FP8_T16;
+  const float a = us[0] * rounds(g, 256, 256, 256), b = us[1] * rounds(g, 256, 192, 256);
+  const float c = us[2] * rounds(g, 128, 192, 256);
+  const int64_t small = tiles(g, 128, 128), rest = small % 512;
+  const float d = us[3] * (small / 512) + (rest > 256 ? us[3] : rest ? us[4] : 0.0f);
+  if (a <= b && a <= c && a <= d) return gemm_tile<2, 4, 8, 4, 2>(g, s);
+  if (b <= c && b <= d) return gemm_tile<2, 4, 8, 3, 2>(g, s);
+  if (c <= d) return gemm_tile<2, 4, 4, 3, 3>(g, s);
+  return gemm_tile<2, 2, 4, 4, 2>(g, s);
 }
 
 bool fp8_fused_fits(int64_t M, int64_t K) { return M <= 16; }
