@@ -133,13 +133,18 @@ int mxmoe_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int64_t row
                         uint8_t* codes_t, uint8_t* scales_t, void* stream);
 
 /* out [M, N] = X W^T + bias for 8-bit X [M, K] (block_rows 1) and W [N, K]
- * (block_rows w_block_rows).  Products and sums in fp32 on the block-scaled
- * matrix cores; bias bf16 [N] or NULL; out bf16 or fp32 (out_dtype), 16-byte
- * aligned, rounded once. */
+ * (block_rows w_block_rows); bias bf16 [N] or NULL; out bf16 or fp32
+ * (out_dtype), 16-byte aligned, rounded once.  fp32 results: products and
+ * sums in fp32 (values below 2^-126 may count as 0).  bf16 results: fp32
+ * sums over K blocks, but within a K block the block-scaled matrix core
+ * drops what lies below 2^-13 of its largest product (about 1.5e-5 of a
+ * result over random values, a hundredth of its rounding to bf16).  A NaN in
+ * a row of X or W stays in that row of the result.  The order of the sums,
+ * and so the result's last bits, depend on M, N and K alone. */
 int mxmoe_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes,
                      const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales,
                      int w_block_rows, const uint16_t* bias, int out_dtype, void* out,
-                     void* stream);
+                     void* workspace, size_t workspace_bytes, void* stream);
 /* The same from bf16 rows x [M, K], which are quantized with block_rows 1
  * (in the product's own launch for few rows, else into the workspace), and
  * W with block_rows 128.  A linear layer's input gradient is this product
@@ -152,9 +157,10 @@ int mxmoe_fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const u
  * one column.  M <= 2^22. */
 int mxmoe_fp8_linear_dw(int64_t M, int64_t N, int64_t K, const uint16_t* dy, const uint16_t* x,
                         float* dw, void* workspace, size_t workspace_bytes, void* stream);
-/* Bytes of workspace of mxmoe_fp8_linear (dw 0) or mxmoe_fp8_linear_dw (dw
- * 1); 0 if a size is out of range. */
-size_t mxmoe_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int dw);
+/* Bytes of workspace of the three products; 0 if a size is out of range. */
+size_t mxmoe_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
+size_t mxmoe_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
+size_t mxmoe_fp8_linear_dw_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* ------------------------------------------- 8-bit activation checkpoints */
 

@@ -506,7 +506,8 @@ __device__ __forceinline__ void fp8_loop(const Fp8Wave& g, int kblocks, const ui
 // 16-byte chunks, and chunk c of fragment row r sits at slot c ^ (r / 2 % 8):
 // the rows that a read touches in one cycle spread over all banks.
 template <class T, bool WROWS, bool F32>
-__global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int ntiles, int mtiles) {
+__global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int ntiles, int mtiles,
+                                                              int splits) {
   constexpr int FN = T::FN, FM = T::FM, WM = T::WM;
   __shared__ __align__(1024) uint8_t lds[T::NST * T::STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -514,11 +515,14 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
   v.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // tile of this block: XCD x takes a contiguous range of the order in which
   // bands of 8 m-tiles run through all n-tiles, m fastest
-  int nt, mt;
+  // (with splits, every tile's parts one after the other)
+  int nt, mt, split;
   {
-    const int L = ntiles * mtiles, b = blockIdx.x;
+    const int L = ntiles * mtiles * splits, b = blockIdx.x;
     const int x = b & 7, base = L >> 3, extra = L & 7;
-    const int item = x * base + min(x, extra) + (b >> 3);
+    int item = x * base + min(x, extra) + (b >> 3);
+    split = item % splits;
+    item /= splits;
     const int band = item / (8 * ntiles), rows = min(8, mtiles - 8 * band);
     const int local = item - band * 8 * ntiles;
     mt = band * 8 + local % rows;
@@ -526,7 +530,8 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
   }
   const int64_t n0 = (int64_t)nt * T::BN, m0 = (int64_t)mt * T::BM;
   const int64_t pitch = fp8_pitch(g.K);
-  const int kblocks = (int)(pitch / 128);
+  const int all = (int)(pitch / 128);
+  const int kb0 = (int)((int64_t)all * split / splits), kblocks = (int)((int64_t)all * (split + 1) / splits) - kb0;
   // copies: lane l brings slot l % 8 of row l / 8 of a piece.  Rows past the
   // matrix repeat its last row (their results are dropped).
   const int nrows = (int)min((int64_t)T::BN, g.N - n0), mrows = (int)min((int64_t)T::BM, g.M - m0);
@@ -540,7 +545,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
     const int at = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);   // LDS row of the operand
     const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
     const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
-    v.off[i] = (uint32_t)min(row, (isw ? nrows : mrows) - 1) * (uint32_t)pitch +
+    v.off[i] = (uint32_t)min(row, (isw ? nrows : mrows) - 1) * (uint32_t)pitch + (uint32_t)kb0 * 128 +
                (((lane & 7) ^ ((fr >> 1) & 7)) << 4);
   }
   // scale copies: four bytes a lane of a K block's row of scales, or with
@@ -553,7 +558,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
     const int left = (int)min(sp - at, (int64_t)256);   // >= 16, or >= 1 of single bytes
     v.soff = (isw && !WROWS) ? min(lane, left - 1) : min(4 * lane, left - 4);
     v.sstep = (uint32_t)sp;
-    v.rs = buffer_of((isw ? g.sw : g.sx) + at, (kblocks - 1) * sp + left);
+    v.rs = buffer_of((isw ? g.sw : g.sx) + kb0 * sp + at, (kblocks - 1) * sp + left);
   }
   const int wn = v.wave / WM, wm = v.wave % WM;
   const int r = lane & 15, q = lane >> 4;
@@ -570,6 +575,20 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
   fp8_loop<T, WROWS, F32>(v, kblocks, lds, acc);
   const int64_t nw0 = n0 + wn * 16 * FN;
   const bool wide = g.N % FN == 0;
+  if (splits > 1) {
+    g.out = g.part + split * g.M * g.N;
+    g.bias = nullptr;
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float o[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) o[i] = acc[i][j][t];
+        fp8_store<FN, true>(g, m0 + wm * 16 * FM + r * FM + j, nw0 + (4 * t + q) * FN, o, wide);
+      }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < FM; ++j)
 #pragma unroll
@@ -579,6 +598,36 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
       for (int i = 0; i < FN; ++i) o[i] = acc[i][j][t];
       fp8_store<FN, F32>(g, m0 + wm * 16 * FM + r * FM + j, nw0 + (4 * t + q) * FN, o, wide);
     }
+}
+
+// The sum of a product's `splits` fp32 parts in their order, plus the bias.
+template <bool F32>
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm g, int splits) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = g.M * g.N;
+  if (i >= all) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool wide = g.N % 4 == 0;   // then the four are of one row, and aligned
+  if (wide) {
+    for (int s = 0; s < splits; ++s) {
+      const f32x4 p = *reinterpret_cast<const f32x4*>(g.part + s * all + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += p[e];
+    }
+    fp8_store<4, F32>(g, i / g.N, i % g.N, v, true);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (i + e >= all) return;
+    float one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s) one[0] += g.part[s * all + i + e];
+    const int64_t n = (i + e) % g.N;
+    if (g.bias) one[0] += bf16_to_f32(g.bias[n]);
+    if (F32)
+      static_cast<float*>(g.out)[i + e] = one[0];
+    else
+      static_cast<uint16_t*>(g.out)[i + e] = (uint16_t)f32_to_bf16(one[0]);
+  }
 }
 
 // Few rows: a workgroup takes 16 rows of W and its waves split the K blocks;
@@ -758,20 +807,20 @@ hipError_t launch_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int
 }
 
 template <int WN, int WM, int FN, int FM, int NST>
-static hipError_t gemm_tile(const Fp8Gemm& g, hipStream_t s) {
+static hipError_t gemm_tile(const Fp8Gemm& g, int splits, hipStream_t s) {
   using T = Fp8Tile<WN, WM, FN, FM, NST>;
-  const int64_t nt = (g.N + T::BN - 1) / T::BN, mt = (g.M + T::BM - 1) / T::BM;
-  const dim3 grid((unsigned)(nt * mt)), block(64 * T::NW);
+  const int nt = (int)((g.N + T::BN - 1) / T::BN), mt = (int)((g.M + T::BM - 1) / T::BM);
+  const dim3 grid((unsigned)((int64_t)nt * mt * splits)), block(64 * T::NW);
   if (g.w_rows) {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, true>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, true>), grid, block, 0, s, g, nt, mt, splits);
     else
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, false>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, false>), grid, block, 0, s, g, nt, mt, splits);
   } else {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, true>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, true>), grid, block, 0, s, g, nt, mt, splits);
     else
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, false>), grid, block, 0, s, g, (int)nt, (int)mt);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, false>), grid, block, 0, s, g, nt, mt, splits);
   }
   return hipGetLastError();
 }
@@ -794,36 +843,91 @@ static hipError_t skinny(const Fp8Gemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-static const float FP8_T16[5] = {1.30f, 1.15f, 0.75f, 1.05f, 0.65f};
-static const float FP8_T32[5] = {2.33f, 1.96f, 1.30f, 1.70f, 1.02f};
+// How a product runs: a tile (0: 256 x 256 of W and X rows, 1: 256 x 192, 2:
+// 128 x 192, 3: 128 x 128), or -1 for few rows; and parts of K.
+struct Fp8Plan {
+  int tile, splits;
+};
 
-static int64_t tiles(const Fp8Gemm& g, int64_t bn, int64_t bm) {
-  return ((g.N + bn - 1) / bn) * ((g.M + bm - 1) / bm);
+// The least time by rounds of the 256 CUs.  A round of a tile takes a time in
+// proportion to its K blocks and about four more (launch, first copies,
+// stores); the factors are measured (us for a K block on one round of 5760 x
+// 2880): bf16 results 1.30, 1.15, 0.75 and, with two workgroups on a CU,
+// 1.05 (one: 0.65); fp32 results 2.33, 1.96, 1.30, 1.70 (1.02).
+//   2047 x 5760 x 2880: 256 x 256 40.1 us, 256 x 192 36.3, 128 x 192 46.0,
+//   128 x 128 43.8;  2048 x 2880 x 5760: 66.2, 58.7, 41.7, 41.9.
+// Where 128 x 128 tiles leave CUs idle, K is split over them, in parts of 3
+// blocks or more, and a second launch joins the fp32 parts, which costs a
+// launch and their bytes (written and read at 4 TB/s).
+static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
+  static const float T16[5] = {1.30f, 1.15f, 0.75f, 1.05f, 0.65f};
+  static const float T32[5] = {2.33f, 1.96f, 1.30f, 1.70f, 1.02f};
+  static const int BN[4] = {256, 256, 128, 128}, BM[4] = {256, 192, 192, 128};
+  // few rows: streaming W once per 16 rows of it beats tiles while there are
+  // enough such groups (32 rows, 5760 x 2880: 11.4 us against 16; 512 x 8192:
+  // 18 against 9), and always for a single fragment of rows
+  if (M <= 16 || (M <= 32 && N >= 2048)) return {-1, 1};
+  const float* t = f32 ? T32 : T16;
+  const int64_t kb = fp8_pitch(K) / 128;
+  Fp8Plan best{0, 1};
+  float least = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t tiles = ((N + BN[i] - 1) / BN[i]) * ((M + BM[i] - 1) / BM[i]);
+    float us;
+    if (i < 3) {
+      us = t[i] * (float)((tiles + 255) / 256);
+    } else {
+      const int64_t rest = tiles % 512;
+      us = t[3] * (float)(tiles / 512) + (rest > 256 ? t[3] : rest ? t[4] : 0.0f);
+    }
+    us *= (float)(kb + 4);
+    if (i == 0 || us < least) {
+      least = us;
+      best = {i, 1};
+    }
+    if (i == 3 && tiles <= 128) {
+      const int64_t s = kb / 3 < 256 / tiles ? kb / 3 : 256 / tiles;
+      if (s > 1) {
+        const float join = 3.0f + (float)(s * M * N) * 8.0f / 4.0e6f;
+        us = t[4] * (float)((kb + s - 1) / s + 4) + join;
+        if (us < least) {
+          least = us;
+          best = {3, (int)s};
+        }
+      }
+    }
+  }
+  return best;
 }
-static float rounds(const Fp8Gemm& g, int64_t bn, int64_t bm, int64_t slots) {
-  return (float)((tiles(g, bn, bm) + slots - 1) / slots);
+
+size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
+  const Fp8Plan p = fp8_plan(M, N, K, out_f32 != 0);
+  return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
 }
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
-  if (g.M <= 16) return skinny<1>(g, s);
-  if (g.M <= 32) return skinny<2>(g, s);
-  if (g.M <= 64) return skinny<4>(g, s);
-  // Tile: the least time by rounds of the 256 CUs.  A round of a tile takes
-  // a time in proportion to its K blocks and about four more (launch, first
-  // copies, stores); the factors are measured (us for a K block on one
-  // round of 5760 x 2880): bf16 results 1.30, 1.15, 0.75 and, with two
-  // workgroups on a CU, 1.05 (one: 0.65); fp32 results 2.33, 1.96, 1.30,
-  // 1.70 (1.02).  2047 x 5760 x 2880: 256 x 256 40.1 us, 256 x 192 36.3, 128
-  // x 192 46.0, 128 x 128 43.8; 2048 x 2880 x 5760: 66.2, 58.7, 41.7, 41.9.
-  const float* us = g.out_f32 ? FP8_T32 : FP8_T16;
-  const float a = us[0] * rounds(g, 256, 256, 256), b = us[1] * rounds(g, 256, 192, 256);
-  const float c = us[2] * rounds(g, 128, 192, 256);
-  const int64_t small = tiles(g, 128, 128), rest = small % 512;
-  const float d = us[3] * (small / 512) + (rest > 256 ? us[3] : rest ? us[4] : 0.0f);
-  if (a <= b && a <= c && a <= d) return gemm_tile<2, 4, 8, 4, 2>(g, s);
-  if (b <= c && b <= d) return gemm_tile<2, 4, 8, 3, 2>(g, s);
-  if (c <= d) return gemm_tile<2, 4, 4, 3, 3>(g, s);
-  return gemm_tile<2, 2, 4, 4, 2>(g, s);
+  const Fp8Plan p = fp8_plan(g.M, g.N, g.K, g.out_f32 != 0);
+  if (p.tile < 0) {
+    if (g.M <= 16) return skinny<1>(g, s);
+    return skinny<2>(g, s);
+  }
+  if (p.splits > 1 && !g.part) return hipErrorInvalidValue;
+  hipError_t e;
+  if (p.tile == 0)
+    e = gemm_tile<2, 4, 8, 4, 2>(g, p.splits, s);
+  else if (p.tile == 1)
+    e = gemm_tile<2, 4, 8, 3, 2>(g, p.splits, s);
+  else if (p.tile == 2)
+    e = gemm_tile<2, 4, 4, 3, 3>(g, p.splits, s);
+  else
+    e = gemm_tile<2, 2, 4, 4, 2>(g, p.splits, s);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const dim3 grid((unsigned)((g.M * g.N + 1023) / 1024)), block(256);
+  if (g.out_f32)
+    hipLaunchKernelGGL(fp8_join_kernel<true>, grid, block, 0, s, g, p.splits);
+  else
+    hipLaunchKernelGGL(fp8_join_kernel<false>, grid, block, 0, s, g, p.splits);
+  return hipGetLastError();
 }
 
 bool fp8_fused_fits(int64_t M, int64_t K) { return M <= 16; }

@@ -35,8 +35,10 @@ struct Fp8Gemm {
   const uint16_t* bias;     // bf16 [N] or nullptr
   void* out;                // [M, N], bf16 or fp32 with out_f32
   int out_f32;
+  float* part;              // fp8_part_bytes of scratch
 };
 // out = X W^T + bias
+size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32);
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s);
 // the same from bf16 rows x (rounded inside) for few rows
 bool fp8_fused_fits(int64_t M, int64_t K);

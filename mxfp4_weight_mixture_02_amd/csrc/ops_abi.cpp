@@ -108,18 +108,24 @@ int check_product(int64_t M, int64_t N, int64_t K) {
   return rc;
 }
 
-// Workspace of a product: X's codes and scales, then (dw) W's.
+// Workspace of a product: X's codes and scales, then (dw) W's, then the
+// product's own.
 struct Fp8Layout {
-  size_t xs, w, ws, total;
+  size_t xs, w, ws, part, total;
 };
-Fp8Layout fp8_layout(int64_t M, int64_t N, int64_t K, bool w) {
+Fp8Layout fp8_layout(int64_t M, int64_t N, int64_t K, bool w, int out_f32) {
   Fp8Layout L;
   const size_t kb = (size_t)mxmoe::fp8_pitch(K) / 128;
   L.xs = up((size_t)M * mxmoe::fp8_pitch(K), ALIGN);
   L.w = L.xs + up(kb * mxmoe::fp8_scale_pitch(M), ALIGN);
   L.ws = L.w + (w ? up((size_t)N * mxmoe::fp8_pitch(K), ALIGN) : 0);
-  L.total = L.ws + (w ? up(kb * mxmoe::fp8_scale_pitch(N), ALIGN) : 0);
+  L.part = L.ws + (w ? up(kb * mxmoe::fp8_scale_pitch(N), ALIGN) : 0);
+  L.total = L.part + up(mxmoe::fp8_part_bytes(M, N, K, out_f32), ALIGN);
   return L;
+}
+
+size_t matmul_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  return up(mxmoe::fp8_part_bytes(M, N, K, out_dtype == MXMOE_F32), ALIGN) + ALIGN;
 }
 
 int check_swiglu8(int64_t R, int64_t I, float alpha, float limit) {
@@ -238,7 +244,7 @@ int mxmoe_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int64_t row
 int mxmoe_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes,
                      const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales,
                      int w_block_rows, const uint16_t* bias, int out_dtype, void* out,
-                     void* stream) {
+                     void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_product(M, N, K);
   if (rc) return rc;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !out)
@@ -250,17 +256,31 @@ int mxmoe_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes,
   if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 16) ||
       (w_block_rows == 1 && !aligned(w_scales, 16)) || !aligned(out, 16) || !aligned(bias, 2))
     return fail(MXFP4_EINVAL, "codes, scales of rows and out must be 16-byte aligned");
+  rc = check_workspace(workspace, workspace_bytes, matmul_bytes(M, N, K, out_dtype));
+  if (rc) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const mxmoe::Fp8Gemm g{M, N, K, x_codes, x_scales, w_codes, w_scales, w_block_rows == 1, bias,
-                         out, out_dtype == MXMOE_F32};
+                         out, out_dtype == MXMOE_F32, static_cast<float*>(workspace)};
   LAUNCH(mxmoe::launch_fp8_gemm(g, s), "fp8_matmul");
   return ok();
 }
 
-size_t mxmoe_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int dw) {
-  if ((dw ? check_product(N, K, M) : check_product(M, N, K)) != MXFP4_OK) return 0;
+size_t mxmoe_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  if (check_product(M, N, K) != MXFP4_OK || check_dtype(out_dtype, nullptr, "out") != MXFP4_OK) return 0;
   ok();
-  return dw ? fp8_layout(N, K, M, true).total : fp8_layout(M, N, K, false).total;
+  return matmul_bytes(M, N, K, out_dtype);
+}
+
+size_t mxmoe_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  if (check_product(M, N, K) != MXFP4_OK || check_dtype(out_dtype, nullptr, "out") != MXFP4_OK) return 0;
+  ok();
+  return fp8_layout(M, N, K, false, out_dtype == MXMOE_F32).total;
+}
+
+size_t mxmoe_fp8_linear_dw_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_product(N, K, M) != MXFP4_OK) return 0;
+  ok();
+  return fp8_layout(N, K, M, true, 1).total;
 }
 
 int mxmoe_fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const uint8_t* w_codes,
@@ -275,13 +295,13 @@ int mxmoe_fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const u
   if (rc) return rc;
   if (!aligned(w_codes, 16) || !aligned(out, 16) || !aligned(bias, 2))
     return fail(MXFP4_EINVAL, "w_codes and out must be 16-byte aligned");
-  const Fp8Layout L = fp8_layout(M, N, K, false);
+  const Fp8Layout L = fp8_layout(M, N, K, false, out_dtype == MXMOE_F32);
   rc = check_workspace(workspace, workspace_bytes, L.total);
   if (rc) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const mxmoe::Fp8Gemm g{M, N, K, ws, ws + L.xs, w_codes, w_scales, 0, bias, out,
-                         out_dtype == MXMOE_F32};
+                         out_dtype == MXMOE_F32, reinterpret_cast<float*>(ws + L.part)};
   if (mxmoe::fp8_fused_fits(M, K)) {
     LAUNCH(mxmoe::launch_fp8_fused(g, x, s), "fp8_linear");
     return ok();
@@ -298,14 +318,15 @@ int mxmoe_fp8_linear_dw(int64_t M, int64_t N, int64_t K, const uint16_t* dy, con
   if (!dy || !x || !dw) return fail(MXFP4_EINVAL, "dy, x and dw are required");
   if (!aligned(dy, 2) || !aligned(x, 2) || !aligned(dw, 16))
     return fail(MXFP4_EINVAL, "dw must be 16-byte, dy and x 2-byte aligned");
-  const Fp8Layout L = fp8_layout(N, K, M, true);
+  const Fp8Layout L = fp8_layout(N, K, M, true, 1);
   rc = check_workspace(workspace, workspace_bytes, L.total);
   if (rc) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   LAUNCH(mxmoe::launch_fp8_quantize_cols(dy, 0, M, N, ws, ws + L.xs, s), "fp8_quantize_cols");
   LAUNCH(mxmoe::launch_fp8_quantize_cols(x, 0, M, K, ws + L.w, ws + L.ws, s), "fp8_quantize_cols");
-  const mxmoe::Fp8Gemm g{N, K, M, ws, ws + L.xs, ws + L.w, ws + L.ws, 1, nullptr, dw, 1};
+  const mxmoe::Fp8Gemm g{N, K, M, ws, ws + L.xs, ws + L.w, ws + L.ws, 1, nullptr, dw, 1,
+                         reinterpret_cast<float*>(ws + L.part)};
   LAUNCH(mxmoe::launch_fp8_gemm(g, s), "fp8_matmul");
   return ok();
 }

@@ -41,12 +41,13 @@ def lib() -> ctypes.CDLL:
         L.mxmoe_route.argtypes = [opts, i64, i32, i32] + [vp] * 7 + [sz, vp]
         L.mxmoe_route_backward.argtypes = [opts, i64, i32, i32] + [vp] * 5
         ci, f32 = ctypes.c_int, ctypes.c_float
-        L.mxmoe_fp8_linear_workspace_bytes.restype = sz
-        L.mxmoe_fp8_linear_workspace_bytes.argtypes = [i64, i64, i64, ci]
+        for n, more in (("matmul", [ci]), ("linear", [ci]), ("linear_dw", [])):
+            f = getattr(L, f"mxmoe_fp8_{n}_workspace_bytes")
+            f.restype, f.argtypes = sz, [i64, i64, i64] + more
         L.mxmoe_fp8_quantize.argtypes = [vp, ci, i64, i64, ci, vp, vp, vp]
         L.mxmoe_fp8_quantize_t.argtypes = [vp, ci, i64, i64, vp, vp, vp]
         L.mxmoe_fp8_transpose.argtypes = [vp, vp, i64, i64, vp, vp, vp]
-        L.mxmoe_fp8_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, ci, vp, ci, vp, vp]
+        L.mxmoe_fp8_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, ci, vp, ci, vp, vp, sz, vp]
         L.mxmoe_fp8_linear.argtypes = [i64, i64, i64, vp, vp, vp, vp, ci, vp, vp, sz, vp]
         L.mxmoe_fp8_linear_dw.argtypes = [i64, i64, i64, vp, vp, vp, vp, sz, vp]
         layer = [ctypes.POINTER(Dims), ctypes.POINTER(Weights)]
@@ -369,8 +370,10 @@ def fp8_matmul(x: Fp8Matrix, w: Fp8Matrix, bias: torch.Tensor | None = None,
     _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
     dev = _same_device(x=x.codes, x_scales=x.scales, w=w.codes, w_scales=w.scales, bias=bias)
     out = _out(M, N, dtype, dev)
+    nbytes = _bytes_needed("mxmoe_fp8_matmul_workspace_bytes", M, N, x.K, _DTYPES[dtype])
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call("mxmoe_fp8_matmul", dev, M, N, x.K, _p(x.codes), _p(x.scales), _p(w.codes), _p(w.scales),
-          w.block_rows, _p(bias), _DTYPES[dtype], _p(out))
+          w.block_rows, _p(bias), _DTYPES[dtype], _p(out), _p(ws), nbytes)
     return out
 
 
@@ -387,8 +390,8 @@ def fp8_linear(x: torch.Tensor, w: Fp8Matrix, bias: torch.Tensor | None = None,
     _shape(x, (M, K), torch.bfloat16, "x")
     _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
     dev = _same_device(x=x, w=w.codes, w_scales=w.scales, bias=bias)
-    nbytes = _bytes_needed("mxmoe_fp8_linear_workspace_bytes", M, N, K, 0)
     out = _out(M, N, dtype, dev)
+    nbytes = _bytes_needed("mxmoe_fp8_linear_workspace_bytes", M, N, K, _DTYPES[dtype])
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call("mxmoe_fp8_linear", dev, M, N, K, _p(x), _p(w.codes), _p(w.scales), _p(bias), _DTYPES[dtype],
           _p(out), _p(ws), nbytes)
@@ -410,7 +413,7 @@ def fp8_linear_dw(dy: torch.Tensor, x: torch.Tensor) -> torch.Tensor:
     _shape(dy, (M, N), torch.bfloat16, "dy")
     _shape(x, (M, K), torch.bfloat16, "x")
     dev = _same_device(dy=dy, x=x)
-    nbytes = _bytes_needed("mxmoe_fp8_linear_workspace_bytes", M, N, K, 1)
+    nbytes = _bytes_needed("mxmoe_fp8_linear_dw_workspace_bytes", M, N, K)
     dw = torch.empty((N, K), dtype=torch.float32, device=dev)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call("mxmoe_fp8_linear_dw", dev, M, N, K, _p(dy), _p(x), _p(dw), _p(ws), nbytes)

@@ -97,7 +97,9 @@ def test_quantize_edges():
 
 PRODUCTS = [(1, 1, 1), (1, 17, 130), (2, 64, 128), (5, 33, 1000), (16, 16, 256), (16, 100, 2880), (17, 130, 260),
             (31, 40, 64), (33, 257, 384), (64, 128, 129), (65, 127, 100), (128, 128, 128), (129, 255, 640),
-            (300, 500, 1300), (1, 5760, 2880), (64, 2880, 640), (700, 96, 33)]
+            (300, 500, 1300), (1, 5760, 2880), (64, 2880, 640), (700, 96, 33),
+            # few tiles: K split into parts and joined
+            (65, 130, 2880), (128, 129, 4000), (200, 40, 5000), (130, 1000, 777)]
 
 
 def _integers(r, shape, top=3):
@@ -133,7 +135,8 @@ def test_integer_products_are_exact(M, N, K):
     assert torch.equal(fp8_matmul(q, V, bias=b), dev(rows + bias, torch.bfloat16))
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 33), (130, 129, 257), (511, 200, 640), (2049, 320, 96), (64, 16, 16)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 33), (130, 129, 257), (511, 200, 640), (2049, 320, 96), (64, 16, 16),
+                                   (5000, 100, 70), (3000, 66, 65)])
 def test_integer_weight_gradients_are_exact(M, N, K):
     print("dw", M, N, K, flush=True)
     r = np.random.default_rng(M + N + K)
@@ -216,21 +219,23 @@ def test_zeros_and_tiny_values():
 
 
 def test_offsets_past_32_bits():
-    """2.2e9 bytes of codes, and 2.2e9 outputs: the last rows equal those of a
-    small call."""
+    """2.2e9 bytes of codes, and 2.2e9 outputs: the last rows are those of a
+    small call, to two bf16 roundings (other sizes may sum in another order)."""
+    def near(a, b):
+        return torch.all((a.float() - b.float()).abs() <= 2.0 ** -7 * b.float().abs() + 1e-3)
+
     g = torch.Generator(device=DEV).manual_seed(0)
     x = torch.empty(540000, 4096, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
     W = fp8_quantize(torch.empty(40, 4096, device=DEV).normal_(generator=g), 128)
     y = fp8_linear(x, W)
-    # rows of a tile are independent, and both calls sum a row in K order
-    assert torch.equal(y[-1000:], fp8_linear(x[-1000:].contiguous(), W))
+    assert near(y[-1000:], fp8_linear(x[-1000:].contiguous(), W))
     q = fp8_quantize(x)
     assert torch.equal(q.codes[-1000:], fp8_quantize(x[-1000:]).codes)
     del x, y, q
     x = torch.empty(70001, 32, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
     W = fp8_quantize(torch.empty(31000, 32, device=DEV).normal_(generator=g), 128)
     y = fp8_linear(x, W)
-    assert torch.equal(y[-200:], fp8_linear(x[-200:].contiguous(), W))
+    assert near(y[-200:], fp8_linear(x[-200:].contiguous(), W))
 
 
 def test_runs_repeat_and_replay():

@@ -73,9 +73,10 @@ def test_transpose_refuses():
     (dict(M=0), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(K=(1 << 22) + 1), -2), (dict(M=1 << 31), -2),
     (dict(M=1 << 30, N=1 << 30), -2), (dict(x=None), -1), (dict(sw=None), -1), (dict(out=None), -1),
     (dict(br=64), -1), (dict(od=3), -1), (dict(out=FAKE + 4), -1), (dict(bias=FAKE + 1), -1),
-    (dict(br=1, sw=FAKE + 1), -1), (dict(w=FAKE + 8), -1)])
+    (dict(br=1, sw=FAKE + 1), -1), (dict(w=FAKE + 8), -1), (dict(ws=None), -3), (dict(ws=FAKE + 8), -1),
+    (dict(M=128, N=256, K=4096, n=1 << 16), -3)])
 def test_matmul_refuses(kw, code):
-    d = dict(M=4, N=4, K=8, x=FAKE, sx=FAKE, w=FAKE, sw=FAKE, br=128, bias=None, od=1, out=FAKE)
+    d = dict(M=4, N=4, K=8, x=FAKE, sx=FAKE, w=FAKE, sw=FAKE, br=128, bias=None, od=1, out=FAKE, ws=FAKE, n=BIG)
     d.update(kw)
     _refused(code, ops.lib().mxmoe_fp8_matmul(*d.values(), None))
 
@@ -96,6 +97,16 @@ def test_linear_dw_refuses(kw, code):
     d = dict(M=4, N=4, K=8, dy=FAKE, x=FAKE, dw=FAKE, ws=FAKE, n=BIG)
     d.update(kw)
     _refused(code, ops.lib().mxmoe_fp8_linear_dw(*d.values(), None))
+
+
+def test_workspace_queries_refuse():
+    L = ops.lib()
+    assert L.mxmoe_fp8_matmul_workspace_bytes(4, 4, 8, 0) > 0 and L.mxmoe_fp8_linear_workspace_bytes(4, 4, 8, 1) > 0
+    for sizes in [(0, 4, 8), (4, 0, 8), (4, 4, 0), (4, 4, 1 << 23)]:
+        assert L.mxmoe_fp8_matmul_workspace_bytes(*sizes, 1) == 0
+        assert L.mxmoe_fp8_linear_workspace_bytes(*sizes, 1) == 0
+    assert L.mxmoe_fp8_linear_dw_workspace_bytes(1 << 23, 4, 4) == 0
+    assert L.mxmoe_fp8_matmul_workspace_bytes(4, 4, 8, 2) == 0
 
 
 @pytest.mark.parametrize("kw,code", [
