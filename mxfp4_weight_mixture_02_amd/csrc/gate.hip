@@ -23,15 +23,49 @@ __device__ __forceinline__ int32_t choice_key(float f) {
   return (f != f) ? INT32_MIN + 1 : (b ^ ((b >> 31) & 0x7FFFFFFF));
 }
 
-__device__ __forceinline__ int32_t wave_max(int32_t v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = max(v, __shfl_xor(v, m));
-  return v;
+// Exchanges within rows of 16 lanes by DPP: lanes xor 1, xor 2, mirrored
+// within 8, mirrored within 16 (a mirror does as an xor once the lanes below
+// agree); a chain of LDS shuffles takes several times the time.
+template <int STEP>
+__device__ __forceinline__ int32_t dpp_swap(int32_t v) {
+  constexpr int CTRL = STEP == 1 ? 0xB1 : STEP == 2 ? 0x4E : STEP == 4 ? 0x141 : 0x140;
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
+__device__ __forceinline__ int32_t row_max(int32_t v) {
+  v = max(v, dpp_swap<1>(v));
+  v = max(v, dpp_swap<2>(v));
+  v = max(v, dpp_swap<4>(v));
+  return max(v, dpp_swap<8>(v));
+}
+// Largest value over the wave, as a scalar: the rows joined by broadcasts
+// (row_bcast:15 into rows 1 and 3, row_bcast:31 into rows 2 and 3).
+__device__ __forceinline__ int32_t wave_max(int32_t v) {
+  v = row_max(v);
+  v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x142, 0xA, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x143, 0xC, 0xF, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+// The number a choice key stands for (a NaN key gives a NaN).
+__device__ __forceinline__ float key_number(int32_t k) {
+  return __uint_as_float((uint32_t)(k ^ ((k >> 31) & 0x7FFFFFFF)));
+}
+// The largest of the wave's floats, NaN below every number.
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+  const int32_t k = wave_max(choice_key(v));
+  return k == INT32_MIN + 1 ? -INFINITY : key_number(k);
+}
+// Sum of the first 8 lanes' values, in each of them.
+template <int STEP>
+__device__ __forceinline__ double dpp_swap(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)dpp_swap<STEP>((int32_t)(uint32_t)b);
+  const uint32_t hi = (uint32_t)dpp_swap<STEP>((int32_t)(uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+__device__ __forceinline__ double sum8(double v) {
+  v += dpp_swap<1>(v);
+  v += dpp_swap<2>(v);
+  return v + dpp_swap<4>(v);
 }
 template <class F>
 __device__ __forceinline__ F wave_sum(F v) {
@@ -73,95 +107,163 @@ __device__ __forceinline__ void token_scores(const float (&v)[NQ], int E, int la
   for (int q = 0; q < NQ; ++q) s[q] *= inv;
 }
 
-// Which groups are open to the choice, as a bit mask: lane g < groups
-// values group g from the token's choice values in LDS and counts the
-// groups that beat it.
+// Which groups are open to the choice, as a bit mask over groups.  `share`
+// (a power of two, share * groups <= 64) lanes value a group from the token's
+// choice values in LDS: each takes every share-th expert, the two largest
+// are merged over the lanes, and a group is open if fewer than top_groups
+// groups beat it.
 __device__ __forceinline__ unsigned long long open_groups(const RouteArgs& a, const float* c,
                                                           int lane) {
-  const int per = a.E / a.groups;
-  int32_t key = INT32_MIN;
-  if (lane < a.groups) {
-    const float* p = c + lane * per;
-    int32_t k1 = INT32_MIN, k2 = INT32_MIN;
-    float c1 = 0.0f, c2 = 0.0f;
-    for (int i = 0; i < per; ++i) {
-      const float v = p[i];
-      const int32_t kv = choice_key(v);
-      if (kv > k1) {
-        k2 = k1;
-        c2 = c1;
-        k1 = kv;
-        c1 = v;
-      } else if (kv > k2) {
-        k2 = kv;
-        c2 = v;
-      }
+  const int per = a.E / a.groups, share = a.share;
+  const int g = lane / share;
+  int32_t k1 = INT32_MIN, k2 = INT32_MIN;
+  float c1 = 0.0f, c2 = 0.0f;
+  auto take = [&](int32_t kv, float v) {
+    const bool first = kv > k1, second = kv > k2;
+    k2 = first ? k1 : second ? kv : k2;
+    c2 = first ? c1 : second ? v : c2;
+    k1 = first ? kv : k1;
+    c1 = first ? v : c1;
+  };
+  if (g < a.groups)
+    for (int i = lane % share; i < per; i += share) {
+      const float v = c[g * per + i];
+      take(choice_key(v), v);
     }
-    key = choice_key(a.top2 && per > 1 ? c1 + c2 : c1);
+  for (int m = 1; m < share; m <<= 1) {
+    const int32_t o1 = __shfl_xor(k1, m), o2 = __shfl_xor(k2, m);
+    const float v1 = __shfl_xor(c1, m), v2 = __shfl_xor(c2, m);
+    take(o1, v1);
+    take(o2, v2);
   }
+  const int32_t key = choice_key(a.top2 && per > 1 ? c1 + c2 : c1);
   int beaten = 0;
-  for (int g = 0; g < a.groups; ++g) {
-    const int32_t o = __shfl(key, g);
-    beaten += o > key || (o == key && g < lane);
+  for (int o = 0; o < a.groups; ++o) {
+    const int32_t ok = __builtin_amdgcn_readlane(key, o * share);
+    beaten += ok > key || (ok == key && o < g);
   }
-  return __ballot(lane < a.groups && beaten < a.top_groups);
+  const unsigned long long lanes =
+      __ballot(lane % share == 0 && g < a.groups && beaten < a.top_groups);
+  if (share == 1) return lanes;
+  unsigned long long open = 0;
+  for (int o = 0; o < a.groups; ++o) open |= ((lanes >> (o * share)) & 1ull) << o;
+  return open;
+}
+
+template <int NQ>
+struct Lane {          // what a lane holds of its experts, whatever the token
+  float bias[NQ];
+  int group[NQ];
+};
+template <int NQ>
+__device__ __forceinline__ Lane<NQ> lane_of(const RouteArgs& a, int lane) {
+  Lane<NQ> l;
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const int e = min(NQ * lane + q, a.E - 1);
+    l.bias[q] = a.bias ? a.bias[e] : 0.0f;
+    l.group[q] = e / (a.E / a.groups);
+  }
+  return l;
+}
+template <int NQ>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int lane, float (&v)[NQ]) {
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) v[q] = a.logits[t * a.E + min(NQ * lane + q, a.E - 1)];
+}
+
+// Whether this lane's group is open, where a group is `lanes` whole lanes (a
+// power of two): k1 and k2 are the largest and second keys of the lane's
+// experts.  The two largest are merged over the group's lanes, then each
+// lane counts the groups that beat its own.
+__device__ __forceinline__ bool lane_group_open(const RouteArgs& a, int lanes, int lane, int32_t k1,
+                                                int32_t k2) {
+  auto merge = [&](int32_t o1, int32_t o2) {
+    k2 = max(min(k1, o1), max(k2, o2));
+    k1 = max(k1, o1);
+  };
+  if (lanes > 1) merge(dpp_swap<1>(k1), dpp_swap<1>(k2));
+  if (lanes > 2) merge(dpp_swap<2>(k1), dpp_swap<2>(k2));
+  if (lanes > 4) merge(dpp_swap<4>(k1), dpp_swap<4>(k2));
+  if (lanes > 8) merge(dpp_swap<8>(k1), dpp_swap<8>(k2));
+  if (lanes > 16) merge(__shfl_xor(k1, 16), __shfl_xor(k2, 16));
+  const int32_t key =
+      a.top2 && a.E > a.groups ? choice_key(key_number(k1) + key_number(k2)) : k1;
+  const int g = lane / lanes;
+  int beaten = 0;
+  for (int o = 0; o < a.groups; ++o) {
+    const int32_t ok = __builtin_amdgcn_readlane(key, o * lanes);
+    beaten += ok > key - (o < g);   // an equal key of a lower group beats too
+  }
+  return beaten < a.top_groups;
 }
 
 // Chooses token t's experts: lane j < k returns slot j's expert (others 0)
-// and writes the slot's index and weight.
+// and writes the slot's index and weight.  A lane's keys are sorted once
+// (stably, so that ties stay in index order); a round takes the wave's
+// largest head, from the lowest lane that has it, and that lane moves on.
 template <int NQ>
-__device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lane, TokenLds& lds) {
-  const float* row = a.logits + t * a.E;
-  float v[NQ];
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) v[q] = row[min(NQ * lane + q, a.E - 1)];
+__device__ __forceinline__ int choose(const RouteArgs& a, const Lane<NQ>& mine_of, int64_t t, int lane,
+                                      const float (&v)[NQ], TokenLds& lds) {
   double s[NQ];
   token_scores<NQ>(v, a.E, lane, a.sigmoid, s);
+  const bool grouped = a.top_groups < a.groups;
   int32_t key[NQ];
+  int at[NQ];
   wave_lds_sync();   // the previous token's reads are done
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     const int e = NQ * lane + q;
-    const float c = (float)(a.bias ? s[q] + (double)a.bias[min(e, a.E - 1)] : s[q]);
+    const float c = (float)(s[q] + (double)mine_of.bias[q]);
     key[q] = e < a.E ? choice_key(c) : INT32_MIN;
+    at[q] = e;
     if (e < a.E) {
       lds.score[e] = s[q];
-      lds.c[e] = c;
+      if (grouped && !a.group_lanes) lds.c[e] = c;
     }
   }
   wave_lds_sync();
-  if (a.top_groups < a.groups) {
+  if (grouped && !a.group_lanes) {
     const unsigned long long open = open_groups(a, lds.c, lane);
-    const int per = a.E / a.groups;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
-      if (!((open >> min((NQ * lane + q) / per, 63)) & 1)) key[q] = INT32_MIN;
+      if (!((open >> mine_of.group[q]) & 1)) key[q] = INT32_MIN;
+  }
+#pragma unroll
+  for (int n = NQ - 1; n > 0; --n)
+#pragma unroll
+    for (int q = 0; q < n; ++q) {
+      const bool swap = key[q] < key[q + 1];
+      const int32_t kq = key[q];
+      const int aq = at[q];
+      key[q] = swap ? key[q + 1] : kq;
+      at[q] = swap ? at[q + 1] : aq;
+      key[q + 1] = swap ? kq : key[q + 1];
+      at[q + 1] = swap ? aq : at[q + 1];
+    }
+  if (grouped && a.group_lanes &&
+      !lane_group_open(a, a.group_lanes, lane, key[0], NQ > 1 ? key[NQ > 1] : INT32_MIN)) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) key[q] = INT32_MIN;
   }
   int mine = 0;
   for (int j = 0; j < a.k; ++j) {
-    int32_t best = key[0];
-#pragma unroll
-    for (int q = 1; q < NQ; ++q) best = max(best, key[q]);
-    const int32_t top = wave_max(best);
-    // the lowest lane that holds it, and its lowest such expert
-    const int owner = __builtin_ctzll(__ballot(best == top));
-    int at = 0;
-#pragma unroll
-    for (int q = NQ - 1; q >= 0; --q)
-      if (key[q] == top) at = q;
-    const int e = __builtin_amdgcn_readlane(NQ * lane + at, owner);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-      if (NQ * lane + q == e) key[q] = INT32_MIN;
+    const int32_t top = wave_max(key[0]);
+    const int owner = (int)__builtin_ctzll(__ballot(key[0] == top));
+    const int e = __builtin_amdgcn_readlane(at[0], owner);
     if (lane == j) mine = e;
+    if (lane == owner) {
+#pragma unroll
+      for (int q = 0; q + 1 < NQ; ++q) {
+        key[q] = key[q + 1];
+        at[q] = at[q + 1];
+      }
+      key[NQ - 1] = INT32_MIN;
+    }
   }
-  // weights: scores of the chosen experts, summed in slot order
+  // weights: the chosen scores, over their sum
   const double sc = lane < a.k ? lds.score[mine] : 0.0;
-  double total = 1.0;
-  if (a.renorm) {
-    total = 0.0;
-    for (int j = 0; j < a.k; ++j) total += __shfl(sc, j);
-  }
+  const double total = a.renorm ? sum8(sc) : 1.0;
   if (lane < a.k) {
     a.topk_idx[t * a.k + lane] = mine;
     a.topk_w[t * a.k + lane] = (float)(total == 0.0 ? 0.0 : sc / total * (double)a.scale);
@@ -169,24 +271,64 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lane, T
   return mine;
 }
 
-// The choice of `per_block` tokens by one workgroup of 4 waves, and the
+// The choice of `per_block` tokens by one workgroup of 16 waves, and the
 // workgroup's histogram of experts.
+constexpr int GATE_W = 16;
 template <int NQ>
-__global__ __launch_bounds__(256) void gate_kernel(RouteArgs a, int per_block,
-                                                   int32_t* __restrict__ hist_out) {
-  __shared__ TokenLds lds[4];
+__global__ __launch_bounds__(64 * GATE_W) void gate_kernel(RouteArgs a, int per_block,
+                                                           int32_t* __restrict__ hist_out) {
+  __shared__ TokenLds lds[GATE_W];
   __shared__ int32_t hist[256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  hist[tid] = 0;
+  if (tid < 256) hist[tid] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * per_block;
   const int n = (int)min((int64_t)per_block, a.T - t0);
-  for (int i = wave; i < n; i += 4) {
-    const int e = choose<NQ>(a, t0 + i, lane, lds[wave]);
+  const Lane<NQ> mine = lane_of<NQ>(a, lane);
+  float v[NQ], next[NQ];
+  load_logits<NQ>(a, t0 + min(wave, n - 1), lane, v);
+  for (int i = wave; i < n; i += GATE_W) {
+    load_logits<NQ>(a, t0 + min(i + GATE_W, n - 1), lane, next);   // the next token's, under this one's choice
+    const int e = choose<NQ>(a, mine, t0 + i, lane, v, lds[wave]);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) v[q] = next[q];
     if (lane < a.k) atomicAdd(&hist[e], 1);   // counts only: order does not matter
   }
   __syncthreads();
   if (tid < a.E) hist_out[(int64_t)blockIdx.x * a.E + tid] = hist[tid];
+}
+
+// Few tokens (T <= GATE_ONE_TOKENS): choice, offsets and permutation in one
+// workgroup.
+constexpr int GATE_ONE_TOKENS = 32;
+template <int NQ>
+__global__ __launch_bounds__(64 * GATE_W) void gate_one_kernel(RouteArgs a) {
+  __shared__ TokenLds lds[GATE_W];
+  __shared__ int32_t ex[GATE_ONE_TOKENS * 8];
+  __shared__ int32_t off[257];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Lane<NQ> mine = lane_of<NQ>(a, lane);
+  for (int t = wave; t < (int)a.T; t += GATE_W) {
+    float v[NQ];
+    load_logits<NQ>(a, t, lane, v);
+    const int e = choose<NQ>(a, mine, t, lane, v, lds[wave]);
+    if (lane < a.k) ex[t * a.k + lane] = e;
+  }
+  __syncthreads();
+  const int R = (int)a.T * a.k;
+  // rows of lower experts are before expert tid's: its offset
+  if (tid <= a.E) {
+    int n = 0;
+    for (int f = 0; f < R; ++f) n += ex[f] < tid;
+    off[tid] = n;
+    a.offsets[tid] = n;
+  }
+  __syncthreads();
+  if (tid < R) {
+    int rank = 0;
+    for (int f = 0; f < tid; ++f) rank += ex[f] == ex[tid];
+    a.sorted_rows[off[ex[tid]] + rank] = tid;
+  }
 }
 
 // Expert e = blockIdx.x: in place, hist[b][e] becomes the number of rows of
@@ -217,49 +359,60 @@ __global__ __launch_bounds__(256) void gate_prefix_kernel(int32_t* __restrict__ 
 }
 
 // Offsets from the totals, and each workgroup's rows to their places:
-// offsets[e] + rows of e in earlier workgroups + earlier rows of e here.
+// offsets[e] + rows of e in earlier workgroups + earlier rows of e here.  A
+// chunk of 256 rows at a time: within a wave, the rows of the same expert
+// come from eight ballots on the bits of its number; over the waves, from
+// counts in LDS.
 __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_block,
                                                            const int32_t* __restrict__ base,
                                                            const int32_t* __restrict__ total) {
   __shared__ int32_t off[256];
-  __shared__ int32_t ex[256];
-  const int tid = threadIdx.x;
+  __shared__ int32_t cnt[4][256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t mine = tid < a.E ? total[tid] : 0;
-  off[tid] = mine;
-  __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
-    const int32_t o = tid >= d ? off[tid - d] : 0;
-    __syncthreads();
-    off[tid] += o;
-    __syncthreads();
+  const int32_t before = tid < a.E ? base[(int64_t)blockIdx.x * a.E + tid] : 0;
+  // exclusive sum of the totals: within a wave by shuffles, over waves by LDS
+  int32_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
   }
-  const int32_t start = off[tid] - mine;
+  if (lane == 63) cnt[0][wave] = inc;
+  __syncthreads();
+  int32_t start = inc - mine;
+  for (int w = 0; w < wave; ++w) start += cnt[0][w];
   if (blockIdx.x == 0) {
     if (tid < a.E) a.offsets[tid] = start;
-    if (tid == a.E - 1) a.offsets[a.E] = off[tid];
+    if (tid == a.E - 1) a.offsets[a.E] = start + mine;
   }
-  __syncthreads();
-  if (tid < a.E) off[tid] = start + base[(int64_t)blockIdx.x * a.E + tid];
+  off[tid] = start + before;
   const int64_t f0 = (int64_t)blockIdx.x * per_block * a.k;
   const int n = (int)min((int64_t)per_block * a.k, a.T * a.k - f0);
   for (int c0 = 0; c0 < n; c0 += 256) {
     const int i = c0 + tid;
-    const int e = i < n ? a.topk_idx[f0 + i] : -1;
+    const bool live = i < n;
+    const int e = live ? a.topk_idx[f0 + i] : 0;
+    unsigned long long same = __ballot(live);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const unsigned long long m = __ballot((e >> b) & 1);
+      same &= (e >> b) & 1 ? m : ~m;
+    }
+    __syncthreads();   // off is there; the counts of the chunk before are used up
+#pragma unroll
+    for (int w = 0; w < 4; ++w) cnt[w][tid] = 0;
     __syncthreads();
-    ex[tid] = e;
+    const int rank = __popcll(same & ((1ull << lane) - 1ull));
+    if (live && rank == 0) cnt[wave][e] = __popcll(same);
     __syncthreads();
-    if (e >= 0) {
-      int rank = 0;
-      for (int j = 0; j < tid; ++j) rank += ex[j] == e;
-      a.sorted_rows[off[e] + rank] = (int32_t)(f0 + i);
+    if (live) {
+      int32_t p = off[e] + rank;
+      for (int w = 0; w < wave; ++w) p += cnt[w][e];
+      a.sorted_rows[p] = (int32_t)(f0 + i);
     }
     __syncthreads();
-    // the chunk's counts move the places on (one thread per expert)
-    if (c0 + 256 < n && tid < a.E) {
-      int cnt = 0;
-      for (int j = 0; j < 256; ++j) cnt += ex[j] == tid;
-      off[tid] += cnt;
-    }
+    off[tid] += cnt[0][tid] + cnt[1][tid] + cnt[2][tid] + cnt[3][tid];
   }
 }
 
@@ -310,21 +463,36 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
   }
 }
 
-// Tokens per workgroup: the plan has one histogram row for each workgroup.
-static int gate_tokens(int64_t T) { return T <= 4096 ? 16 : 64; }
+// Tokens per workgroup of the choice, which has a histogram row for each: a
+// wave takes one token while that gives at most four waves a SIMD, then 4, 8
+// or 16 (16384 tokens x 256 experts: 4; with one wave a SIMD, 16 each, the
+// first form of the choice took 120 us against 34).
+static int gate_tokens(int64_t T) {
+  const int64_t per_wave = (T + 4095) / 4096;
+  return GATE_W * (int)(per_wave < 16 ? per_wave : 16);
+}
 
 int64_t gate_blocks(int64_t T) { return (T + gate_tokens(T) - 1) / gate_tokens(T); }
+bool gate_in_one(int64_t T) { return T <= GATE_ONE_TOKENS; }
+
+#define GATE_LAUNCH(kernel, ...)                         \
+  do {                                                   \
+    if (a.E <= 64)                                       \
+      hipLaunchKernelGGL(kernel<1>, __VA_ARGS__);        \
+    else if (a.E <= 128)                                 \
+      hipLaunchKernelGGL(kernel<2>, __VA_ARGS__);        \
+    else                                                 \
+      hipLaunchKernelGGL(kernel<4>, __VA_ARGS__);        \
+    return hipGetLastError();                            \
+  } while (0)
+
+hipError_t launch_gate_one(const RouteArgs& a, hipStream_t s) {
+  GATE_LAUNCH(gate_one_kernel, dim3(1), dim3(64 * GATE_W), 0, s, a);
+}
 
 hipError_t launch_gate(const RouteArgs& a, int32_t* hist, hipStream_t s) {
-  const int per = gate_tokens(a.T);
-  const dim3 grid((unsigned)gate_blocks(a.T)), block(256);
-  if (a.E <= 64)
-    hipLaunchKernelGGL(gate_kernel<1>, grid, block, 0, s, a, per, hist);
-  else if (a.E <= 128)
-    hipLaunchKernelGGL(gate_kernel<2>, grid, block, 0, s, a, per, hist);
-  else
-    hipLaunchKernelGGL(gate_kernel<4>, grid, block, 0, s, a, per, hist);
-  return hipGetLastError();
+  GATE_LAUNCH(gate_kernel, dim3((unsigned)gate_blocks(a.T)), dim3(64 * GATE_W), 0, s, a,
+              gate_tokens(a.T), hist);
 }
 
 hipError_t launch_gate_prefix(const RouteArgs& a, int32_t* hist, int32_t* total, hipStream_t s) {
@@ -342,14 +510,7 @@ hipError_t launch_gate_scatter(const RouteArgs& a, const int32_t* base, const in
 
 hipError_t launch_gate_bwd(const RouteArgs& a, const int32_t* idx, const float* dw, float* dlogits,
                            hipStream_t s) {
-  const dim3 grid((unsigned)((a.T + 3) / 4)), block(256);
-  if (a.E <= 64)
-    hipLaunchKernelGGL(gate_bwd_kernel<1>, grid, block, 0, s, a, idx, dw, dlogits);
-  else if (a.E <= 128)
-    hipLaunchKernelGGL(gate_bwd_kernel<2>, grid, block, 0, s, a, idx, dw, dlogits);
-  else
-    hipLaunchKernelGGL(gate_bwd_kernel<4>, grid, block, 0, s, a, idx, dw, dlogits);
-  return hipGetLastError();
+  GATE_LAUNCH(gate_bwd_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, idx, dw, dlogits);
 }
 
 }  // namespace mxmoe

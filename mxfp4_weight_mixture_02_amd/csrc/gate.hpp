@@ -10,6 +10,8 @@ struct RouteArgs {
   int64_t T;
   int E, k;
   int groups, top_groups;   // top_groups == groups: no groups
+  int share;                // lanes that value a group: a power of two, share * groups <= 64
+  int group_lanes;          // lanes whose experts are a whole group, if a power of two, else 0
   int sigmoid, top2, renorm;
   float scale;
   const float* logits;      // [T, E]
@@ -20,10 +22,13 @@ struct RouteArgs {
   int32_t* sorted_rows;     // [T * k]
 };
 
-// The choice and each workgroup's histogram [gate_blocks(T), E]; then in
+// Few tokens (gate_in_one): all in one launch, without workspace.  Else: the
+// choice and each workgroup's histogram [gate_blocks(T), E]; then in
 // place the rows of earlier workgroups, with the totals [E]; then offsets
 // and permutation.
+bool gate_in_one(int64_t T);
 int64_t gate_blocks(int64_t T);
+hipError_t launch_gate_one(const RouteArgs& a, hipStream_t s);
 hipError_t launch_gate(const RouteArgs& a, int32_t* hist, hipStream_t s);
 hipError_t launch_gate_prefix(const RouteArgs& a, int32_t* hist, int32_t* total, hipStream_t s);
 hipError_t launch_gate_scatter(const RouteArgs& a, const int32_t* base, const int32_t* total,

@@ -66,6 +66,12 @@ mxmoe::RouteArgs route_args(const mxmoe_route_opts& o, int64_t T, int32_t E, int
   a.k = k;
   a.groups = o.groups;
   a.top_groups = o.top_groups;
+  a.share = 1;
+  while (2 * a.share * o.groups <= 64) a.share *= 2;
+  // the choice gives a lane ceil(E / 64) experts, as 1, 2 or 4
+  const int each = E <= 64 ? 1 : E <= 128 ? 2 : 4, per = E / o.groups;
+  const int lanes = per % each == 0 ? per / each : 0;
+  a.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
   a.sigmoid = o.score == MXMOE_SCORE_SIGMOID;
   a.top2 = o.group_score == MXMOE_GROUP_TOP2;
   a.renorm = o.renorm != 0;
@@ -170,6 +176,10 @@ int mxmoe_route(const mxmoe_route_opts* opts, int64_t T, int32_t E, int32_t k, c
   int32_t* hist = static_cast<int32_t*>(workspace);
   int32_t* total = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) +
                                               up((size_t)mxmoe::gate_blocks(T) * E * 4, ALIGN));
+  if (mxmoe::gate_in_one(T)) {
+    LAUNCH(mxmoe::launch_gate_one(a, s), "gate");
+    return ok();
+  }
   LAUNCH(mxmoe::launch_gate(a, hist, s), "gate");
   LAUNCH(mxmoe::launch_gate_prefix(a, hist, total, s), "gate_prefix");
   LAUNCH(mxmoe::launch_gate_scatter(a, hist, total, s), "gate_scatter");
