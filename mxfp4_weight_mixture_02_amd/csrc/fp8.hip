@@ -631,17 +631,60 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm g, int splits) {
 }
 
 // Few rows: a workgroup takes 16 rows of W and its waves split the K blocks;
-// every wave streams its part of W straight into fragments (a lane 32 bytes
-// of its row, a wave 16 whole 128-byte lines) and the partial sums meet in
-// LDS in wave order.  All loads of SK_CH K blocks are issued before the
-// first product, X's before W's, so a chunk costs one memory round trip.
-// FUSED: X comes as bf16 and is rounded to E4M3 in the lane that feeds it to
-// the matrix core: the lane's 32 elements, the block's largest magnitude
-// from the four lanes that share the row.
+// every wave streams its part of W straight into fragments and the partial
+// sums meet in LDS in wave order.  Lane (r, q) takes bytes 16 q .. + 15 and
+// 64 + 16 q .. + 15 of its row's block, of W and of X alike, so a load
+// instruction brings 64 contiguous bytes of each of 16 rows.
 constexpr int SK_NW = 8, SK_CH = 3;   // waves; K blocks in flight per wave
 
-template <int FM, bool WROWS, bool F32, bool FUSED, bool VEC>
-__global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g, const uint16_t* __restrict__ xb) {
+// W's fragments and scales of K blocks c0 .. c0 + SK_CH - 1 (past b1 - 1: that
+// block again, not multiplied).
+struct SkinnyW {
+  u32x4 lo[SK_CH], hi[SK_CH];
+  uint32_t s[SK_CH];
+};
+__device__ __forceinline__ void skinny_load(const uint8_t* w, const uint8_t* sw, int64_t swp, int c0,
+                                            int b1, SkinnyW& f) {
+#pragma unroll
+  for (int u = 0; u < SK_CH; ++u) {
+    const int64_t kb = min(c0 + u, b1 - 1);
+    f.lo[u] = gload16(w + kb * 128);
+    f.hi[u] = gload16(w + kb * 128 + 64);
+    f.s[u] = sw[kb * swp];
+  }
+}
+template <bool F32>
+__device__ __forceinline__ f32x4 skinny_product(const u32x4& wl, const u32x4& wh, uint32_t sw,
+                                                const u32x4& xl, const u32x4& xh, uint32_t sx, f32x4 acc) {
+  const i32x8 a = {(int)wl[0], (int)wl[1], (int)wl[2], (int)wl[3], (int)wh[0], (int)wh[1], (int)wh[2], (int)wh[3]};
+  const i32x8 b = {(int)xl[0], (int)xl[1], (int)xl[2], (int)xl[3], (int)xh[0], (int)xh[1], (int)xh[2], (int)xh[3]};
+  if (!F32) return fp8_mfma<0, 0>(a, b, acc, (int)sw, (int)sx);
+  bf16x8 av[4], bv[4];
+  fp8_to_bf16(a, sw, av);
+  fp8_to_bf16(b, sx, bv);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[t], bv[t], acc, 0, 0, 0);
+  return acc;
+}
+// The waves' sums in their order, plus the bias, to rows 16 j .. of out.
+// Lane l holds D rows 4 (l / 16) .. + 3 (n) of column l % 16 (m).
+template <int FM, bool F32>
+__device__ __forceinline__ void skinny_store(const Fp8Gemm& g, f32x4 (*part)[FM][64], int64_t n0, int wave,
+                                             int lane) {
+  const bool wide = g.N % 4 == 0;
+  for (int j = wave; j < FM; j += SK_NW) {
+    f32x4 sum = part[0][j][lane];
+#pragma unroll
+    for (int u = 1; u < SK_NW; ++u) sum += part[u][j][lane];
+    float o[4] = {sum[0], sum[1], sum[2], sum[3]};
+    fp8_store<4, F32>(g, 16 * j + (lane & 15), n0 + 4 * (lane >> 4), o, wide);
+  }
+}
+
+// 8-bit X, up to 16 FM rows: X's fragments come straight from memory too,
+// all loads of SK_CH K blocks before the first product.
+template <int FM, bool WROWS, bool F32>
+__global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g) {
   __shared__ f32x4 part[SK_NW][FM][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, q = lane >> 4;
@@ -650,7 +693,7 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g, const
   const int kblocks = (int)(pitch / 128);
   const int b0 = wave * kblocks / SK_NW, b1 = (wave + 1) * kblocks / SK_NW;
   const int64_t n = min(n0 + r, g.N - 1);
-  const uint8_t* w = g.w + n * pitch + 32 * q;
+  const uint8_t* w = g.w + n * pitch + 16 * q;
   const int64_t sxp = fp8_scale_pitch(g.M);
   const int64_t swp = WROWS ? fp8_scale_pitch(g.N) : (g.N + 127) / 128;
   const uint8_t* sw = g.sw + (WROWS ? n : n / 128);
@@ -658,105 +701,121 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g, const
 #pragma unroll
   for (int j = 0; j < FM; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int c0 = b0; c0 < b1; c0 += SK_CH) {
-    // blocks past the wave's last repeat it and are not multiplied
-    u32x4 wl[SK_CH], wh[SK_CH], xr[SK_CH][FM][FUSED ? 4 : 2];
-    uint32_t s[SK_CH], sx[SK_CH][FM];
+    u32x4 xl[SK_CH][FM], xh[SK_CH][FM];
+    uint32_t sx[SK_CH][FM];
 #pragma unroll
     for (int u = 0; u < SK_CH; ++u) {
       const int64_t kb = min(c0 + u, b1 - 1);
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
         const int64_t m = min((int64_t)(16 * j + r), g.M - 1);
-        if (FUSED && VEC) {
-          const int64_t k0 = kb * 128 + 32 * q;
-#pragma unroll
-          for (int p = 0; p < 4; ++p)   // past K: the row's last elements, zeroed below
-            xr[u][j][p] = gload16(xb + m * g.K + min(k0 + 8 * p, g.K - 8));
-        } else if (!FUSED) {
-          xr[u][j][0] = gload16(g.x + m * pitch + kb * 128 + 32 * q);
-          xr[u][j][1] = gload16(g.x + m * pitch + kb * 128 + 32 * q + 16);
-          sx[u][j] = g.sx[kb * sxp + m];
-        }
+        xl[u][j] = gload16(g.x + m * pitch + kb * 128 + 16 * q);
+        xh[u][j] = gload16(g.x + m * pitch + kb * 128 + 16 * q + 64);
+        sx[u][j] = g.sx[kb * sxp + m];
       }
     }
-#pragma unroll
-    for (int u = 0; u < SK_CH; ++u) {
-      const int64_t kb = min(c0 + u, b1 - 1);
-      wl[u] = gload16(w + kb * 128);
-      wh[u] = gload16(w + kb * 128 + 16);
-      s[u] = sw[kb * swp];
-    }
+    SkinnyW f;
+    skinny_load(w, sw, swp, c0, b1, f);
 #pragma unroll
     for (int u = 0; u < SK_CH; ++u) {
       if (c0 + u >= b1) continue;
-      const int64_t kb = c0 + u;
-      const i32x8 a = {(int)wl[u][0], (int)wl[u][1], (int)wl[u][2], (int)wl[u][3],
-                       (int)wh[u][0], (int)wh[u][1], (int)wh[u][2], (int)wh[u][3]};
 #pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        i32x8 b;
-        uint32_t sb;
-        if (FUSED) {
-          const int64_t k0 = kb * 128 + 32 * q;
-          float v[4][8];
-          uint32_t top = 0;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            if (VEC) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t h = xr[u][j][p][i >> 1];
-                v[p][i] = k0 + 8 * p < g.K ? __uint_as_float((i & 1) ? h & 0xFFFF0000u : h << 16) : 0.0f;
-              }
-            } else {
-              const int64_t m = min((int64_t)(16 * j + r), g.M - 1);
-              load8<false, false>(xb, m * g.K + k0 + 8 * p, g.K - k0 - 8 * p, v[p]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(top, finite_bits(v[p][i]));
-          }
-          top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-          top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-          const int e = e4m3_exponent(top);
-          const float f = e4m3_inverse(e);
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] = nan_unless_finite(v[p][i]) * f;
-            b[2 * p] = (int)e4m3_pack4(v[p][0], v[p][1], v[p][2], v[p][3]);
-            b[2 * p + 1] = (int)e4m3_pack4(v[p][4], v[p][5], v[p][6], v[p][7]);
-          }
-          sb = (uint32_t)(e + 127);
-        } else {
-          const u32x4 xl = xr[u][j][0], xh = xr[u][j][1];
-          b = i32x8{(int)xl[0], (int)xl[1], (int)xl[2], (int)xl[3], (int)xh[0], (int)xh[1], (int)xh[2], (int)xh[3]};
-          sb = sx[u][j];
-        }
-        if (F32) {
-          bf16x8 av[4], bv[4];
-          fp8_to_bf16(a, s[u], av);
-          fp8_to_bf16(b, sb, bv);
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[t], bv[t], acc[j], 0, 0, 0);
-        } else {
-          acc[j] = fp8_mfma<0, 0>(a, b, acc[j], (int)s[u], (int)sb);
-        }
-      }
+      for (int j = 0; j < FM; ++j)
+        acc[j] = skinny_product<F32>(f.lo[u], f.hi[u], f.s[u], xl[u][j], xh[u][j], sx[u][j], acc[j]);
     }
   }
 #pragma unroll
   for (int j = 0; j < FM; ++j) part[wave][j][lane] = acc[j];
   __syncthreads();
-  // lane l holds D rows 4 (l / 16) .. + 3 (n) of column l % 16 (m)
-  const bool wide = g.N % 4 == 0;
-  for (int j = wave; j < FM; j += SK_NW) {
-    f32x4 sum = part[0][j][lane];
+  skinny_store<FM, F32>(g, part, n0, wave, lane);
+}
+
+// bf16 X of up to 16 rows, rounded to E4M3 here: every workgroup rounds all
+// of X into LDS (16 lanes a block, 8 elements a lane), while its first W
+// loads are under way.  Rounding in the lanes that feed the matrix core
+// instead repeated it for the 16 columns, and was most of the time at one
+// row.  LDS row kb * M + m holds row m's block kb, 16-byte chunk c at slot c
+// ^ (m % 8).
+constexpr int FUSED_BYTES = 32768, FUSED_ROUNDS = FUSED_BYTES / 8 / (64 * SK_NW);
+
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(64 * SK_NW) void fp8_fused_kernel(Fp8Gemm g, const uint16_t* __restrict__ xb) {
+  __shared__ __align__(16) uint8_t xs[FUSED_BYTES];
+  __shared__ uint8_t sxs[FUSED_BYTES / 128];
+  __shared__ f32x4 part[SK_NW][1][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t pitch = fp8_pitch(g.K);
+  const int M = (int)g.M, kblocks = (int)(pitch / 128);
+  const int b0 = wave * kblocks / SK_NW, b1 = (wave + 1) * kblocks / SK_NW;
+  const int64_t n = min(n0 + r, g.N - 1);
+  const uint8_t* w = g.w + n * pitch + 16 * q;
+  const int64_t swp = (g.N + 127) / 128;
+  const uint8_t* sw = g.sw + n / 128;
+  // the 8 elements of X of each of this thread's turns, then W's first chunk
+  const int groups = M * kblocks * 16, turns = (groups + 64 * SK_NW - 1) / (64 * SK_NW);   // turns <= FUSED_ROUNDS
+  u32x4 xv[FUSED_ROUNDS];
+  if (VEC) {
 #pragma unroll
-    for (int u = 1; u < SK_NW; ++u) sum += part[u][j][lane];
-    float o[4] = {sum[0], sum[1], sum[2], sum[3]};
-    fp8_store<4, F32>(g, 16 * j + r, n0 + 4 * q, o, wide);
+    for (int u = 0; u < FUSED_ROUNDS; ++u) {
+      if (u >= turns) break;
+      const int id = min(tid + u * 64 * SK_NW, groups - 1), row = id >> 4;
+      const int64_t k0 = (int64_t)(row / M) * 128 + 8 * (id & 15);
+      xv[u] = gload16(xb + (int64_t)(row % M) * g.K + min(k0, g.K - 8));   // past K: zeroed below
+    }
   }
+  SkinnyW f;
+  if (b0 < b1) skinny_load(w, sw, swp, b0, b1, f);
+#pragma unroll
+  for (int u = 0; u < FUSED_ROUNDS; ++u) {
+    if (u >= turns) break;
+    const int id = min(tid + u * 64 * SK_NW, groups - 1), row = id >> 4, l = id & 15, m = row % M;
+    const int64_t k0 = (int64_t)(row / M) * 128 + 8 * l;
+    float v[8];
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t h = xv[u][i >> 1];
+        v[i] = k0 < g.K ? __uint_as_float((i & 1) ? h & 0xFFFF0000u : h << 16) : 0.0f;
+      }
+    } else {
+      load8<false, false>(xb, m * g.K + k0, g.K - k0, v);
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, finite_bits(v[i]));
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    const int e = e4m3_exponent(top);
+    const float k = e4m3_inverse(e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = nan_unless_finite(v[i]) * k;
+    // (a clamped id writes the last group's bytes again)
+    *reinterpret_cast<u32x2*>(xs + row * 128 + (((l >> 1) ^ (m & 7)) << 4) + 8 * (l & 1)) =
+        u32x2{e4m3_pack4(v[0], v[1], v[2], v[3]), e4m3_pack4(v[4], v[5], v[6], v[7])};
+    if (l == 0) sxs[row] = (uint8_t)(e + 127);
+  }
+  wave_lds_sync();
+  barrier_only();   // leaves W's loads under way
+  const int m = min(r, M - 1);
+  const uint8_t* x = xs + m * 128;
+  const int s0 = (q ^ (m & 7)) << 4, s1 = ((q + 4) ^ (m & 7)) << 4;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c0 = b0; c0 < b1; c0 += SK_CH) {
+    if (c0 > b0) skinny_load(w, sw, swp, c0, b1, f);
+#pragma unroll
+    for (int u = 0; u < SK_CH; ++u) {
+      const int kb = c0 + u;
+      if (kb >= b1) continue;
+      const u32x4 xl = *reinterpret_cast<const u32x4*>(x + kb * M * 128 + s0);
+      const u32x4 xh = *reinterpret_cast<const u32x4*>(x + kb * M * 128 + s1);
+      acc = skinny_product<F32>(f.lo[u], f.hi[u], f.s[u], xl, xh, sxs[kb * M + m], acc);
+    }
+  }
+  part[wave][0][lane] = acc;
+  __syncthreads();
+  skinny_store<1, F32>(g, part, n0, wave, lane);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -828,17 +887,16 @@ static hipError_t gemm_tile(const Fp8Gemm& g, int splits, hipStream_t s) {
 template <int FM>
 static hipError_t skinny(const Fp8Gemm& g, hipStream_t s) {
   const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * SK_NW);
-  const uint16_t* none = nullptr;
   if (g.w_rows) {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, true, true, false, true>), grid, block, 0, s, g, none);
+      hipLaunchKernelGGL((fp8_skinny_kernel<FM, true, true>), grid, block, 0, s, g);
     else
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, true, false, false, true>), grid, block, 0, s, g, none);
+      hipLaunchKernelGGL((fp8_skinny_kernel<FM, true, false>), grid, block, 0, s, g);
   } else {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, false, true, false, true>), grid, block, 0, s, g, none);
+      hipLaunchKernelGGL((fp8_skinny_kernel<FM, false, true>), grid, block, 0, s, g);
     else
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, false, false, false, true>), grid, block, 0, s, g, none);
+      hipLaunchKernelGGL((fp8_skinny_kernel<FM, false, false>), grid, block, 0, s, g);
   }
   return hipGetLastError();
 }
@@ -930,21 +988,23 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-bool fp8_fused_fits(int64_t M, int64_t K) { return M <= 16; }
+// X's codes fit the LDS of the one-launch form.
+bool fp8_fused_fits(int64_t M, int64_t K) { return M <= 16 && M * fp8_pitch(K) <= FUSED_BYTES; }
 
 hipError_t launch_fp8_fused(const Fp8Gemm& g, const uint16_t* x, hipStream_t s) {
+  if (!fp8_fused_fits(g.M, g.K)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * SK_NW);
   const bool vec = g.K % 8 == 0 && (reinterpret_cast<uintptr_t>(x) % 16) == 0;
   if (g.out_f32) {
     if (vec)
-      hipLaunchKernelGGL((fp8_skinny_kernel<1, false, true, true, true>), grid, block, 0, s, g, x);
+      hipLaunchKernelGGL((fp8_fused_kernel<true, true>), grid, block, 0, s, g, x);
     else
-      hipLaunchKernelGGL((fp8_skinny_kernel<1, false, true, true, false>), grid, block, 0, s, g, x);
+      hipLaunchKernelGGL((fp8_fused_kernel<true, false>), grid, block, 0, s, g, x);
   } else {
     if (vec)
-      hipLaunchKernelGGL((fp8_skinny_kernel<1, false, false, true, true>), grid, block, 0, s, g, x);
+      hipLaunchKernelGGL((fp8_fused_kernel<false, true>), grid, block, 0, s, g, x);
     else
-      hipLaunchKernelGGL((fp8_skinny_kernel<1, false, false, true, false>), grid, block, 0, s, g, x);
+      hipLaunchKernelGGL((fp8_fused_kernel<false, false>), grid, block, 0, s, g, x);
   }
   return hipGetLastError();
 }

@@ -7,6 +7,8 @@
 // c = fp32(s + bias), so that neighbours in the order do not change places
 // with the rounding of an fp32 exponential.  The k largest come from k
 // rounds of a wave maximum over integer keys.
+#include <type_traits>
+
 #include "common.hpp"
 #include "gate.hpp"
 #include "launch.hpp"
@@ -67,11 +69,24 @@ __device__ __forceinline__ double sum8(double v) {
   v += dpp_swap<2>(v);
   return v + dpp_swap<4>(v);
 }
-template <class F>
-__device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+// Sum over the wave, in every lane.
+__device__ __forceinline__ double wave_sum(double v) {
+  v = sum8(v);
+  v += dpp_swap<8>(v);
+  auto bcast = [](double x, auto ctrl, auto rows) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, decltype(ctrl)::value,
+                                                              decltype(rows)::value, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), decltype(ctrl)::value,
+                                                              decltype(rows)::value, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+  };
+  v += bcast(v, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+  v += bcast(v, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
 
 // LDS of one wave's token.
@@ -362,15 +377,45 @@ __global__ __launch_bounds__(256) void gate_prefix_kernel(int32_t* __restrict__ 
 // offsets[e] + rows of e in earlier workgroups + earlier rows of e here.  A
 // chunk of 256 rows at a time: within a wave, the rows of the same expert
 // come from eight ballots on the bits of its number; over the waves, from
-// counts in LDS.
+// counts in LDS.  base and total are gate_prefix_kernel's, or with total ==
+// nullptr base holds the workgroups' histograms and every workgroup adds up
+// the few there are (2048 tokens: one launch less, 3 us of host time).
 __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_block,
                                                            const int32_t* __restrict__ base,
                                                            const int32_t* __restrict__ total) {
   __shared__ int32_t off[256];
   __shared__ int32_t cnt[4][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int32_t mine = tid < a.E ? total[tid] : 0;
-  const int32_t before = tid < a.E ? base[(int64_t)blockIdx.x * a.E + tid] : 0;
+  int32_t mine = 0, before = 0;
+  if (total) {
+    mine = tid < a.E ? total[tid] : 0;
+    before = tid < a.E ? base[(int64_t)blockIdx.x * a.E + tid] : 0;
+  } else {
+    // thread (c, e) adds workgroups c, c + C, ... of expert e
+    const int C = 256 / a.E, c = tid / a.E, e = tid % a.E, nblk = gridDim.x;
+    cnt[0][tid] = cnt[1][tid] = 0;
+    __syncthreads();
+    if (c < C) {
+      int32_t all = 0, early = 0;
+      for (int b0 = c; b0 < nblk; b0 += 8 * C) {
+        int32_t v[8];   // eight loads under way
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = base[(int64_t)min(b0 + u * C, nblk - 1) * a.E + e];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int b = b0 + u * C;
+          all += b < nblk ? v[u] : 0;
+          early += b < (int)blockIdx.x ? v[u] : 0;
+        }
+      }
+      atomicAdd(&cnt[0][e], all);   // whole numbers: order does not matter
+      atomicAdd(&cnt[1][e], early);
+    }
+    __syncthreads();
+    mine = cnt[0][tid];
+    before = cnt[1][tid];
+    __syncthreads();
+  }
   // exclusive sum of the totals: within a wave by shuffles, over waves by LDS
   int32_t inc = mine;
 #pragma unroll
@@ -442,16 +487,20 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
   const double sc = on ? lds[wave].score[e] : 0.0;
   double ds = on ? (double)a.scale * (double)dw[t * a.k + lane] : 0.0;
   if (a.renorm) {
-    const double total = wave_sum(sc), dot = wave_sum(ds * sc);
+    const double total = sum8(sc), dot = sum8(ds * sc);   // slots are the first 8 lanes
     ds = on && total != 0.0 ? (ds - dot / total) / total : 0.0;
   }
-  const double mean = a.sigmoid ? 0.0 : wave_sum(ds * sc);
+  const double mean = a.sigmoid ? 0.0 : wave_sum(ds * sc);   // 0 past the slots
   double g[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) g[q] = 0.0;
+  const int ej_of = on ? e : -1;
+  const uint64_t ds_bits = __builtin_bit_cast(uint64_t, ds);
   for (int j = 0; j < a.k; ++j) {
-    const int ej = __shfl(on ? e : -1, j);
-    const double dj = __shfl(ds, j);
+    const int ej = __builtin_amdgcn_readlane(ej_of, j);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)ds_bits, j);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(ds_bits >> 32), j);
+    const double dj = __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 #pragma unroll
     for (int q = 0; q < NQ; ++q) g[q] += NQ * lane + q == ej ? dj : 0.0;
   }
@@ -473,6 +522,7 @@ static int gate_tokens(int64_t T) {
 }
 
 int64_t gate_blocks(int64_t T) { return (T + gate_tokens(T) - 1) / gate_tokens(T); }
+bool gate_adds(int64_t T) { return gate_blocks(T) <= 128; }
 bool gate_in_one(int64_t T) { return T <= GATE_ONE_TOKENS; }
 
 #define GATE_LAUNCH(kernel, ...)                         \

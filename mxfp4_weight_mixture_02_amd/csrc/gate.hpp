@@ -27,6 +27,7 @@ struct RouteArgs {
 // place the rows of earlier workgroups, with the totals [E]; then offsets
 // and permutation.
 bool gate_in_one(int64_t T);
+bool gate_adds(int64_t T);   // few workgroups: the scatter adds up their histograms itself
 int64_t gate_blocks(int64_t T);
 hipError_t launch_gate_one(const RouteArgs& a, hipStream_t s);
 hipError_t launch_gate(const RouteArgs& a, int32_t* hist, hipStream_t s);

@@ -120,7 +120,11 @@ struct Fp8Layout {
   size_t xs, w, ws, part, total;
 };
 Fp8Layout fp8_layout(int64_t M, int64_t N, int64_t K, bool w, int out_f32) {
-  Fp8Layout L;
+  Fp8Layout L{};
+  if (!w && mxmoe::fp8_fused_fits(M, K)) {   // X never leaves the product's launch
+    L.total = ALIGN;
+    return L;
+  }
   const size_t kb = (size_t)mxmoe::fp8_pitch(K) / 128;
   L.xs = up((size_t)M * mxmoe::fp8_pitch(K), ALIGN);
   L.w = L.xs + up(kb * mxmoe::fp8_scale_pitch(M), ALIGN);
@@ -152,6 +156,7 @@ extern "C" {
 size_t mxmoe_route_workspace_bytes(int64_t T, int32_t E, int32_t k) {
   if (check_route_sizes(T, E, k) != MXFP4_OK) return 0;
   ok();
+  if (mxmoe::gate_in_one(T)) return ALIGN;
   return up((size_t)mxmoe::gate_blocks(T) * E * 4, ALIGN) + up((size_t)E * 4, ALIGN);
 }
 
@@ -181,7 +186,10 @@ int mxmoe_route(const mxmoe_route_opts* opts, int64_t T, int32_t E, int32_t k, c
     return ok();
   }
   LAUNCH(mxmoe::launch_gate(a, hist, s), "gate");
-  LAUNCH(mxmoe::launch_gate_prefix(a, hist, total, s), "gate_prefix");
+  if (mxmoe::gate_adds(T))
+    total = nullptr;
+  else
+    LAUNCH(mxmoe::launch_gate_prefix(a, hist, total, s), "gate_prefix");
   LAUNCH(mxmoe::launch_gate_scatter(a, hist, total, s), "gate_scatter");
   return ok();
 }

@@ -15,7 +15,7 @@ from dataclasses import dataclass
 import torch
 
 from . import native
-from .native import Dims, Grads, MoeLayer, Mxfp4Error, Saved, SavedState, Weights, _shape
+from .native import Dims, Grads, MoeLayer, Mxfp4Error, Saved, SavedState, Weights
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"max": 0, "top2": 1}
@@ -66,13 +66,24 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def _shape(t, shape, dtype, name, optional=False):
+    """Refuse a tensor whose shape or dtype differs from what the C ABI will
+    assume; before the device checks, and on any device."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
 def _same_device(**tensors):
     """Every tensor contiguous and on one GPU; returns that device."""
     dev = None
     for name, t in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda or not t.is_contiguous():
+        if not (t.is_cuda and t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
         if dev is None:
             dev = t.device
@@ -81,14 +92,24 @@ def _same_device(**tensors):
     return dev
 
 
+_functions = {}
+
+
+def _function(name):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    return f
+
+
 def _call(name, dev, *args):
-    """lib().<name>(*args, stream) on dev and its current stream."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    """<name>(*args, stream) on dev and its current stream."""
+    fn, index = _function(name), dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != native.MXFP4_OK:
         raise Mxfp4Error(name, rc, lib().mxfp4_last_error().decode())
 
@@ -98,10 +119,27 @@ def _p(t):
 
 
 def _bytes_needed(name, *args):
-    n = getattr(lib(), name)(*args)
+    n = _function(name)(*args)
     if n == 0:
         raise Mxfp4Error(name, -1, lib().mxfp4_last_error().decode())
     return n
+
+
+_unused = {}
+
+
+def _workspace(name, dev, *args):
+    """(scratch for the call, its bytes).  Up to 256 bytes are never used (a
+    call that needs no scratch asks for them), so one tensor serves all."""
+    n = _bytes_needed(name, *args)
+    if n > 256:
+        return torch.empty(n, dtype=torch.uint8, device=dev), n
+    t = _unused.get(dev)
+    if t is None:
+        t = torch.empty(256, dtype=torch.uint8, device=dev)
+        if not torch.cuda.is_current_stream_capturing():   # a graph's memory is the graph's
+            _unused[dev] = t
+    return t, n
 
 
 # ---------------------------------------------------------------- routing
@@ -150,11 +188,10 @@ def moe_route(logits: torch.Tensor, k: int, options: RouteOptions = RouteOptions
     T, E = _logits(logits)
     _shape(bias, (E,), torch.float32, "bias", optional=True)
     dev = _same_device(logits=logits, bias=bias)
-    nbytes = _bytes_needed("mxmoe_route_workspace_bytes", T, E, k)
+    ws, nbytes = _workspace("mxmoe_route_workspace_bytes", dev, T, E, k)
     i32 = dict(dtype=torch.int32, device=dev)
     r = Routing(torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev),
                 torch.empty(E + 1, **i32), torch.empty(T * k, **i32))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call("mxmoe_route", dev, options.struct, T, E, k, _p(logits), _p(bias), _p(r.topk_idx),
           _p(r.topk_w), _p(r.expert_offsets), _p(r.sorted_rows), _p(ws), nbytes)
     return r
@@ -370,8 +407,7 @@ def fp8_matmul(x: Fp8Matrix, w: Fp8Matrix, bias: torch.Tensor | None = None,
     _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
     dev = _same_device(x=x.codes, x_scales=x.scales, w=w.codes, w_scales=w.scales, bias=bias)
     out = _out(M, N, dtype, dev)
-    nbytes = _bytes_needed("mxmoe_fp8_matmul_workspace_bytes", M, N, x.K, _DTYPES[dtype])
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws, nbytes = _workspace("mxmoe_fp8_matmul_workspace_bytes", dev, M, N, x.K, _DTYPES[dtype])
     _call("mxmoe_fp8_matmul", dev, M, N, x.K, _p(x.codes), _p(x.scales), _p(w.codes), _p(w.scales),
           w.block_rows, _p(bias), _DTYPES[dtype], _p(out), _p(ws), nbytes)
     return out
@@ -391,8 +427,7 @@ def fp8_linear(x: torch.Tensor, w: Fp8Matrix, bias: torch.Tensor | None = None,
     _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
     dev = _same_device(x=x, w=w.codes, w_scales=w.scales, bias=bias)
     out = _out(M, N, dtype, dev)
-    nbytes = _bytes_needed("mxmoe_fp8_linear_workspace_bytes", M, N, K, _DTYPES[dtype])
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws, nbytes = _workspace("mxmoe_fp8_linear_workspace_bytes", dev, M, N, K, _DTYPES[dtype])
     _call("mxmoe_fp8_linear", dev, M, N, K, _p(x), _p(w.codes), _p(w.scales), _p(bias), _DTYPES[dtype],
           _p(out), _p(ws), nbytes)
     return out
@@ -413,9 +448,8 @@ def fp8_linear_dw(dy: torch.Tensor, x: torch.Tensor) -> torch.Tensor:
     _shape(dy, (M, N), torch.bfloat16, "dy")
     _shape(x, (M, K), torch.bfloat16, "x")
     dev = _same_device(dy=dy, x=x)
-    nbytes = _bytes_needed("mxmoe_fp8_linear_dw_workspace_bytes", M, N, K)
+    ws, nbytes = _workspace("mxmoe_fp8_linear_dw_workspace_bytes", dev, M, N, K)
     dw = torch.empty((N, K), dtype=torch.float32, device=dev)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call("mxmoe_fp8_linear_dw", dev, M, N, K, _p(dy), _p(x), _p(dw), _p(ws), nbytes)
     return dw
 
