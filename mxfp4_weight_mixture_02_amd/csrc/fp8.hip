@@ -501,32 +501,37 @@ __device__ __forceinline__ void fp8_loop(const Fp8Wave& g, int kblocks, const ui
   }
 }
 
+// Tile `item` of the order in which bands of 8 m-tiles run through all
+// n-tiles, m fastest.
+__device__ __forceinline__ void fp8_tile_at(int item, int ntiles, int mtiles, int& nt, int& mt) {
+  const int band = item / (8 * ntiles), rows = min(8, mtiles - 8 * band);
+  const int local = item - band * 8 * ntiles;
+  mt = band * 8 + local % rows;
+  nt = local / rows;
+}
+
 // One BN x BM tile per workgroup; K in steps of one scale block (128).  In
 // LDS an operand's 16-row fragments follow each other, a row is 128 bytes in
 // 16-byte chunks, and chunk c of fragment row r sits at slot c ^ (r / 2 % 8):
 // the rows that a read touches in one cycle spread over all banks.
 template <class T, bool WROWS, bool F32>
 __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int ntiles, int mtiles,
-                                                              int splits) {
+                                                              int first, int count, int splits) {
   constexpr int FN = T::FN, FM = T::FM, WM = T::WM;
   __shared__ __align__(1024) uint8_t lds[T::NST * T::STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
   Fp8Wave v;
   v.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // tile of this block: XCD x takes a contiguous range of the order in which
-  // bands of 8 m-tiles run through all n-tiles, m fastest
-  // (with splits, every tile's parts one after the other)
-  int nt, mt, split;
+  // Tiles `first` .. `first + count - 1`: XCD x takes a contiguous range of
+  // them (with splits, every tile's parts one after the other).
+  int nt, mt, split, tile;
   {
-    const int L = ntiles * mtiles * splits, b = blockIdx.x;
+    const int L = count * splits, b = blockIdx.x;
     const int x = b & 7, base = L >> 3, extra = L & 7;
-    int item = x * base + min(x, extra) + (b >> 3);
+    const int item = x * base + min(x, extra) + (b >> 3);
     split = item % splits;
-    item /= splits;
-    const int band = item / (8 * ntiles), rows = min(8, mtiles - 8 * band);
-    const int local = item - band * 8 * ntiles;
-    mt = band * 8 + local % rows;
-    nt = local / rows;
+    tile = item / splits;
+    fp8_tile_at(first + tile, ntiles, mtiles, nt, mt);
   }
   const int64_t n0 = (int64_t)nt * T::BN, m0 = (int64_t)mt * T::BM;
   const int64_t pitch = fp8_pitch(g.K);
@@ -575,18 +580,19 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
   fp8_loop<T, WROWS, F32>(v, kblocks, lds, acc);
   const int64_t nw0 = n0 + wn * 16 * FN;
   const bool wide = g.N % FN == 0;
-  if (splits > 1) {
-    g.out = g.part + split * g.M * g.N;
-    g.bias = nullptr;
+  if (splits > 1) {   // the tile's part, the rows that exist, as [BM][BN] fp32
+    float* part = g.part + ((int64_t)split * count + tile) * (T::BN * T::BM);
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
+    for (int j = 0; j < FM; ++j) {
+      if (wm * 16 * FM + r * FM + j >= mrows) break;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        float o[FN];
+        f32x4* d = reinterpret_cast<f32x4*>(part + (wm * 16 * FM + r * FM + j) * T::BN + wn * 16 * FN + (4 * t + q) * FN);
 #pragma unroll
-        for (int i = 0; i < FN; ++i) o[i] = acc[i][j][t];
-        fp8_store<FN, true>(g, m0 + wm * 16 * FM + r * FM + j, nw0 + (4 * t + q) * FN, o, wide);
+        for (int i = 0; i < FN / 4; ++i)
+          d[i] = f32x4{acc[4 * i][j][t], acc[4 * i + 1][j][t], acc[4 * i + 2][j][t], acc[4 * i + 3][j][t]};
       }
+    }
     return;
   }
 #pragma unroll
@@ -600,34 +606,26 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
     }
 }
 
-// The sum of a product's `splits` fp32 parts in their order, plus the bias.
+// The sum of each tile's `splits` fp32 parts in their order, plus the bias:
+// 1024 values of a tile per workgroup, 4 a thread.
 template <bool F32>
-__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm g, int splits) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = g.M * g.N;
-  if (i >= all) return;
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm g, int ntiles, int mtiles, int first,
+                                                       int count, int splits, int bn, int bm) {
+  const int per = bn * bm / 1024, tile = blockIdx.x / per;
+  const int i = (blockIdx.x % per * 256 + threadIdx.x) * 4;   // in the tile
+  int nt, mt;
+  fp8_tile_at(first + tile, ntiles, mtiles, nt, mt);
+  const int64_t m = (int64_t)mt * bm + i / bn, n = (int64_t)nt * bn + i % bn;
+  if (m >= g.M || n >= g.N) return;
+  const float* p = g.part + (int64_t)tile * bn * bm + i;
+  const int64_t step = (int64_t)count * bn * bm;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const bool wide = g.N % 4 == 0;   // then the four are of one row, and aligned
-  if (wide) {
-    for (int s = 0; s < splits; ++s) {
-      const f32x4 p = *reinterpret_cast<const f32x4*>(g.part + s * all + i);
+  for (int s = 0; s < splits; ++s) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(p + s * step);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += p[e];
-    }
-    fp8_store<4, F32>(g, i / g.N, i % g.N, v, true);
-    return;
+    for (int e = 0; e < 4; ++e) v[e] += x[e];
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (i + e >= all) return;
-    float one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) one[0] += g.part[s * all + i + e];
-    const int64_t n = (i + e) % g.N;
-    if (g.bias) one[0] += bf16_to_f32(g.bias[n]);
-    if (F32)
-      static_cast<float*>(g.out)[i + e] = one[0];
-    else
-      static_cast<uint16_t*>(g.out)[i + e] = (uint16_t)f32_to_bf16(one[0]);
-  }
+  fp8_store<4, F32>(g, m, n, v, g.N % 4 == 0);
 }
 
 // Few rows: a workgroup takes 16 rows of W and its waves split the K blocks;
@@ -865,22 +863,29 @@ hipError_t launch_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int
   return hipGetLastError();
 }
 
-template <int WN, int WM, int FN, int FM, int NST>
-static hipError_t gemm_tile(const Fp8Gemm& g, int splits, hipStream_t s) {
-  using T = Fp8Tile<WN, WM, FN, FM, NST>;
+// Tiles first .. first + count - 1, in `splits` parts of K.
+template <class T>
+static hipError_t gemm_tiles(const Fp8Gemm& g, int first, int count, int splits, hipStream_t s) {
   const int nt = (int)((g.N + T::BN - 1) / T::BN), mt = (int)((g.M + T::BM - 1) / T::BM);
-  const dim3 grid((unsigned)((int64_t)nt * mt * splits)), block(64 * T::NW);
+  const dim3 grid((unsigned)((int64_t)count * splits)), block(64 * T::NW);
   if (g.w_rows) {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, true>), grid, block, 0, s, g, nt, mt, splits);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, true>), grid, block, 0, s, g, nt, mt, first, count, splits);
     else
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, false>), grid, block, 0, s, g, nt, mt, splits);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, true, false>), grid, block, 0, s, g, nt, mt, first, count, splits);
   } else {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, true>), grid, block, 0, s, g, nt, mt, splits);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, true>), grid, block, 0, s, g, nt, mt, first, count, splits);
     else
-      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, false>), grid, block, 0, s, g, nt, mt, splits);
+      hipLaunchKernelGGL((fp8_gemm_kernel<T, false, false>), grid, block, 0, s, g, nt, mt, first, count, splits);
   }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const dim3 join((unsigned)((int64_t)count * (T::BN * T::BM / 1024)));
+  if (g.out_f32)
+    hipLaunchKernelGGL(fp8_join_kernel<true>, join, dim3(256), 0, s, g, nt, mt, first, count, splits, T::BN, T::BM);
+  else
+    hipLaunchKernelGGL(fp8_join_kernel<false>, join, dim3(256), 0, s, g, nt, mt, first, count, splits, T::BN, T::BM);
   return hipGetLastError();
 }
 
@@ -902,10 +907,12 @@ static hipError_t skinny(const Fp8Gemm& g, hipStream_t s) {
 }
 
 // How a product runs: a tile (0: 256 x 256 of W and X rows, 1: 256 x 192, 2:
-// 128 x 192, 3: 128 x 128), or -1 for few rows; and parts of K.
+// 128 x 192, 3: 128 x 128; -1: few rows), the tiles that are computed whole,
+// and the parts of K in which the others are.
 struct Fp8Plan {
-  int tile, splits;
+  int tile, whole, rest, splits;
 };
+static constexpr int FP8_BN[4] = {256, 256, 128, 128}, FP8_BM[4] = {256, 192, 192, 128};
 
 // The least time by rounds of the 256 CUs.  A round of a tile takes a time in
 // proportion to its K blocks and about four more (launch, first copies,
@@ -914,45 +921,40 @@ struct Fp8Plan {
 // 1.05 (one: 0.65); fp32 results 2.33, 1.96, 1.30, 1.70 (1.02).
 //   2047 x 5760 x 2880: 256 x 256 40.1 us, 256 x 192 36.3, 128 x 192 46.0,
 //   128 x 128 43.8;  2048 x 2880 x 5760: 66.2, 58.7, 41.7, 41.9.
-// Where 128 x 128 tiles leave CUs idle, K is split over them, in parts of 3
-// blocks or more, and a second launch joins the fp32 parts, which costs a
-// launch and their bytes (written and read at 4 TB/s).
+// The tiles of a last round that leaves CUs idle may be split over K, in
+// parts of 3 blocks or more; another launch joins the fp32 parts, which
+// costs the launches and the parts' bytes (written and read at 4 TB/s).
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
   static const float T16[5] = {1.30f, 1.15f, 0.75f, 1.05f, 0.65f};
   static const float T32[5] = {2.33f, 1.96f, 1.30f, 1.70f, 1.02f};
-  static const int BN[4] = {256, 256, 128, 128}, BM[4] = {256, 192, 192, 128};
   // few rows: streaming W once per 16 rows of it beats tiles while there are
-  // enough such groups (32 rows, 5760 x 2880: 11.4 us against 16; 512 x 8192:
-  // 18 against 9), and always for a single fragment of rows
-  if (M <= 16 || (M <= 32 && N >= 2048)) return {-1, 1};
+  // enough such groups (32 rows, 5760 x 2880: 11.4 us against 15; 512 x 8192:
+  // 18 against 16), and always for a single fragment of rows
+  if (M <= 16 || (M <= 32 && N >= 2048)) return {-1, 0, 0, 1};
   const float* t = f32 ? T32 : T16;
   const int64_t kb = fp8_pitch(K) / 128;
-  Fp8Plan best{0, 1};
-  float least = 0.0f;
+  Fp8Plan best{};
+  float least = -1.0f;
   for (int i = 0; i < 4; ++i) {
-    const int64_t tiles = ((N + BN[i] - 1) / BN[i]) * ((M + BM[i] - 1) / BM[i]);
-    float us;
-    if (i < 3) {
-      us = t[i] * (float)((tiles + 255) / 256);
-    } else {
-      const int64_t rest = tiles % 512;
-      us = t[3] * (float)(tiles / 512) + (rest > 256 ? t[3] : rest ? t[4] : 0.0f);
-    }
-    us *= (float)(kb + 4);
-    if (i == 0 || us < least) {
+    const int64_t tiles = ((N + FP8_BN[i] - 1) / FP8_BN[i]) * ((M + FP8_BM[i] - 1) / FP8_BM[i]);
+    const int slots = i == 3 ? 512 : 256;
+    const int rest = (int)(tiles % slots);
+    const float full = t[i] * (float)(tiles / slots) * (float)(kb + 4);
+    auto round = [&](int64_t groups) { return groups == 0 ? 0.0f : i == 3 && groups <= 256 ? t[4] : t[i]; };
+    const float us = full + round(rest) * (float)(kb + 4);
+    if (least < 0.0f || us < least) {
       least = us;
-      best = {i, 1};
+      best = {i, (int)tiles, 0, 1};
     }
-    if (i == 3 && tiles <= 128) {
-      const int64_t s = kb / 3 < 256 / tiles ? kb / 3 : 256 / tiles;
-      if (s > 1) {
-        const float join = 3.0f + (float)(s * M * N) * 8.0f / 4.0e6f;
-        us = t[4] * (float)((kb + s - 1) / s + 4) + join;
-        if (us < least) {
-          least = us;
-          best = {3, (int)s};
-        }
-      }
+    if (rest == 0 || rest > 128) continue;
+    const int64_t s = kb / 3 < 256 / rest ? kb / 3 : 256 / rest;
+    if (s < 2) continue;
+    const int64_t tile = (int64_t)FP8_BN[i] * (M < FP8_BM[i] ? M : FP8_BM[i]);
+    const float join = (full > 0.0f ? 6.0f : 3.0f) + (float)(s * rest * tile) * 8.0f / 4.0e6f;
+    const float split = full + round(rest * s) * (float)((kb + s - 1) / s + 4) + join;
+    if (split < least) {
+      least = split;
+      best = {i, (int)(tiles - rest), rest, (int)s};
     }
   }
   return best;
@@ -960,32 +962,28 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
 
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
   const Fp8Plan p = fp8_plan(M, N, K, out_f32 != 0);
-  return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
+  return p.rest ? (size_t)p.splits * p.rest * FP8_BN[p.tile] * FP8_BM[p.tile] * sizeof(float) : 0;
+}
+
+template <class T>
+static hipError_t gemm(const Fp8Gemm& g, const Fp8Plan& p, hipStream_t s) {
+  if (p.rest && !g.part) return hipErrorInvalidValue;
+  if (p.whole) {
+    const hipError_t e = gemm_tiles<T>(g, 0, p.whole, 1, s);
+    if (e != hipSuccess) return e;
+  }
+  return p.rest ? gemm_tiles<T>(g, p.whole, p.rest, p.splits, s) : hipSuccess;
 }
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
   const Fp8Plan p = fp8_plan(g.M, g.N, g.K, g.out_f32 != 0);
-  if (p.tile < 0) {
-    if (g.M <= 16) return skinny<1>(g, s);
-    return skinny<2>(g, s);
+  switch (p.tile) {
+    case 0: return gemm<Fp8Tile<2, 4, 8, 4, 2>>(g, p, s);
+    case 1: return gemm<Fp8Tile<2, 4, 8, 3, 2>>(g, p, s);
+    case 2: return gemm<Fp8Tile<2, 4, 4, 3, 3>>(g, p, s);
+    case 3: return gemm<Fp8Tile<2, 2, 4, 4, 2>>(g, p, s);
+    default: return g.M <= 16 ? skinny<1>(g, s) : skinny<2>(g, s);
   }
-  if (p.splits > 1 && !g.part) return hipErrorInvalidValue;
-  hipError_t e;
-  if (p.tile == 0)
-    e = gemm_tile<2, 4, 8, 4, 2>(g, p.splits, s);
-  else if (p.tile == 1)
-    e = gemm_tile<2, 4, 8, 3, 2>(g, p.splits, s);
-  else if (p.tile == 2)
-    e = gemm_tile<2, 4, 4, 3, 3>(g, p.splits, s);
-  else
-    e = gemm_tile<2, 2, 4, 4, 2>(g, p.splits, s);
-  if (e != hipSuccess || p.splits == 1) return e;
-  const dim3 grid((unsigned)((g.M * g.N + 1023) / 1024)), block(256);
-  if (g.out_f32)
-    hipLaunchKernelGGL(fp8_join_kernel<true>, grid, block, 0, s, g, p.splits);
-  else
-    hipLaunchKernelGGL(fp8_join_kernel<false>, grid, block, 0, s, g, p.splits);
-  return hipGetLastError();
 }
 
 // X's codes fit the LDS of the one-launch form.
