@@ -768,7 +768,8 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_fused_kernel(Fp8Gemm g, const 
 #pragma unroll
   for (int u = 0; u < FUSED_ROUNDS; ++u) {
     if (u >= turns) break;
-    const int id = min(tid + u * 64 * SK_NW, groups - 1), row = id >> 4, l = id & 15, m = row % M;
+    const int id = tid + u * 64 * SK_NW, row = id >> 4, l = id & 15, m = row % M;
+    if (id >= groups) break;   // whole blocks: the 16 lanes of one leave together
     const int64_t k0 = (int64_t)(row / M) * 128 + 8 * l;
     float v[8];
     if (VEC) {
@@ -789,7 +790,6 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_fused_kernel(Fp8Gemm g, const 
     const float k = e4m3_inverse(e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = nan_unless_finite(v[i]) * k;
-    // (a clamped id writes the last group's bytes again)
     *reinterpret_cast<u32x2*>(xs + row * 128 + (((l >> 1) ^ (m & 7)) << 4) + 8 * (l & 1)) =
         u32x2{e4m3_pack4(v[0], v[1], v[2], v[3]), e4m3_pack4(v[4], v[5], v[6], v[7])};
     if (l == 0) sxs[row] = (uint8_t)(e + 127);

@@ -208,7 +208,7 @@ __device__ __forceinline__ bool lane_group_open(const RouteArgs& a, int lanes, i
   int beaten = 0;
   for (int o = 0; o < a.groups; ++o) {
     const int32_t ok = __builtin_amdgcn_readlane(key, o * lanes);
-    beaten += ok > key - (o < g);   // an equal key of a lower group beats too
+    beaten += ok >= key + (o >= g);   // an equal key of a lower group beats too
   }
   return beaten < a.top_groups;
 }

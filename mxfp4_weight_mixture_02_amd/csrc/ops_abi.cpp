@@ -33,8 +33,9 @@ int check_route_sizes(int64_t T, int32_t E, int32_t k) {
     return fail(MXFP4_EINVAL, "T, E and k must be >= 1 (T=%lld E=%d k=%d)", (long long)T, E, k);
   if (E > 256) return fail(MXFP4_EUNSUPPORTED, "E=%d > 256", E);
   if (k > E || k > 8) return fail(MXFP4_EUNSUPPORTED, "k=%d must be <= min(E, 8)", k);
-  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31))
-    return fail(MXFP4_EUNSUPPORTED, "T*k routed rows exceed int32 (T=%lld k=%d)", (long long)T, k);
+  // the gradient launches 64 threads a token, and a launch has 2^32
+  if (T >= (int64_t(1) << 26))
+    return fail(MXFP4_EUNSUPPORTED, "T=%lld tokens (must be < 2^26)", (long long)T);
   return MXFP4_OK;
 }
 
@@ -89,13 +90,13 @@ int check_fp8(int64_t rows, int64_t K, const char* what) {
   if (rows < 1 || K < 1)
     return fail(MXFP4_EINVAL, "%s: sizes must be >= 1 (%lld x %lld)", what, (long long)rows,
                 (long long)K);
-  if (rows >= (int64_t(1) << 31) || K > FP8_MAX_K)
-    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld (rows must be < 2^31, K <= 2^22)", what,
+  if (rows >= (int64_t(1) << 27) || K > FP8_MAX_K)
+    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld (rows must be < 2^27, K <= 2^22)", what,
                 (long long)rows, (long long)K);
-  // one workgroup for 16 rows of a K block
-  if ((rows + 15) / 16 * ((K + 63) / 64) >= (int64_t(1) << 31))
-    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld is too large", what, (long long)rows,
-                (long long)K);
+  // the quantizers launch a thread for 8 elements, and a launch has 2^32
+  if ((rows + 127) * mxmoe::fp8_pitch(K) >= (int64_t(1) << 35))
+    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld elements (must be < 2^35)", what,
+                (long long)rows, (long long)K);
   return MXFP4_OK;
 }
 
@@ -109,7 +110,7 @@ int check_dtype(int dtype, const void* p, const char* what) {
 int check_product(int64_t M, int64_t N, int64_t K) {
   int rc = check_fp8(M, K, "X");
   if (!rc) rc = check_fp8(N, K, "W");
-  if (!rc && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 31))
+  if (!rc && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 23))
     rc = fail(MXFP4_EUNSUPPORTED, "M=%lld N=%lld: too many tiles", (long long)M, (long long)N);
   return rc;
 }
@@ -142,8 +143,9 @@ int check_swiglu8(int64_t R, int64_t I, float alpha, float limit) {
   if (R < 1 || I < 1)
     return fail(MXFP4_EINVAL, "R and I must be >= 1 (R=%lld I=%lld)", (long long)R, (long long)I);
   if (I % 16) return fail(MXFP4_EUNSUPPORTED, "I=%lld is not a multiple of 16", (long long)I);
-  if (I >= (int64_t(1) << 32) || R >= (int64_t(1) << 40) / I)
-    return fail(MXFP4_EUNSUPPORTED, "R=%lld I=%lld is too large", (long long)R, (long long)I);
+  // a thread for 8 elements of h, and a launch has 2^32
+  if (I >= (int64_t(1) << 32) || R >= (int64_t(1) << 34) / I)
+    return fail(MXFP4_EUNSUPPORTED, "R=%lld I=%lld: R * 2I elements must be < 2^35", (long long)R, (long long)I);
   if (!finite(alpha) || !finite(limit) || !(limit > 0.0f))
     return fail(MXFP4_EINVAL, "alpha must be finite and limit finite and > 0");
   return MXFP4_OK;

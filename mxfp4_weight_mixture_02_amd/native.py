@@ -319,6 +319,11 @@ class SavedState:
         return Saved(*[_ptr(getattr(self, n)) for n, _ in Saved._fields_])
 
 
+def _bf16_state(saved):
+    if not isinstance(saved, SavedState):
+        raise ValueError(f"saved: a forward writes a SavedState, got {type(saved).__name__}")
+
+
 class Workspace:
     """Grow-only device workspace, reused across calls on one stream."""
 
@@ -368,6 +373,7 @@ def mxfp4_moe_forward(layer: MoeLayer, x: torch.Tensor, saved: SavedState | bool
     if out is not None:
         _shape(out, (T, layer.H), torch.bfloat16, "out")
     if saved is not None and saved is not True and saved is not False:
+        _bf16_state(saved)
         saved.check_shapes(layer, T)
     x = _dev(x, torch.bfloat16, "x")
     if saved is True:
@@ -401,6 +407,7 @@ def mxfp4_moe_forward_noalloc(layer: MoeLayer, x: torch.Tensor, out: torch.Tenso
     _shape(x, (T, layer.H), torch.bfloat16, "x")
     _shape(out, (T, layer.H), torch.bfloat16, "out")
     if saved is not None:
+        _bf16_state(saved)
         saved.check_shapes(layer, T)
     _dev(x, torch.bfloat16, "x")
     _dev(out, torch.bfloat16, "out")

@@ -207,6 +207,22 @@ def test_nan_stays_in_its_row_and_scale_padding_is_unused():
             assert torch.all(y[bad].isnan()) and torch.all(y[~bad].isfinite())
 
 
+@pytest.mark.parametrize("M,K", [(1, 128), (2, 256), (3, 2944), (16, 384), (11, 2048), (13, 2688)])
+def test_one_launch_form_where_the_last_elements_are_small(M, K):
+    """The form for few rows rounds X itself: a row whose last 8 elements are
+    far below its block's largest still has the block's scale."""
+    r = np.random.default_rng(M)
+    x = r.integers(-7, 8, size=(M, K)).astype(np.float32) * 32
+    x[:, -8:] = [1, -1, 0.5, 2, 0.25, -0.5, 1, 1]
+    w = _integers(r, (40, K))
+    for dtype in (torch.float32, torch.bfloat16):
+        y = fp8_linear(dev(x, torch.bfloat16), fp8_quantize(dev(w), 128), dtype=dtype)
+        q = fp8_matmul(fp8_quantize(dev(x)), fp8_quantize(dev(w), 128), dtype=dtype)
+        assert np.array_equal(host(q), host(y))
+    assert np.array_equal(host(fp8_linear(dev(x, torch.bfloat16), fp8_quantize(dev(w), 128), dtype=torch.float32)),
+                          ref.rounded(x) @ w.T.astype(np.float64))
+
+
 def test_zeros_and_tiny_values():
     z = torch.zeros(20, 300, dtype=torch.bfloat16, device=DEV)
     W = fp8_quantize(torch.zeros(40, 300, device=DEV), 128)

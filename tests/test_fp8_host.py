@@ -48,8 +48,8 @@ def _refused(code, rc):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(rows=0), -1), (dict(K=0), -1), (dict(K=(1 << 22) + 1), -2), (dict(rows=1 << 31), -2),
-    (dict(rows=1 << 30, K=1 << 22), -2), (dict(x=None), -1), (dict(codes=None), -1), (dict(scales=None), -1),
+    (dict(rows=0), -1), (dict(K=0), -1), (dict(K=(1 << 22) + 1), -2), (dict(rows=1 << 27), -2),
+    (dict(rows=1 << 26, K=1 << 12), -2), (dict(x=None), -1), (dict(codes=None), -1), (dict(scales=None), -1),
     (dict(dtype=2), -1), (dict(dtype=0, x=FAKE + 2), -1), (dict(dtype=1, x=FAKE + 1), -1),
     (dict(block_rows=2), -1), (dict(codes=FAKE + 8), -1), (dict(scales=FAKE + 8), -1)])
 def test_quantize_refuses(kw, code):
@@ -70,8 +70,8 @@ def test_transpose_refuses():
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(M=0), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(K=(1 << 22) + 1), -2), (dict(M=1 << 31), -2),
-    (dict(M=1 << 30, N=1 << 30), -2), (dict(x=None), -1), (dict(sw=None), -1), (dict(out=None), -1),
+    (dict(M=0), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(K=(1 << 22) + 1), -2), (dict(M=1 << 27), -2),
+    (dict(M=1 << 26, N=1 << 26), -2), (dict(x=None), -1), (dict(sw=None), -1), (dict(out=None), -1),
     (dict(br=64), -1), (dict(od=3), -1), (dict(out=FAKE + 4), -1), (dict(bias=FAKE + 1), -1),
     (dict(br=1, sw=FAKE + 1), -1), (dict(w=FAKE + 8), -1), (dict(ws=None), -3), (dict(ws=FAKE + 8), -1),
     (dict(M=128, N=256, K=4096, n=1 << 16), -3)])
@@ -110,7 +110,7 @@ def test_workspace_queries_refuse():
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(R=0), -1), (dict(I=0), -1), (dict(I=24), -2), (dict(R=1 << 38, I=16), -2), (dict(R=1 << 30, I=1 << 12), -2),
+    (dict(R=0), -1), (dict(I=0), -1), (dict(I=24), -2), (dict(R=1 << 30, I=16), -2), (dict(R=1 << 22, I=1 << 12), -2),
     (dict(alpha=float("nan")), -1), (dict(limit=float("inf")), -1), (dict(limit=0.0), -1), (dict(limit=-7.0), -1)])
 def test_swiglu_refuses(kw, code):
     d = dict(R=4, I=32, alpha=1.702, limit=7.0)

@@ -29,7 +29,7 @@ def _route(o, T=4, E=16, k=2, logits=FAKE, idx=FAKE, ws=FAKE, n=1 << 20):
     (dict(groups=3), {}, -2), (dict(groups=128, top_groups=128), dict(E=256), -2),
     (dict(groups=8, top_groups=1), dict(k=3), -2), (dict(scale=float("inf")), {}, -1),
     ({}, dict(T=0), -1), ({}, dict(k=0), -1), ({}, dict(E=0), -1), ({}, dict(E=300), -2),
-    ({}, dict(E=4, k=5), -2), ({}, dict(k=9), -2), ({}, dict(T=1 << 30, k=4), -2),
+    ({}, dict(E=4, k=5), -2), ({}, dict(k=9), -2), ({}, dict(T=1 << 26, k=4), -2),
     ({}, dict(T=1 << 62, k=4), -2),
     ({}, dict(logits=None), -1), ({}, dict(idx=None), -1), ({}, dict(logits=FAKE + 2), -1),
     ({}, dict(ws=None), -3), ({}, dict(n=16), -3), ({}, dict(ws=FAKE + 16), -1),
@@ -103,6 +103,7 @@ def test_router_logits_refuse():
     f = ops.lib().mxmoe_router_logits
     for args, code in [((0, 64, 8, FAKE, FAKE, None, FAKE), -1), ((4, 60, 8, FAKE, FAKE, None, FAKE), -2),
                        ((4, 64, 300, FAKE, FAKE, None, FAKE), -2), ((1 << 30, 64, 8, FAKE, FAKE, None, FAKE), -2),
+                       ((1 << 25, 32, 256, FAKE, FAKE, None, FAKE), -2),
                        ((4, 64, 8, None, FAKE, None, FAKE), -1), ((4, 64, 8, FAKE + 8, FAKE, None, FAKE), -1)]:
         assert f(*args, None) == code and ops.lib().mxfp4_last_error()
 
@@ -130,9 +131,12 @@ def test_routed_block_refuses():
 
 def test_routed_binding_refuses():
     import test_binding_host as th
-    from mxfp4_weight_mixture_02_amd import Routing, mxfp4_moe_backward_routed, mxfp4_moe_forward, mxfp4_moe_forward_routed
+    from mxfp4_weight_mixture_02_amd import (Routing, SavedState8, SwigluCheckpoint, mxfp4_moe_backward_routed,
+                                             mxfp4_moe_forward, mxfp4_moe_forward_routed)
     layer, x, st = th._layer(), th._x(), th._saved(5)
     r = Routing(st.topk_idx, st.topk_w, st.expert_offsets, st.sorted_rows)
+    eight = SavedState8(st.topk_idx, st.topk_w, st.expert_offsets, st.sorted_rows,
+                        SwigluCheckpoint(torch.zeros(10, 192, dtype=torch.uint8), torch.zeros(10, 6, dtype=torch.uint8)))
     short = Routing(st.topk_idx, st.topk_w, st.expert_offsets[:-1], st.sorted_rows)
     for match, call in [("CUDA tensor", lambda: mxfp4_moe_forward_routed(layer, x, r)),
                         ("CUDA tensor", lambda: mxfp4_moe_forward_routed(th._layer(router_w=None), x, r)),
@@ -140,6 +144,7 @@ def test_routed_binding_refuses():
                         ("topk_idx", lambda: mxfp4_moe_forward_routed(layer, th._x(6), r)),
                         ("mxfp8", lambda: mxfp4_moe_forward_routed(layer, x, r, saved="int8")),
                         ("mxfp8", lambda: mxfp4_moe_forward(layer, x, saved="int8")),
+                        ("a forward writes a SavedState", lambda: mxfp4_moe_forward(layer, x, saved=eight)),
                         ("router_w", lambda: mxfp4_moe_forward(th._layer(router_w=None), x)),
                         ("x is required", lambda: mxfp4_moe_backward_routed(layer, st, x, base=True)),
                         ("CUDA tensor", lambda: mxfp4_moe_backward_routed(layer, st, x))]:
