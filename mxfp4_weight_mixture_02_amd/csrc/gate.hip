@@ -262,7 +262,9 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const Lane<NQ>& mine_o
     for (int q = 0; q < NQ; ++q) key[q] = INT32_MIN;
   }
   int mine = 0;
-  for (int j = 0; j < a.k; ++j) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j >= a.k) break;
     const int32_t top = wave_max(key[0]);
     const int owner = (int)__builtin_ctzll(__ballot(key[0] == top));
     const int e = __builtin_amdgcn_readlane(at[0], owner);
