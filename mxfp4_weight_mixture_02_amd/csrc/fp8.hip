@@ -285,7 +285,12 @@ __device__ __forceinline__ void fp8_store(const Fp8Gemm& g, int64_t m, int64_t n
   }
   const int64_t at = m * g.N + n;
   if (wide) {   // N % F == 0: the F values exist and are aligned
-    if (F32) {
+    if constexpr (F == 2) {
+      if (F32)
+        *reinterpret_cast<f32x2*>(static_cast<float*>(g.out) + at) = f32x2{v[0], v[1]};
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + at) = pack_bf16x2(v[0], v[1]);
+    } else if constexpr (F32) {
       f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
 #pragma unroll
       for (int i = 0; i < F / 4; ++i) d[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
@@ -325,8 +330,8 @@ struct Fp8Tile {
   static_assert(BN <= 256 && BM <= 256 && NST >= 2 && NST * STAGE <= 160 * 1024, "LDS");
   static_assert((NST - 1) * (LOADS + 1) < 64, "vector-memory counter");
   static constexpr bool SPREAD = 2 * NST * STAGE > 160 * 1024;   // one workgroup on a CU
-  // scale bytes of X are read four at a time, or with F_M % 4 one by one
-  static constexpr int XW = FM % 4 ? FM : FM / 4;
+  // scale bytes of X and W are read four at a time, or with F % 4 one by one
+  static constexpr int XW = FM % 4 ? FM : FM / 4, WW = FN % 4 ? FN : FN / 4;
 };
 
 // Copy from global memory to LDS: 16, 4 or 1 bytes a lane from base + off +
@@ -412,7 +417,7 @@ __device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p, int s0) {
 // A K block's scales of this lane's rows: words of four bytes, or bytes.
 template <class T>
 struct Fp8Scales {
-  uint32_t x[T::XW], w[T::FN / 4];
+  uint32_t x[T::XW], w[T::WW];
 };
 template <class T, bool WROWS>
 __device__ __forceinline__ Fp8Scales<T> fp8_scales(const Fp8Wave& g, const uint8_t* st) {
@@ -421,8 +426,8 @@ __device__ __forceinline__ Fp8Scales<T> fp8_scales(const Fp8Wave& g, const uint8
   for (int i = 0; i < T::XW; ++i)
     s.x[i] = T::FM % 4 ? st[g.sxoff + i] : *reinterpret_cast<const uint32_t*>(st + g.sxoff + 4 * i);
 #pragma unroll
-  for (int i = 0; i < (WROWS ? T::FN / 4 : 1); ++i)
-    s.w[i] = *reinterpret_cast<const uint32_t*>(st + g.swoff + 4 * i);
+  for (int i = 0; i < (WROWS ? T::WW : 1); ++i)
+    s.w[i] = WROWS && T::FN % 4 ? st[g.swoff + i] : *reinterpret_cast<const uint32_t*>(st + g.swoff + 4 * i);
   return s;
 }
 
@@ -467,7 +472,7 @@ __device__ __forceinline__ void fp8_loop(const Fp8Wave& g, int kblocks, const ui
       for (int i = 0; i < FN; ++i) {
         bf16x8 a[4];
         fp8_to_bf16(fp8_frag(cur + g.woff + i * 2048, g.s0),
-                    byte_of(c.w[WROWS ? i >> 2 : 0], WROWS ? i & 3 : 0), a);
+                    byte_of(c.w[!WROWS ? 0 : FN % 4 ? i : i >> 2], WROWS && FN % 4 == 0 ? i & 3 : 0), a);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -489,7 +494,8 @@ __device__ __forceinline__ void fp8_loop(const Fp8Wave& g, int kblocks, const ui
         if (T::SPREAD) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < FM; ++j)
-          acc[i][j] = fp8_mfma(a[i & 1], b[j], acc[i][j], WROWS ? i & 3 : 0, (int)c.w[WROWS ? i >> 2 : 0],
+          acc[i][j] = fp8_mfma(a[i & 1], b[j], acc[i][j], WROWS && FN % 4 == 0 ? i & 3 : 0,
+                               (int)c.w[!WROWS ? 0 : FN % 4 ? i : i >> 2],
                                FM % 4 ? 0 : j & 3, (int)c.x[FM % 4 ? j : j >> 2]);
         if (T::SPREAD) {
           __builtin_amdgcn_sched_barrier(0);
@@ -587,10 +593,14 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
       if (wm * 16 * FM + r * FM + j >= mrows) break;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        f32x4* d = reinterpret_cast<f32x4*>(part + (wm * 16 * FM + r * FM + j) * T::BN + wn * 16 * FN + (4 * t + q) * FN);
+        float* d = part + (wm * 16 * FM + r * FM + j) * T::BN + wn * 16 * FN + (4 * t + q) * FN;
 #pragma unroll
-        for (int i = 0; i < FN / 4; ++i)
-          d[i] = f32x4{acc[4 * i][j][t], acc[4 * i + 1][j][t], acc[4 * i + 2][j][t], acc[4 * i + 3][j][t]};
+        for (int i = 0; i < FN; i += FN < 4 ? FN : 4) {
+          if constexpr (FN < 4)
+            *reinterpret_cast<f32x2*>(d) = f32x2{acc[0][j][t], acc[1][j][t]};
+          else
+            *reinterpret_cast<f32x4*>(d + i) = f32x4{acc[i][j][t], acc[i + 1][j][t], acc[i + 2][j][t], acc[i + 3][j][t]};
+        }
       }
     }
     return;
@@ -620,6 +630,7 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm g, int ntiles, in
   const float* p = g.part + (int64_t)tile * bn * bm + i;
   const int64_t step = (int64_t)count * bn * bm;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
   for (int s = 0; s < splits; ++s) {
     const f32x4 x = *reinterpret_cast<const f32x4*>(p + s * step);
 #pragma unroll
@@ -635,7 +646,7 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm g, int ntiles, in
 // instruction brings 64 contiguous bytes of each of 16 rows.
 constexpr int SK_NW = 8, SK_CH = 3;   // waves; K blocks in flight per wave
 
-// W's fragments and scales of K blocks c0 .. c0 + SK_CH - 1 (past b1 - 1: that
+// A row's fragments and scales of K blocks c0 .. c0 + SK_CH - 1 (past b1 - 1: that
 // block again, not multiplied).
 struct SkinnyW {
   u32x4 lo[SK_CH], hi[SK_CH];
@@ -664,68 +675,49 @@ __device__ __forceinline__ f32x4 skinny_product(const u32x4& wl, const u32x4& wh
   for (int t = 0; t < 4; ++t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[t], bv[t], acc, 0, 0, 0);
   return acc;
 }
-// The waves' sums in their order, plus the bias, to rows 16 j .. of out.
-// Lane l holds D rows 4 (l / 16) .. + 3 (n) of column l % 16 (m).
-template <int FM, bool F32>
-__device__ __forceinline__ void skinny_store(const Fp8Gemm& g, f32x4 (*part)[FM][64], int64_t n0, int wave,
-                                             int lane) {
-  const bool wide = g.N % 4 == 0;
-  for (int j = wave; j < FM; j += SK_NW) {
-    f32x4 sum = part[0][j][lane];
+// The waves' sums in their order, plus the bias, by the first wave.  Lane l
+// holds D rows 4 (l / 16) .. + 3 (n) of column l % 16 (m).
+template <bool F32>
+__device__ __forceinline__ void skinny_store(const Fp8Gemm& g, f32x4 (*part)[64], int64_t n0, int wave, int lane) {
+  if (wave) return;
+  f32x4 sum = part[0][lane];
 #pragma unroll
-    for (int u = 1; u < SK_NW; ++u) sum += part[u][j][lane];
-    float o[4] = {sum[0], sum[1], sum[2], sum[3]};
-    fp8_store<4, F32>(g, 16 * j + (lane & 15), n0 + 4 * (lane >> 4), o, wide);
-  }
+  for (int u = 1; u < SK_NW; ++u) sum += part[u][lane];
+  float o[4] = {sum[0], sum[1], sum[2], sum[3]};
+  fp8_store<4, F32>(g, lane & 15, n0 + 4 * (lane >> 4), o, g.N % 4 == 0);
 }
 
-// 8-bit X, up to 16 FM rows: X's fragments come straight from memory too,
-// all loads of SK_CH K blocks before the first product.
-template <int FM, bool WROWS, bool F32>
+// 8-bit X, up to 16 rows: X's fragments come straight from memory too, all
+// loads of SK_CH K blocks before the first product.
+template <bool WROWS, bool F32>
 __global__ __launch_bounds__(64 * SK_NW) void fp8_skinny_kernel(Fp8Gemm g) {
-  __shared__ f32x4 part[SK_NW][FM][64];
+  __shared__ f32x4 part[SK_NW][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, q = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int64_t pitch = fp8_pitch(g.K);
   const int kblocks = (int)(pitch / 128);
   const int b0 = wave * kblocks / SK_NW, b1 = (wave + 1) * kblocks / SK_NW;
-  const int64_t n = min(n0 + r, g.N - 1);
+  const int64_t n = min(n0 + r, g.N - 1), m = min((int64_t)r, g.M - 1);
   const uint8_t* w = g.w + n * pitch + 16 * q;
+  const uint8_t* x = g.x + m * pitch + 16 * q;
   const int64_t sxp = fp8_scale_pitch(g.M);
   const int64_t swp = WROWS ? fp8_scale_pitch(g.N) : (g.N + 127) / 128;
   const uint8_t* sw = g.sw + (WROWS ? n : n / 128);
-  f32x4 acc[FM];
-#pragma unroll
-  for (int j = 0; j < FM; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int c0 = b0; c0 < b1; c0 += SK_CH) {
-    u32x4 xl[SK_CH][FM], xh[SK_CH][FM];
-    uint32_t sx[SK_CH][FM];
-#pragma unroll
-    for (int u = 0; u < SK_CH; ++u) {
-      const int64_t kb = min(c0 + u, b1 - 1);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        const int64_t m = min((int64_t)(16 * j + r), g.M - 1);
-        xl[u][j] = gload16(g.x + m * pitch + kb * 128 + 16 * q);
-        xh[u][j] = gload16(g.x + m * pitch + kb * 128 + 16 * q + 64);
-        sx[u][j] = g.sx[kb * sxp + m];
-      }
-    }
-    SkinnyW f;
-    skinny_load(w, sw, swp, c0, b1, f);
+    SkinnyW fx, fw;
+    skinny_load(x, g.sx + m, sxp, c0, b1, fx);
+    skinny_load(w, sw, swp, c0, b1, fw);
 #pragma unroll
     for (int u = 0; u < SK_CH; ++u) {
       if (c0 + u >= b1) continue;
-#pragma unroll
-      for (int j = 0; j < FM; ++j)
-        acc[j] = skinny_product<F32>(f.lo[u], f.hi[u], f.s[u], xl[u][j], xh[u][j], sx[u][j], acc[j]);
+      acc = skinny_product<F32>(fw.lo[u], fw.hi[u], fw.s[u], fx.lo[u], fx.hi[u], fx.s[u], acc);
     }
   }
-#pragma unroll
-  for (int j = 0; j < FM; ++j) part[wave][j][lane] = acc[j];
+  part[wave][lane] = acc;
   __syncthreads();
-  skinny_store<FM, F32>(g, part, n0, wave, lane);
+  skinny_store<F32>(g, part, n0, wave, lane);
 }
 
 // bf16 X of up to 16 rows, rounded to E4M3 here: every workgroup rounds all
@@ -740,7 +732,7 @@ template <bool F32, bool VEC>
 __global__ __launch_bounds__(64 * SK_NW) void fp8_fused_kernel(Fp8Gemm g, const uint16_t* __restrict__ xb) {
   __shared__ __align__(16) uint8_t xs[FUSED_BYTES];
   __shared__ uint8_t sxs[FUSED_BYTES / 128];
-  __shared__ f32x4 part[SK_NW][1][64];
+  __shared__ f32x4 part[SK_NW][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, q = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
@@ -811,9 +803,9 @@ __global__ __launch_bounds__(64 * SK_NW) void fp8_fused_kernel(Fp8Gemm g, const 
       acc = skinny_product<F32>(f.lo[u], f.hi[u], f.s[u], xl, xh, sxs[kb * M + m], acc);
     }
   }
-  part[wave][0][lane] = acc;
+  part[wave][lane] = acc;
   __syncthreads();
-  skinny_store<1, F32>(g, part, n0, wave, lane);
+  skinny_store<F32>(g, part, n0, wave, lane);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -889,72 +881,98 @@ static hipError_t gemm_tiles(const Fp8Gemm& g, int first, int count, int splits,
   return hipGetLastError();
 }
 
-template <int FM>
 static hipError_t skinny(const Fp8Gemm& g, hipStream_t s) {
   const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * SK_NW);
   if (g.w_rows) {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, true, true>), grid, block, 0, s, g);
+      hipLaunchKernelGGL((fp8_skinny_kernel<true, true>), grid, block, 0, s, g);
     else
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, true, false>), grid, block, 0, s, g);
+      hipLaunchKernelGGL((fp8_skinny_kernel<true, false>), grid, block, 0, s, g);
   } else {
     if (g.out_f32)
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, false, true>), grid, block, 0, s, g);
+      hipLaunchKernelGGL((fp8_skinny_kernel<false, true>), grid, block, 0, s, g);
     else
-      hipLaunchKernelGGL((fp8_skinny_kernel<FM, false, false>), grid, block, 0, s, g);
+      hipLaunchKernelGGL((fp8_skinny_kernel<false, false>), grid, block, 0, s, g);
   }
   return hipGetLastError();
 }
 
-// How a product runs: a tile (0: 256 x 256 of W and X rows, 1: 256 x 192, 2:
-// 128 x 192, 3: 128 x 128; -1: few rows), the tiles that are computed whole,
-// and the parts of K in which the others are.
+// How a product runs: a tile (-1: few rows), the tiles that are computed
+// whole, and the parts of K in which the others are.
 struct Fp8Plan {
   int tile, whole, rest, splits;
 };
-static constexpr int FP8_BN[4] = {256, 256, 128, 128}, FP8_BM[4] = {256, 192, 192, 128};
 
-// The least time by rounds of the 256 CUs.  A round of a tile takes a time in
-// proportion to its K blocks and about four more (launch, first copies,
-// stores); the factors are measured (us for a K block on one round of 5760 x
-// 2880): bf16 results 1.30, 1.15, 0.75 and, with two workgroups on a CU,
-// 1.05 (one: 0.65); fp32 results 2.33, 1.96, 1.30, 1.70 (1.02).
-//   2047 x 5760 x 2880: 256 x 256 40.1 us, 256 x 192 36.3, 128 x 192 46.0,
-//   128 x 128 43.8;  2048 x 2880 x 5760: 66.2, 58.7, 41.7, 41.9.
-// The tiles of a last round that leaves CUs idle may be split over K, in
-// parts of 3 blocks or more; another launch joins the fp32 parts, which
-// costs the launches and the parts' bytes (written and read at 4 TB/s).
+// The tiles, W rows x X rows, with what a launch of each takes, for bf16 and
+// for fp32 results: `lat` us for a K block while a CU has one workgroup, `thr`
+// us for each workgroup that a CU has when it has more, and `c` us for every
+// `res` of them (launch, first copies, stores).  Fitted to launches of 64 to
+// 2048 rows by 5760 x 2880, 2880 x 5760, 4096 x 4096 and 8192 x 1024 whose W
+// comes from HBM; the choice is then 2-3% slower than the best tile of each.
+// Wide tiles keep the matrix cores busy, narrow ones reach all CUs and bring
+// W faster (us; 5760 x 2880):
+//   rows       64    128    256    512   1024   2048
+//   256 x 256  38.2  38.9   41.2   41.0   41.1   41.7
+//   256 x 192  36.7  38.0   37.9   38.1   38.2   39.1
+//   128 x 192  21.6  22.7   24.3   24.9   46.3   48.4
+//   128 x 128  23.5  28.2   27.7   27.5   32.1   54.5   two stages, two workgroups on a CU
+//   128 x 128  18.4  20.1   19.9   20.1   38.3   57.1   three stages, one
+//   64 x 128   14.4  15.3   15.5   24.5   34.4   60.1
+//   64 x 64    12.2  12.6   17.8   26.6   44.2   84.1
+//   32 x 64    10.1  14.1   18.7   31.0   54.8   99.5
+//   32 x 32    10.5  12.8   22.6   35.6   64.7    121   (32 rows: 8.9)
+struct Fp8Shape {
+  int bn, bm, res;
+  float lat[2], thr[2], c[2];
+};
+static constexpr Fp8Shape FP8_SHAPE[] = {
+    {256, 256, 1, {1.40f, 2.52f}, {1.40f, 2.52f}, {7.5f, 10.3f}},
+    {256, 192, 1, {1.33f, 2.12f}, {1.33f, 2.12f}, {7.2f, 9.3f}},
+    {128, 192, 1, {0.73f, 1.22f}, {0.73f, 1.22f}, {7.0f, 7.4f}},
+    {128, 128, 2, {0.90f, 1.00f}, {0.59f, 0.87f}, {4.9f, 5.8f}},
+    {128, 128, 1, {0.60f, 1.08f}, {0.60f, 1.08f}, {5.7f, 5.8f}},
+    {64, 128, 2, {0.46f, 0.65f}, {0.38f, 0.52f}, {4.4f, 4.6f}},
+    {64, 64, 2, {0.37f, 0.55f}, {0.27f, 0.36f}, {3.9f, 4.0f}},
+    {32, 64, 3, {0.28f, 0.38f}, {0.22f, 0.25f}, {3.7f, 3.8f}},
+    {32, 32, 4, {0.24f, 0.37f}, {0.13f, 0.21f}, {3.5f, 3.5f}},
+};
+
+// The tile of the least time.  The tiles of a last round that leaves CUs idle
+// may be split over K, in parts of 3 blocks or more; another launch joins the
+// fp32 parts, which costs the launches and the parts' bytes (written and read
+// at 4 TB/s).
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
-  static const float T16[5] = {1.30f, 1.15f, 0.75f, 1.05f, 0.65f};
-  static const float T32[5] = {2.33f, 1.96f, 1.30f, 1.70f, 1.02f};
-  // few rows: streaming W once per 16 rows of it beats tiles while there are
-  // enough such groups (32 rows, 5760 x 2880: 11.4 us against 15; 512 x 8192:
-  // 18 against 16), and always for a single fragment of rows
-  if (M <= 16 || (M <= 32 && N >= 2048)) return {-1, 0, 0, 1};
-  const float* t = f32 ? T32 : T16;
+  // one fragment of rows: streaming W in 16-row groups over K, while there are
+  // enough of these (16 rows, 5760 x 2880: 8.4 us against 8.9 in 32 x 32
+  // tiles; 4096 x 4096: 7.4, 9.6; 512 x 8192: 10.7, 7.8)
+  if (M <= 16 && N >= 1024) return {-1, 0, 0, 1};
   const int64_t kb = fp8_pitch(K) / 128;
   Fp8Plan best{};
   float least = -1.0f;
-  for (int i = 0; i < 4; ++i) {
-    const int64_t tiles = ((N + FP8_BN[i] - 1) / FP8_BN[i]) * ((M + FP8_BM[i] - 1) / FP8_BM[i]);
-    const int slots = i == 3 ? 512 : 256;
-    const int rest = (int)(tiles % slots);
-    const float full = t[i] * (float)(tiles / slots) * (float)(kb + 4);
-    auto round = [&](int64_t groups) { return groups == 0 ? 0.0f : i == 3 && groups <= 256 ? t[4] : t[i]; };
-    const float us = full + round(rest) * (float)(kb + 4);
+  for (int i = 0; i < (int)(sizeof(FP8_SHAPE) / sizeof(FP8_SHAPE[0])); ++i) {
+    const Fp8Shape& t = FP8_SHAPE[i];
+    const int64_t tiles = ((N + t.bn - 1) / t.bn) * ((M + t.bm - 1) / t.bm);
+    if (tiles > 1 << 23) continue;   // more than a launch takes; the wide ones of such a product are fewer
+    auto launch = [&](int64_t groups, int64_t blocks) {
+      const int64_t w = (groups + 255) / 256, rounds = (w + t.res - 1) / t.res;
+      const float block = w > 1 && t.thr[f32] * (float)w > t.lat[f32] ? t.thr[f32] * (float)w : t.lat[f32];
+      return groups == 0 ? 0.0f : block * (float)blocks + t.c[f32] * (float)rounds;
+    };
+    const float us = launch(tiles, kb);
     if (least < 0.0f || us < least) {
       least = us;
       best = {i, (int)tiles, 0, 1};
     }
+    const int64_t rest = tiles % (256 * t.res);
     if (rest == 0 || rest > 128) continue;
     const int64_t s = kb / 3 < 256 / rest ? kb / 3 : 256 / rest;
     if (s < 2) continue;
-    const int64_t tile = (int64_t)FP8_BN[i] * (M < FP8_BM[i] ? M : FP8_BM[i]);
-    const float join = (full > 0.0f ? 6.0f : 3.0f) + (float)(s * rest * tile) * 8.0f / 4.0e6f;
-    const float split = full + round(rest * s) * (float)((kb + s - 1) / s + 4) + join;
+    const int64_t tile = (int64_t)t.bn * (M < t.bm ? M : t.bm);
+    const float join = (tiles > rest ? 6.0f : 3.0f) + (float)(s * rest * tile) * 8.0f / 4.0e6f;
+    const float split = launch(tiles - rest, kb) + launch(rest * s, (kb + s - 1) / s) + join;
     if (split < least) {
       least = split;
-      best = {i, (int)(tiles - rest), rest, (int)s};
+      best = {i, (int)(tiles - rest), (int)rest, (int)s};
     }
   }
   return best;
@@ -962,7 +980,7 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
 
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
   const Fp8Plan p = fp8_plan(M, N, K, out_f32 != 0);
-  return p.rest ? (size_t)p.splits * p.rest * FP8_BN[p.tile] * FP8_BM[p.tile] * sizeof(float) : 0;
+  return p.rest ? (size_t)p.splits * p.rest * FP8_SHAPE[p.tile].bn * FP8_SHAPE[p.tile].bm * sizeof(float) : 0;
 }
 
 template <class T>
@@ -982,7 +1000,12 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
     case 1: return gemm<Fp8Tile<2, 4, 8, 3, 2>>(g, p, s);
     case 2: return gemm<Fp8Tile<2, 4, 4, 3, 3>>(g, p, s);
     case 3: return gemm<Fp8Tile<2, 2, 4, 4, 2>>(g, p, s);
-    default: return g.M <= 16 ? skinny<1>(g, s) : skinny<2>(g, s);
+    case 4: return gemm<Fp8Tile<2, 2, 4, 4, 3>>(g, p, s);
+    case 5: return gemm<Fp8Tile<1, 4, 4, 2, 3>>(g, p, s);
+    case 6: return gemm<Fp8Tile<1, 4, 4, 1, 4>>(g, p, s);
+    case 7: return gemm<Fp8Tile<1, 4, 2, 1, 4>>(g, p, s);
+    case 8: return gemm<Fp8Tile<1, 2, 2, 1, 4>>(g, p, s);
+    default: return skinny(g, s);
   }
 }
 

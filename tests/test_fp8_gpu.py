@@ -135,6 +135,38 @@ def test_integer_products_are_exact(M, N, K):
     assert torch.equal(fp8_matmul(q, V, bias=b), dev(rows + bias, torch.bfloat16))
 
 
+
+# every tile of the products, with rows and columns past its edge, whole and
+# in parts of K, and a product whose last round alone is in parts
+TILES = [(4099, 2881, 100), (2050, 4101, 100), (4097, 1001, 640), (4100, 1001, 99), (2050, 1001, 1300),
+         (2049, 1001, 100), (130, 8201, 100), (1030, 1001, 100), (33, 1001, 2881), (20, 2881, 2881),
+         (3, 1030, 384), (16, 2049, 140), (2050, 7250, 2881), (3000, 5500, 2881), (1030, 7250, 5000)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_tiles_are_exact(M, N, K):
+    """Integers times block magnitudes, as above, against products in 64 bits:
+    |x| and |w| stay below 12 in steps of 1/4, a sum of 5000 products below
+    2^24 steps of 1/16."""
+    print("tiles", M, N, K, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(M + 3 * N + 7 * K)
+
+    def draw(rows, per):
+        v = torch.randint(-3, 4, (rows, K), generator=g, device=DEV).float()
+        e = torch.randint(-2, 3, (-(-rows // per), -(-K // 128)), generator=g, device=DEV).float().exp2()
+        return v * e.repeat_interleave(per, 0)[:rows].repeat_interleave(128, 1)[:, :K]
+
+    x, wb, wv = draw(M, 1), draw(N, 128), draw(N, 1)
+    q = fp8_quantize(x)
+    for w, rows in ((wb, 128), (wv, 1)):
+        W = fp8_quantize(w, rows)
+        want = x.double() @ w.double().t()
+        assert torch.equal(fp8_matmul(q, W, dtype=torch.float32).double(), want)
+        # bf16: a K block's products of a row and a column share a scale and
+        # are integers up to 9, of which the scaled matrix core drops nothing
+        assert torch.equal(fp8_matmul(q, W), want.float().bfloat16())
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 33), (130, 129, 257), (511, 200, 640), (2049, 320, 96), (64, 16, 16),
                                    (5000, 100, 70), (3000, 66, 65)])
 def test_integer_weight_gradients_are_exact(M, N, K):
