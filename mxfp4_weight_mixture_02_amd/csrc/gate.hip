@@ -289,7 +289,9 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const Lane<NQ>& mine_o
 }
 
 // The choice of `per_block` tokens by one workgroup of 16 waves, and the
-// workgroup's histogram of experts.
+// workgroup's histogram of experts.  Bound by vector instructions (about 600 a
+// token, the units 75% busy): 16384 tokens x 256 experts, k = 8 in 25.4 us,
+// 0.8 TB/s of logits; 2048 x 32, k = 4 in 5.5 us.
 constexpr int GATE_W = 16;
 template <int NQ>
 __global__ __launch_bounds__(64 * GATE_W) void gate_kernel(RouteArgs a, int per_block,
@@ -316,7 +318,8 @@ __global__ __launch_bounds__(64 * GATE_W) void gate_kernel(RouteArgs a, int per_
 }
 
 // Few tokens (T <= GATE_ONE_TOKENS): choice, offsets and permutation in one
-// workgroup.
+// workgroup.  A chain of dependent steps, so bound by latency: one token of
+// 256 experts, k = 8 in 5.5 us, against three launches of 3 us and more.
 constexpr int GATE_ONE_TOKENS = 32;
 template <int NQ>
 __global__ __launch_bounds__(64 * GATE_W) void gate_one_kernel(RouteArgs a) {
@@ -349,7 +352,8 @@ __global__ __launch_bounds__(64 * GATE_W) void gate_one_kernel(RouteArgs a) {
 }
 
 // Expert e = blockIdx.x: in place, hist[b][e] becomes the number of rows of
-// e in workgroups before b; total[e] their sum.
+// e in workgroups before b; total[e] their sum.  Latency (a scan of 256
+// numbers): 4.0 us for 256 workgroups x 256 experts.
 __global__ __launch_bounds__(256) void gate_prefix_kernel(int32_t* __restrict__ hist, int nblk,
                                                           int E, int32_t* __restrict__ total) {
   __shared__ int32_t part[256];
@@ -382,6 +386,7 @@ __global__ __launch_bounds__(256) void gate_prefix_kernel(int32_t* __restrict__ 
 // counts in LDS.  base and total are gate_prefix_kernel's, or with total ==
 // nullptr base holds the workgroups' histograms and every workgroup adds up
 // the few there are (2048 tokens: one launch less, 3 us of host time).
+// 131072 rows of 256 experts in 4.1 us.
 __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_block,
                                                            const int32_t* __restrict__ base,
                                                            const int32_t* __restrict__ total) {
@@ -466,7 +471,8 @@ __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_
 // dlogits of one token per wave.  With w = scale * s / S (renorm) the
 // chosen scores' gradients are ds_j = scale (dw_j - sum_i dw_i s_i / S) / S,
 // else ds_j = scale dw_j; sigmoid dl = ds s (1 - s), softmax dl_e =
-// s_e (ds_e - sum_j ds_j s_j).  Scores in fp64, as in the choice.
+// s_e (ds_e - sum_j ds_j s_j).  Scores in fp64, as in the choice, which bounds
+// it: 8192 tokens x 128 experts in 6.9 us, 8.7 MB at 1.3 TB/s.
 template <int NQ>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_t* __restrict__ idx,
                                                        const float* __restrict__ dw,
@@ -516,8 +522,9 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
 
 // Tokens per workgroup of the choice, which has a histogram row for each: a
 // wave takes one token while that gives at most four waves a SIMD, then 4, 8
-// or 16 (16384 tokens x 256 experts: 4; with one wave a SIMD, 16 each, the
-// first form of the choice took 120 us against 34).
+// or 16.  Whole routing of 16384 tokens x 256 experts with 1, 2, 4, 8, 16 each:
+// 42.9, 34.4, 31.0 (taken), 50.0, 79.9 us: fewer leave the two later launches
+// more histograms, more leave SIMDs empty.
 static int gate_tokens(int64_t T) {
   const int64_t per_wave = (T + 4095) / 4096;
   return GATE_W * (int)(per_wave < 16 ? per_wave : 16);
