@@ -58,9 +58,9 @@ def lib() -> ctypes.CDLL:
         L.mxmoe_swiglu8_forward.argtypes = [vp, i64, i64, f32, f32, vp, vp, vp, vp]
         L.mxmoe_swiglu8_backward.argtypes = [vp, vp, vp, i64, i64, f32, f32, vp, vp, vp]
         L.mxmoe_swiglu8_restore.argtypes = [vp, vp, i64, i64, f32, f32, vp, vp, vp]
-        for n in ("route", "route_backward", "router_logits", "forward_routed", "backward_routed", "fp8_quantize", "fp8_quantize_t", "fp8_transpose",
-                  "fp8_matmul", "fp8_linear", "fp8_linear_dw", "swiglu8_forward",
-                  "swiglu8_backward", "swiglu8_restore"):
+        for n in ("route", "route_backward", "router_logits", "forward_routed", "backward_routed", "fp8_quantize",
+                  "fp8_quantize_t", "fp8_transpose", "fp8_matmul", "fp8_linear", "fp8_linear_dw",
+                  "swiglu8_forward", "swiglu8_backward", "swiglu8_restore"):
             getattr(L, "mxmoe_" + n).restype = ci
         _lib = L
     return _lib
@@ -256,7 +256,7 @@ def mxfp4_moe_forward_routed(layer: MoeLayer, x: torch.Tensor, routing: Routing,
     T = x.shape[0]
     _shape(x, (T, layer.H), torch.bfloat16, "x")
     _routing_shapes(layer, T, routing)
-    if isinstance(saved, str):
+    if not isinstance(saved, bool):
         SavedState8.check_format(saved)
     dev = _layer_device(layer, x=x, **_fields(routing))
     state = SavedState(**_fields(routing), h=None, a=None)

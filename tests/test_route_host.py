@@ -143,6 +143,7 @@ def test_routed_binding_refuses():
                         ("expert_offsets", lambda: mxfp4_moe_forward_routed(layer, x, short)),
                         ("topk_idx", lambda: mxfp4_moe_forward_routed(layer, th._x(6), r)),
                         ("mxfp8", lambda: mxfp4_moe_forward_routed(layer, x, r, saved="int8")),
+                        ("mxfp8", lambda: mxfp4_moe_forward_routed(layer, x, r, saved=st)),
                         ("mxfp8", lambda: mxfp4_moe_forward(layer, x, saved="int8")),
                         ("a forward writes a SavedState", lambda: mxfp4_moe_forward(layer, x, saved=eight)),
                         ("router_w", lambda: mxfp4_moe_forward(th._layer(router_w=None), x)),

@@ -1,5 +1,7 @@
 """The expert block on a given routing, the 8-bit saved state, and a layer of
 routed experts and an 8-bit shared expert, forward and backward."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -66,6 +68,20 @@ def test_the_blocks_own_routing_gives_its_own_results(kw):
     assert np.all(np.abs(to_f64(full["dx"]) - want) <= 2 * 2.0 ** -8 * (np.abs(want) + np.abs(to_f64(part["dx"]))) + 1e-6)
     dx_only = mxfp4_moe_backward_routed(L, st2, dy)
     assert torch.equal(dx_only["dx"], part["dx"]) and torch.equal(dx_only["dw"], part["dw"])
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("act_format", ["mxfp8", "mxfp8x2"])
+def test_block_scaled_activations_on_a_given_routing(T, act_format):
+    s = _spec(T=T, H=128)
+    print("routed", s, act_format, flush=True)
+    L, (x, dy) = dataclasses.replace(device_layer(s), act_format=act_format), _inputs(s)
+    out, st = mxfp4_moe_forward(L, x, saved=True)
+    got, st2 = mxfp4_moe_forward_routed(dataclasses.replace(L, router_w=None, router_b=None), x, st, saved=True)
+    assert torch.equal(got, out) and torch.equal(st2.h, st.h) and torch.equal(st2.a, st.a)
+    full, part = mxfp4_moe_backward(L, st, x, dy), mxfp4_moe_backward_routed(L, st2, dy, x=x, base=True)
+    for n in ("dW_gu", "dW_dn", "db_gu", "db_dn"):
+        assert torch.equal(full[n], part[n]), n
 
 
 def test_logits_are_the_blocks():
