@@ -166,6 +166,9 @@ __device__ __forceinline__ unsigned long long open_groups(const RouteArgs& a, co
 }
 
 template <int NQ>
+using Floats = float __attribute__((ext_vector_type(NQ)));
+
+template <int NQ>
 struct Lane {          // what a lane holds of its experts, whatever the token
   float bias[NQ];
   int group[NQ];
@@ -181,10 +184,18 @@ __device__ __forceinline__ Lane<NQ> lane_of(const RouteArgs& a, int lane) {
   }
   return l;
 }
+// A lane's logits of token t (past E: some of the row's).
 template <int NQ>
 __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int lane, float (&v)[NQ]) {
+  const float* row = a.logits + t * a.E;
+  if (a.wide) {   // whole vectors: E % NQ == 0
+    const auto x = *reinterpret_cast<const Floats<NQ>*>(row + min(NQ * lane, a.E - NQ));
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) v[q] = a.logits[t * a.E + min(NQ * lane + q, a.E - 1)];
+    for (int q = 0; q < NQ; ++q) v[q] = x[q];
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) v[q] = row[min(NQ * lane + q, a.E - 1)];
 }
 
 // Whether this lane's group is open, where a group is `lanes` whole lanes (a
@@ -472,7 +483,7 @@ __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_
 // chosen scores' gradients are ds_j = scale (dw_j - sum_i dw_i s_i / S) / S,
 // else ds_j = scale dw_j; sigmoid dl = ds s (1 - s), softmax dl_e =
 // s_e (ds_e - sum_j ds_j s_j).  Scores in fp64, as in the choice, which bounds
-// it: 8192 tokens x 128 experts in 6.9 us, 8.7 MB at 1.3 TB/s.
+// it: 8192 tokens x 128 experts in 6.6 us, 8.7 MB at 1.3 TB/s.
 template <int NQ>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_t* __restrict__ idx,
                                                        const float* __restrict__ dw,
@@ -482,18 +493,18 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   if (t >= a.T) return;
   float v[NQ];
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) v[q] = a.logits[t * a.E + min(NQ * lane + q, a.E - 1)];
+  load_logits<NQ>(a, t, lane, v);
+  const int e = lane < a.k ? idx[t * a.k + lane] : -1;   // all loads at the start
+  const float d = lane < a.k ? dw[t * a.k + lane] : 0.0f;
   double s[NQ];
   token_scores<NQ>(v, a.E, lane, a.sigmoid, s);
 #pragma unroll
   for (int q = 0; q < NQ; ++q)
     if (NQ * lane + q < a.E) lds[wave].score[NQ * lane + q] = s[q];
   wave_lds_sync();
-  const int e = lane < a.k ? idx[t * a.k + lane] : -1;
   const bool on = e >= 0 && e < a.E;
   const double sc = on ? lds[wave].score[e] : 0.0;
-  double ds = on ? (double)a.scale * (double)dw[t * a.k + lane] : 0.0;
+  double ds = on ? (double)a.scale * (double)d : 0.0;
   if (a.renorm) {
     const double total = sum8(sc), dot = sum8(ds * sc);   // slots are the first 8 lanes
     ds = on && total != 0.0 ? (ds - dot / total) / total : 0.0;
@@ -512,12 +523,18 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
 #pragma unroll
     for (int q = 0; q < NQ; ++q) g[q] += NQ * lane + q == ej ? dj : 0.0;
   }
+  Floats<NQ> o;
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const int x = NQ * lane + q;
-    if (x < a.E)
-      dlogits[t * a.E + x] = (float)(a.sigmoid ? g[q] * s[q] * (1.0 - s[q]) : s[q] * (g[q] - mean));
+  for (int q = 0; q < NQ; ++q)
+    o[q] = (float)(a.sigmoid ? g[q] * s[q] * (1.0 - s[q]) : s[q] * (g[q] - mean));
+  float* out = dlogits + t * a.E + NQ * lane;
+  if (a.wide) {
+    if (NQ * lane < a.E) *reinterpret_cast<Floats<NQ>*>(out) = o;
+    return;
   }
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+    if (NQ * lane + q < a.E) out[q] = o[q];
 }
 
 // Tokens per workgroup of the choice, which has a histogram row for each: a

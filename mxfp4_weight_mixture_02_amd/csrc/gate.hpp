@@ -12,6 +12,7 @@ struct RouteArgs {
   int groups, top_groups;   // top_groups == groups: no groups
   int share;                // lanes that value a group: a power of two, share * groups <= 64
   int group_lanes;          // lanes whose experts are a whole group, if a power of two, else 0
+  int wide;                 // a lane's experts exist together, at their vector's alignment
   int sigmoid, top2, renorm;
   float scale;
   const float* logits;      // [T, E]

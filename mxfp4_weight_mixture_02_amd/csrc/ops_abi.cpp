@@ -60,7 +60,7 @@ int check_route(const mxmoe_route_opts* o, int64_t T, int32_t E, int32_t k) {
 }
 
 mxmoe::RouteArgs route_args(const mxmoe_route_opts& o, int64_t T, int32_t E, int32_t k,
-                            const float* logits, const float* bias) {
+                            const float* logits, const float* bias, const float* dlogits = nullptr) {
   mxmoe::RouteArgs a{};
   a.T = T;
   a.E = E;
@@ -73,6 +73,7 @@ mxmoe::RouteArgs route_args(const mxmoe_route_opts& o, int64_t T, int32_t E, int
   const int each = E <= 64 ? 1 : E <= 128 ? 2 : 4, per = E / o.groups;
   const int lanes = per % each == 0 ? per / each : 0;
   a.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  a.wide = E % each == 0 && aligned(logits, 4 * each) && aligned(dlogits, 4 * each);
   a.sigmoid = o.score == MXMOE_SCORE_SIGMOID;
   a.top2 = o.group_score == MXMOE_GROUP_TOP2;
   a.renorm = o.renorm != 0;
@@ -206,7 +207,7 @@ int mxmoe_route_backward(const mxmoe_route_opts* opts, int64_t T, int32_t E, int
   if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(dw, 4) || !aligned(dlogits, 4))
     return fail(MXFP4_EINVAL, "tensors must be 4-byte aligned");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  LAUNCH(mxmoe::launch_gate_bwd(route_args(*opts, T, E, k, logits, nullptr), topk_idx, dw, dlogits, s),
+  LAUNCH(mxmoe::launch_gate_bwd(route_args(*opts, T, E, k, logits, nullptr, dlogits), topk_idx, dw, dlogits, s),
          "gate_bwd");
   return ok();
 }

@@ -149,3 +149,19 @@ def test_runs_repeat_and_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(getattr(got, n), getattr(want[i], n)) for n in vars(got))
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (37, 66, 2), (40, 128, 8), (100, 64, 3), (130, 200, 8), (50, 130, 4)])
+def test_unaligned_rows_give_the_same(T, E, k):
+    """Logits (and the gradient's rows) at any 4-byte address: the same values as aligned ones."""
+    print("unaligned", T, E, k, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    off = torch.empty(T * E + 1, device="cuda")[1:].view(T, E)
+    off.copy_(logits)
+    for o in (RouteOptions(), RouteOptions(score="sigmoid")):
+        a, b = moe_route(logits, k, o), moe_route(off, k, o)
+        for n in ("topk_idx", "topk_w", "expert_offsets", "sorted_rows"):
+            assert torch.equal(getattr(a, n), getattr(b, n)), n
+        assert torch.equal(moe_route_backward(logits, a.topk_idx, dw, o), moe_route_backward(off, a.topk_idx, dw, o))
