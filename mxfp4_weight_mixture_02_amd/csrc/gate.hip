@@ -272,15 +272,17 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const Lane<NQ>& mine_o
 #pragma unroll
     for (int q = 0; q < NQ; ++q) key[q] = INT32_MIN;
   }
-  int mine = 0;
+  int mine = 0, k = a.k, l = lane;
+  // compared in the rounds, not in registers kept (and spilled) for all tokens
+  asm volatile("" : "+s"(k), "+v"(l));
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (j >= a.k) break;
+    if (j >= k) break;
     const int32_t top = wave_max(key[0]);
     const int owner = (int)__builtin_ctzll(__ballot(key[0] == top));
     const int e = __builtin_amdgcn_readlane(at[0], owner);
-    if (lane == j) mine = e;
-    if (lane == owner) {
+    if (l == j) mine = e;
+    if (l == owner) {
 #pragma unroll
       for (int q = 0; q + 1 < NQ; ++q) {
         key[q] = key[q + 1];
