@@ -330,6 +330,180 @@ __global__ __launch_bounds__(64 * GATE_W) void gate_kernel(RouteArgs a, int per_
   if (tid < a.E) hist_out[(int64_t)blockIdx.x * a.E + tid] = hist[tid];
 }
 
+// Many tokens: four at a time in a wave, a row of 16 lanes each, lane r with
+// experts NQ r .. NQ r + NQ - 1.  A round of the choice is then eight DPP
+// steps for four tokens instead of six and three scalar reads for each; what
+// it costs more is the sorting of a lane's 4, 8 or 16 experts (networks of
+// 5 and 19 comparisons; of two sorted eights the larger halves are merged).
+// Entries are (key, 255 - expert) in 64 bits, so ties sort by index.
+template <int I, int J, int N>
+__device__ __forceinline__ void exchange(int64_t (&x)[N]) {   // the larger to I
+  const int64_t a = x[I], b = x[J];
+  const bool swap = a < b;
+  x[I] = swap ? b : a;
+  x[J] = swap ? a : b;
+}
+template <int O, int N>
+__device__ __forceinline__ void sort4(int64_t (&x)[N]) {
+  exchange<O, O + 1>(x), exchange<O + 2, O + 3>(x);
+  exchange<O, O + 2>(x), exchange<O + 1, O + 3>(x);
+  exchange<O + 1, O + 2>(x);
+}
+template <int O, int N>
+__device__ __forceinline__ void sort8(int64_t (&x)[N]) {
+  exchange<O, O + 2>(x), exchange<O + 1, O + 3>(x), exchange<O + 4, O + 6>(x), exchange<O + 5, O + 7>(x);
+  exchange<O, O + 4>(x), exchange<O + 1, O + 5>(x), exchange<O + 2, O + 6>(x), exchange<O + 3, O + 7>(x);
+  exchange<O, O + 1>(x), exchange<O + 2, O + 3>(x), exchange<O + 4, O + 5>(x), exchange<O + 6, O + 7>(x);
+  exchange<O + 2, O + 4>(x), exchange<O + 3, O + 5>(x);
+  exchange<O + 1, O + 4>(x), exchange<O + 3, O + 6>(x);
+  exchange<O + 1, O + 2>(x), exchange<O + 3, O + 4>(x), exchange<O + 5, O + 6>(x);
+}
+// The eight largest (all, if there are fewer), descending, in x[0] ..
+template <int N>
+__device__ __forceinline__ void sort_heads(int64_t (&x)[N]) {
+  if constexpr (N == 4) {
+    sort4<0>(x);
+  } else {
+    sort8<0>(x);
+    if constexpr (N == 16) {
+      sort8<8>(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = x[i] < x[15 - i] ? x[15 - i] : x[i];
+      exchange<0, 4>(x), exchange<1, 5>(x), exchange<2, 6>(x), exchange<3, 7>(x);
+      exchange<0, 2>(x), exchange<1, 3>(x), exchange<4, 6>(x), exchange<5, 7>(x);
+      exchange<0, 1>(x), exchange<2, 3>(x), exchange<4, 5>(x), exchange<6, 7>(x);
+    }
+  }
+}
+__device__ __forceinline__ int32_t key_of(int64_t x) { return (int32_t)(x >> 32); }
+
+// Chooses token t's experts, as choose() does; t per row of 16 lanes, r the
+// lane in it.  The sum of a softmax is added in choose()'s order.
+template <int NQ>
+__device__ __forceinline__ int choose_row(const RouteArgs& a, const float* bias, int64_t t, bool on,
+                                          int lane) {
+  constexpr int HEADS = NQ < 8 ? NQ : 8;
+  const int r = lane & 15;
+  const float* row = a.logits + t * a.E;
+  float v[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; q += 4) {
+    const auto y = *reinterpret_cast<const Floats<4>*>(row + min(NQ * r + q, a.E - 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[q + i] = y[i];
+  }
+  int64_t x[NQ];
+  auto enter = [&](int q, double s) {
+    const int e = NQ * r + q;
+    const int32_t key = e < a.E ? choice_key((float)(s + (double)bias[e])) : INT32_MIN;
+    x[q] = (int64_t)((uint64_t)(uint32_t)key << 32 | (uint32_t)(255 - e));
+  };
+  // barriers: interleaved further, the exponentials of 16 experts do not fit
+  // the registers of four waves a SIMD
+  double inv = 0.0;
+  float m = -INFINITY;
+  if (a.sigmoid) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      enter(q, 1.0 / (1.0 + exp(-(double)v[q])));
+      if (NQ > 8 && q % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    double s[NQ], part[4];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      if (NQ * r + q < a.E) m = fmaxf(m, v[q]);
+    m = key_number(row_max(choice_key(m)));
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      part[p] = 0.0;
+#pragma unroll
+      for (int q = p * NQ / 4; q < (p + 1) * NQ / 4; ++q) {
+        s[q] = NQ * r + q < a.E && !(v[q] == -INFINITY) ? exp((double)v[q] - (double)m) : 0.0;
+        part[p] += s[q];
+        if (NQ > 8 && q % 2) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    double sum = sum8((part[0] + part[1]) + (part[2] + part[3]));
+    sum += dpp_swap<8>(sum);
+    inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) enter(q, s[q] * inv);
+  }
+  sort_heads(x);
+  if (a.top_groups < a.groups) {
+    // as lane_group_open, the groups' values from lanes of the token's row
+    int32_t k1 = key_of(x[0]), k2 = key_of(x[1]);
+    auto merge = [&](int32_t o1, int32_t o2) {
+      k2 = max(min(k1, o1), max(k2, o2));
+      k1 = max(k1, o1);
+    };
+    if (a.row_lanes > 1) merge(dpp_swap<1>(k1), dpp_swap<1>(k2));
+    if (a.row_lanes > 2) merge(dpp_swap<2>(k1), dpp_swap<2>(k2));
+    if (a.row_lanes > 4) merge(dpp_swap<4>(k1), dpp_swap<4>(k2));
+    const int32_t key = a.top2 && a.E > a.groups ? choice_key(key_number(k1) + key_number(k2)) : k1;
+    const int g = r / a.row_lanes;
+    int beaten = 0;
+    for (int o = 0; o < a.groups; ++o)
+      beaten += __shfl(key, (lane & 48) + o * a.row_lanes) >= key + (o >= g);
+    if (beaten >= a.top_groups) {
+#pragma unroll
+      for (int q = 0; q < HEADS; ++q) x[q] = (int64_t)((uint64_t)0x80000000u << 32 | (uint32_t)x[q]);
+    }
+  }
+  int mine = 0, k = a.k;
+  asm volatile("" : "+s"(k));   // compared in the rounds
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j >= k) break;
+    const int32_t top = row_max(key_of(x[0]));
+    const int32_t low = row_max(key_of(x[0]) == top ? (int32_t)x[0] : -1);
+    if (r == j) mine = 255 - low;
+    if ((int32_t)x[0] == low) {
+#pragma unroll
+      for (int q = 0; q + 1 < HEADS; ++q) x[q] = x[q + 1];
+      x[HEADS - 1] = (int64_t)((uint64_t)0x80000000u << 32 | 0xFFFFFFFFu);
+    }
+  }
+  // the chosen scores again from their logits, by the same steps
+  double sc = 0.0;
+  if (r < k) {
+    const float l = row[mine];
+    if (a.sigmoid)
+      sc = 1.0 / (1.0 + exp(-(double)l));
+    else
+      sc = (l == -INFINITY ? 0.0 : exp((double)l - (double)m)) * inv;
+  }
+  const double total = a.renorm ? sum8(sc) : 1.0;
+  if (r < k && on) {
+    a.topk_idx[t * k + r] = mine;
+    a.topk_w[t * k + r] = (float)(total == 0.0 ? 0.0 : sc / total * (double)a.scale);
+  }
+  return mine;
+}
+
+template <int NQ>
+__global__ __launch_bounds__(64 * GATE_W) void gate_rows_kernel(RouteArgs a, int per_block,
+                                                                int32_t* __restrict__ hist_out) {
+  __shared__ int32_t hist[256];
+  __shared__ __align__(16) float bias[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15;
+  if (tid < 256) {
+    hist[tid] = 0;
+    bias[tid] = a.bias && tid < a.E ? a.bias[tid] : 0.0f;
+  }
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * per_block;
+  const int n = (int)min((int64_t)per_block, a.T - t0);
+  for (int b = 4 * wave; b < n; b += 4 * GATE_W) {
+    const int i = b + (lane >> 4);
+    const int e = choose_row<NQ>(a, bias, t0 + min(i, n - 1), i < n, lane);
+    if (r < a.k && i < n) atomicAdd(&hist[e], 1);   // counts only: order does not matter
+  }
+  __syncthreads();
+  if (tid < a.E) hist_out[(int64_t)blockIdx.x * a.E + tid] = hist[tid];
+}
+
 // Few tokens (T <= GATE_ONE_TOKENS): choice, offsets and permutation in one
 // workgroup.  A chain of dependent steps, so bound by latency: one token of
 // 256 experts, k = 8 in 5.5 us, against three launches of 3 us and more.
@@ -417,17 +591,22 @@ __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_
     __syncthreads();
     if (c < C) {
       int32_t all = 0, early = 0;
-      for (int b0 = c; b0 < nblk; b0 += 8 * C) {
-        int32_t v[8];   // eight loads under way
+      int b0 = c;
+      auto add = [&](auto loads) {   // of so many workgroups, all under way at once
+        constexpr int N = decltype(loads)::value;
+        int32_t v[N];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = base[(int64_t)min(b0 + u * C, nblk - 1) * a.E + e];
+        for (int u = 0; u < N; ++u) v[u] = base[(int64_t)min(b0 + u * C, nblk - 1) * a.E + e];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < N; ++u) {
           const int b = b0 + u * C;
           all += b < nblk ? v[u] : 0;
           early += b < (int)blockIdx.x ? v[u] : 0;
         }
-      }
+        b0 += N * C;
+      };
+      while (b0 + 16 * C < nblk) add(std::integral_constant<int, 32>{});
+      while (b0 < nblk) add(std::integral_constant<int, 8>{});
       atomicAdd(&cnt[0][e], all);   // whole numbers: order does not matter
       atomicAdd(&cnt[1][e], early);
     }
@@ -569,6 +748,16 @@ hipError_t launch_gate_one(const RouteArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_gate(const RouteArgs& a, int32_t* hist, hipStream_t s) {
+  if (a.row_lanes) {
+    const dim3 grid((unsigned)gate_blocks(a.T)), block(64 * GATE_W);
+    if (a.E <= 64)
+      hipLaunchKernelGGL(gate_rows_kernel<4>, grid, block, 0, s, a, gate_tokens(a.T), hist);
+    else if (a.E <= 128)
+      hipLaunchKernelGGL(gate_rows_kernel<8>, grid, block, 0, s, a, gate_tokens(a.T), hist);
+    else
+      hipLaunchKernelGGL(gate_rows_kernel<16>, grid, block, 0, s, a, gate_tokens(a.T), hist);
+    return hipGetLastError();
+  }
   GATE_LAUNCH(gate_kernel, dim3((unsigned)gate_blocks(a.T)), dim3(64 * GATE_W), 0, s, a,
               gate_tokens(a.T), hist);
 }

@@ -73,6 +73,9 @@ mxmoe::RouteArgs route_args(const mxmoe_route_opts& o, int64_t T, int32_t E, int
   const int each = E <= 64 ? 1 : E <= 128 ? 2 : 4, per = E / o.groups;
   const int lanes = per % each == 0 ? per / each : 0;
   a.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  const int row_each = 4 * each, row_of = per % row_each == 0 ? per / row_each : 0;
+  a.row_lanes = o.top_groups == o.groups ? 16 : (row_of & (row_of - 1)) == 0 ? row_of : 0;
+  if (E % 4 || !aligned(logits, 16)) a.row_lanes = 0;
   a.wide = E % each == 0 && aligned(logits, 4 * each) && aligned(dlogits, 4 * each);
   a.sigmoid = o.score == MXMOE_SCORE_SIGMOID;
   a.top2 = o.group_score == MXMOE_GROUP_TOP2;

@@ -89,6 +89,26 @@ def test_ties_masks_and_non_finite():
         _check(x, 8, o, r.normal(size=96) * 0.1)
 
 
+@pytest.mark.parametrize("T,E,groups", [(67, 256, 8), (67, 256, 16), (67, 256, 1), (45, 128, 4), (45, 128, 16),
+                                        (99, 64, 2), (99, 64, 16), (35, 192, 4), (35, 192, 12), (50, 48, 3),
+                                        (41, 40, 5), (33, 256, 32), (33, 100, 1), (33, 102, 3), (2050, 256, 8)])
+@pytest.mark.parametrize("score,group_score", [("sigmoid", "top2"), ("softmax", "max"), ("sigmoid", "max")])
+def test_ties_and_masks_in_groups(T, E, groups, score, group_score):
+    """Groups of whole and of part lanes; few distinct logits, so that most
+    choices are ties, and rows of -inf, NaN, lowest values and infinities."""
+    r = np.random.default_rng(T + E + groups)
+    x = r.integers(-1, 2, size=(T, E)).astype(np.float32)
+    x[T // 2:] = (r.normal(size=(T - T // 2, E)) * 3).astype(np.float32)
+    x[3], x[4], x[5] = -np.inf, np.nan, np.finfo(np.float32).min
+    x[6, E // 2:], x[7, : E // 2], x[8, ::3] = -np.inf, np.nan, -np.inf
+    x[9, 1::2], x[10, 5], x[11] = np.nan, np.inf, 0.0
+    per = E // groups
+    for top in sorted({1, (groups + 1) // 2, groups}):
+        o = RouteOptions(score=score, groups=groups, top_groups=top, group_score=group_score, scale=1.25)
+        _check(x, min(8, top * per), o, r.integers(-1, 2, size=E) * 0.5)
+        _check(x, min(3, top * per), o)
+
+
 def test_every_token_to_the_same_experts():
     x = np.zeros((3000, 40), np.float32)
     x[:, 7] = 1
