@@ -2,8 +2,9 @@
 // groups of experts, top-k, weights and the permutation plan; and the
 // gradient of the weights with respect to the logits.
 //
-// One wave owns a token: lane l holds experts NQ l .. NQ l + NQ - 1 (NQ =
-// ceil(E / 64)).  Scores are formed in fp64 and the choice is taken on
+// A token belongs to a wave, lane l with experts NQ l .. NQ l + NQ - 1 (NQ =
+// ceil(E / 64)), or to a row of 16 lanes, four tokens in a wave (NQ =
+// ceil(E / 16)).  Scores are formed in fp64 and the choice is taken on
 // c = fp32(s + bias), so that neighbours in the order do not change places
 // with the rounding of an fp32 exponential.  The k largest come from k
 // rounds of a wave maximum over integer keys.
@@ -12,6 +13,11 @@
 #include "common.hpp"
 #include "gate.hpp"
 #include "launch.hpp"
+
+// Sums and products are rounded one by one: a score is the same number where
+// its bias is added and where the weights are formed, and every layout of the
+// choice and of the gradient gives the same bits.
+#pragma clang fp contract(off)
 
 namespace mxmoe {
 
@@ -302,9 +308,10 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const Lane<NQ>& mine_o
 }
 
 // The choice of `per_block` tokens by one workgroup of 16 waves, and the
-// workgroup's histogram of experts.  Bound by vector instructions (about 600 a
-// token, the units 75% busy): 16384 tokens x 256 experts, k = 8 in 25.4 us,
-// 0.8 TB/s of logits; 2048 x 32, k = 4 in 5.5 us.
+// workgroup's histogram of experts.  This form takes what rows of 16 lanes do
+// not (gate_rows_kernel): groups that are not whole lanes of a row, E % 4,
+// unaligned logits.  Bound by vector instructions (about 550 a token): 16384
+// tokens x 256 experts, k = 8 in 25 us.
 constexpr int GATE_W = 16;
 template <int NQ>
 __global__ __launch_bounds__(64 * GATE_W) void gate_kernel(RouteArgs a, int per_block,
@@ -330,12 +337,14 @@ __global__ __launch_bounds__(64 * GATE_W) void gate_kernel(RouteArgs a, int per_
   if (tid < a.E) hist_out[(int64_t)blockIdx.x * a.E + tid] = hist[tid];
 }
 
-// Many tokens: four at a time in a wave, a row of 16 lanes each, lane r with
-// experts NQ r .. NQ r + NQ - 1.  A round of the choice is then eight DPP
-// steps for four tokens instead of six and three scalar reads for each; what
-// it costs more is the sorting of a lane's 4, 8 or 16 experts (networks of
-// 5 and 19 comparisons; of two sorted eights the larger halves are merged).
-// Entries are (key, 255 - expert) in 64 bits, so ties sort by index.
+// Four tokens at a time in a wave, a row of 16 lanes each, lane r with experts
+// NQ r .. NQ r + NQ - 1.  A round of the choice is then eight DPP steps for
+// four tokens instead of six and three scalar reads for each; what it costs
+// more is the sorting of a lane's 4, 8 or 16 experts (networks of 5 and 19
+// comparisons; of two sorted eights the larger halves are merged).  Entries
+// are (key, 255 - expert) in 64 bits, so ties sort by index.  Whole routing,
+// one token a wave against this (us): 16384 x 256, k 8 28.2, 23.7; 65536 x
+// 64, k 6 47.3, 28.9; 2048 x 32, k 4 8.6, 7.6; 100 x 256 10.6, 10.4.
 template <int I, int J, int N>
 __device__ __forceinline__ void exchange(int64_t (&x)[N]) {   // the larger to I
   const int64_t a = x[I], b = x[J];
@@ -377,8 +386,51 @@ __device__ __forceinline__ void sort_heads(int64_t (&x)[N]) {
 }
 __device__ __forceinline__ int32_t key_of(int64_t x) { return (int32_t)(x >> 32); }
 
+// A lane's NQ logits of its row's token (E % 4 == 0).
+template <int NQ>
+__device__ __forceinline__ void load_row(const float* row, int E, int r, float (&v)[NQ]) {
+#pragma unroll
+  for (int q = 0; q < NQ; q += 4) {
+    const auto y = *reinterpret_cast<const Floats<4>*>(row + min(NQ * r + q, E - 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[q + i] = y[i];
+  }
+}
+// Softmax over a row of 16 lanes: s = exp(v - m) in fp64, 0 past E, and the
+// inverse of their sum, added in token_scores()'s order.
+template <int NQ>
+__device__ __forceinline__ double row_softmax(const float (&v)[NQ], int E, int r, float& m, double (&s)[NQ]) {
+  double part[4];
+  m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+    if (NQ * r + q < E) m = fmaxf(m, v[q]);
+  const int32_t top = row_max(choice_key(m));
+  m = key_number(top);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    part[p] = 0.0;
+#pragma unroll
+    for (int q = p * NQ / 4; q < (p + 1) * NQ / 4; ++q) {
+      s[q] = NQ * r + q < E && !(v[q] == -INFINITY) ? exp((double)v[q] - (double)m) : 0.0;
+      part[p] += s[q];
+      // interleaved further, the exponentials of 16 experts do not fit the
+      // registers of four waves a SIMD
+      if (NQ > 8 && q % 2) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  double sum = sum8((part[0] + part[1]) + (part[2] + part[3]));
+  sum += dpp_swap<8>(sum);
+  return sum == 0.0 ? 0.0 : 1.0 / sum;
+}
+// One logit's score, by the same steps.
+__device__ __forceinline__ double one_score(int sigmoid, float l, float m, double inv) {
+  if (sigmoid) return 1.0 / (1.0 + exp(-(double)l));
+  return (l == -INFINITY ? 0.0 : exp((double)l - (double)m)) * inv;
+}
+
 // Chooses token t's experts, as choose() does; t per row of 16 lanes, r the
-// lane in it.  The sum of a softmax is added in choose()'s order.
+// lane in it.
 template <int NQ>
 __device__ __forceinline__ int choose_row(const RouteArgs& a, const float* bias, int64_t t, bool on,
                                           int lane) {
@@ -386,47 +438,24 @@ __device__ __forceinline__ int choose_row(const RouteArgs& a, const float* bias,
   const int r = lane & 15;
   const float* row = a.logits + t * a.E;
   float v[NQ];
-#pragma unroll
-  for (int q = 0; q < NQ; q += 4) {
-    const auto y = *reinterpret_cast<const Floats<4>*>(row + min(NQ * r + q, a.E - 4));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[q + i] = y[i];
-  }
+  load_row<NQ>(row, a.E, r, v);
   int64_t x[NQ];
   auto enter = [&](int q, double s) {
     const int e = NQ * r + q;
     const int32_t key = e < a.E ? choice_key((float)(s + (double)bias[e])) : INT32_MIN;
     x[q] = (int64_t)((uint64_t)(uint32_t)key << 32 | (uint32_t)(255 - e));
   };
-  // barriers: interleaved further, the exponentials of 16 experts do not fit
-  // the registers of four waves a SIMD
   double inv = 0.0;
-  float m = -INFINITY;
+  float m = 0.0f;
   if (a.sigmoid) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      enter(q, 1.0 / (1.0 + exp(-(double)v[q])));
-      if (NQ > 8 && q % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      enter(q, one_score(1, v[q], 0.0f, 0.0));
+      if (NQ > 8 && q % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // registers, as above
     }
   } else {
-    double s[NQ], part[4];
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-      if (NQ * r + q < a.E) m = fmaxf(m, v[q]);
-    m = key_number(row_max(choice_key(m)));
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      part[p] = 0.0;
-#pragma unroll
-      for (int q = p * NQ / 4; q < (p + 1) * NQ / 4; ++q) {
-        s[q] = NQ * r + q < a.E && !(v[q] == -INFINITY) ? exp((double)v[q] - (double)m) : 0.0;
-        part[p] += s[q];
-        if (NQ > 8 && q % 2) __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    double sum = sum8((part[0] + part[1]) + (part[2] + part[3]));
-    sum += dpp_swap<8>(sum);
-    inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+    double s[NQ];
+    inv = row_softmax<NQ>(v, a.E, r, m, s);
 #pragma unroll
     for (int q = 0; q < NQ; ++q) enter(q, s[q] * inv);
   }
@@ -465,15 +494,8 @@ __device__ __forceinline__ int choose_row(const RouteArgs& a, const float* bias,
       x[HEADS - 1] = (int64_t)((uint64_t)0x80000000u << 32 | 0xFFFFFFFFu);
     }
   }
-  // the chosen scores again from their logits, by the same steps
-  double sc = 0.0;
-  if (r < k) {
-    const float l = row[mine];
-    if (a.sigmoid)
-      sc = 1.0 / (1.0 + exp(-(double)l));
-    else
-      sc = (l == -INFINITY ? 0.0 : exp((double)l - (double)m)) * inv;
-  }
+  // the chosen scores again from their logits
+  const double sc = r < k ? one_score(a.sigmoid, row[mine], m, inv) : 0.0;
   const double total = a.renorm ? sum8(sc) : 1.0;
   if (r < k && on) {
     a.topk_idx[t * k + r] = mine;
@@ -482,6 +504,9 @@ __device__ __forceinline__ int choose_row(const RouteArgs& a, const float* bias,
   return mine;
 }
 
+// gate_kernel's work in rows of 16 lanes.  Bound by vector instructions, of
+// which the fp64 scores are about half: 16384 x 256, k 8 in 17.6 us, 2048 x 32
+// in 4.2.
 template <int NQ>
 __global__ __launch_bounds__(64 * GATE_W) void gate_rows_kernel(RouteArgs a, int per_block,
                                                                 int32_t* __restrict__ hist_out) {
@@ -664,7 +689,7 @@ __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_
 // chosen scores' gradients are ds_j = scale (dw_j - sum_i dw_i s_i / S) / S,
 // else ds_j = scale dw_j; sigmoid dl = ds s (1 - s), softmax dl_e =
 // s_e (ds_e - sum_j ds_j s_j).  Scores in fp64, as in the choice, which bounds
-// it: 8192 tokens x 128 experts in 6.6 us, 8.7 MB at 1.3 TB/s.
+// it: 2048 tokens x 256 experts in 4.5 us, 16384 in 17.7 (1.9 TB/s).
 template <int NQ>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_t* __restrict__ idx,
                                                        const float* __restrict__ dw,
@@ -718,11 +743,71 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
     if (NQ * lane + q < a.E) out[q] = o[q];
 }
 
+// The same, four tokens at a time in a wave, a row of 16 lanes each (E % 4 ==
+// 0).  All that a choice changes is at the chosen experts: a lane writes its
+// experts' gradients as if none were chosen to LDS, the slots' lanes put
+// theirs over them.  A sigmoid is needed at the chosen experts alone.  8192 x
+// 128 in 5.7 us (softmax), 16384 x 256 in 12.8 (2.6 TB/s), by sigmoids 7.8
+// (4.3 TB/s, the memory's rate).
+template <int NQ>
+__global__ __launch_bounds__(256) void gate_bwd_rows_kernel(RouteArgs a, const int32_t* __restrict__ idx,
+                                                            const float* __restrict__ dw,
+                                                            float* __restrict__ dlogits) {
+  __shared__ __align__(16) float lds[16][16 * NQ];
+  const int lane = threadIdx.x & 63, r = lane & 15;
+  const int64_t t0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), t = min(t0, a.T - 1);
+  const float* row = a.logits + t * a.E;
+  float v[NQ], *mine = lds[threadIdx.x >> 4];
+  load_row<NQ>(row, a.E, r, v);
+  const int e = r < a.k ? idx[t * a.k + r] : -1;
+  const float d = r < a.k ? dw[t * a.k + r] : 0.0f;
+  const bool on = e >= 0 && e < a.E;
+  const float l = on ? row[e] : 0.0f;
+  double s[NQ], inv = 0.0;
+  float m = 0.0f;
+  if (!a.sigmoid) inv = row_softmax<NQ>(v, a.E, r, m, s);
+  const double sc = on ? one_score(a.sigmoid, l, m, inv) : 0.0;
+  double ds = on ? (double)a.scale * (double)d : 0.0;
+  if (a.renorm) {
+    const double total = sum8(sc), dot = sum8(ds * sc);   // slots are the first 8 lanes
+    ds = on && total != 0.0 ? (ds - dot / total) / total : 0.0;
+  }
+  double mean = 0.0;
+  if (!a.sigmoid) {
+    mean = sum8(ds * sc);
+    mean += dpp_swap<8>(mean);   // 0 past the slots
+  }
+  double g = 0.0;   // of all slots with this lane's expert
+  for (int j = 0; j < a.k; ++j) {
+    const double dj = __shfl(ds, (lane & 48) + j);
+    g += __shfl(e, (lane & 48) + j) == e ? dj : 0.0;
+  }
+#pragma unroll
+  for (int q = 0; q < NQ; q += 4) {
+    Floats<4> o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)   // a NaN's derivative is NaN, chosen or not
+      o[i] = a.sigmoid ? (v[q + i] != v[q + i] ? v[q + i] : 0.0f) : (float)(s[q + i] * inv * (0.0 - mean));
+    *reinterpret_cast<Floats<4>*>(mine + NQ * r + q) = o;
+  }
+  wave_lds_sync();
+  if (on) mine[e] = (float)(a.sigmoid ? g * sc * (1.0 - sc) : sc * (g - mean));
+  wave_lds_sync();
+  if (t0 >= a.T) return;
+  float* out = dlogits + t * a.E;
+#pragma unroll
+  for (int q = 0; q < NQ; q += 4) {   // whole rows of 256 bytes at a time
+    const int x = 4 * r + 16 * q;
+    if (x < a.E) *reinterpret_cast<Floats<4>*>(out + x) = *reinterpret_cast<const Floats<4>*>(mine + x);
+  }
+}
+
 // Tokens per workgroup of the choice, which has a histogram row for each: a
 // wave takes one token while that gives at most four waves a SIMD, then 4, 8
-// or 16.  Whole routing of 16384 tokens x 256 experts with 1, 2, 4, 8, 16 each:
-// 42.9, 34.4, 31.0 (taken), 50.0, 79.9 us: fewer leave the two later launches
-// more histograms, more leave SIMDs empty.
+// or 16.  Whole routing with 1, 2, 4, 8, 16 each (us): 16384 tokens x 256
+// experts 38.4, 27.3, 23.7 (taken), 35.4, 57.8; 4096 x 256 14.6 (taken), 16.3,
+// 20.5, 31.8, 56.5; 65536 x 256 134, 93, 72, 65, 65 (taken).  Fewer leave the
+// two later launches more histograms, more leave SIMDs empty.
 static int gate_tokens(int64_t T) {
   const int64_t per_wave = (T + 4095) / 4096;
   return GATE_W * (int)(per_wave < 16 ? per_wave : 16);
@@ -777,6 +862,19 @@ hipError_t launch_gate_scatter(const RouteArgs& a, const int32_t* base, const in
 
 hipError_t launch_gate_bwd(const RouteArgs& a, const int32_t* idx, const float* dw, float* dlogits,
                            hipStream_t s) {
+  // four tokens a wave from 4096 tokens on (softmax, 256 experts, us: 2048
+  // tokens 4.5 with one a wave, 6.2 with four; 6000: 8.1, 7.9; 16384: 17.7,
+  // 12.8; sigmoid 4.0, 4.0; 7.4, 4.9; 16.0, 7.8)
+  if (a.rows && a.T >= 4096) {
+    const dim3 grid((unsigned)((a.T + 15) / 16)), block(256);
+    if (a.E <= 64)
+      hipLaunchKernelGGL(gate_bwd_rows_kernel<4>, grid, block, 0, s, a, idx, dw, dlogits);
+    else if (a.E <= 128)
+      hipLaunchKernelGGL(gate_bwd_rows_kernel<8>, grid, block, 0, s, a, idx, dw, dlogits);
+    else
+      hipLaunchKernelGGL(gate_bwd_rows_kernel<16>, grid, block, 0, s, a, idx, dw, dlogits);
+    return hipGetLastError();
+  }
   GATE_LAUNCH(gate_bwd_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, idx, dw, dlogits);
 }
 

@@ -12,7 +12,8 @@ struct RouteArgs {
   int groups, top_groups;   // top_groups == groups: no groups
   int share;                // lanes that value a group: a power of two, share * groups <= 64
   int group_lanes;          // lanes whose experts are a whole group, if a power of two, else 0
-  int row_lanes;            // the same of 16 lanes (all 16 without groups), or 0: not in rows of 16
+  int rows;                 // rows of 16 lanes can read (and write) four experts at a time
+  int row_lanes;            // group_lanes of 16 lanes (16 without groups), or 0: not in rows of 16
   int wide;                 // a lane's experts exist together, at their vector's alignment
   int sigmoid, top2, renorm;
   float scale;

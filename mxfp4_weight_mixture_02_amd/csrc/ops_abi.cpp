@@ -75,7 +75,8 @@ mxmoe::RouteArgs route_args(const mxmoe_route_opts& o, int64_t T, int32_t E, int
   a.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
   const int row_each = 4 * each, row_of = per % row_each == 0 ? per / row_each : 0;
   a.row_lanes = o.top_groups == o.groups ? 16 : (row_of & (row_of - 1)) == 0 ? row_of : 0;
-  if (E % 4 || !aligned(logits, 16)) a.row_lanes = 0;
+  a.rows = E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
+  if (!a.rows) a.row_lanes = 0;
   a.wide = E % each == 0 && aligned(logits, 4 * each) && aligned(dlogits, 4 * each);
   a.sigmoid = o.score == MXMOE_SCORE_SIGMOID;
   a.top2 = o.group_score == MXMOE_GROUP_TOP2;

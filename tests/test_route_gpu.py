@@ -146,6 +146,36 @@ def test_gradient_edges():
         assert torch.all(moe_route_backward(*t, o)[3] == 0)
 
 
+@pytest.mark.parametrize("T,E", [(1, 8), (33, 4), (19, 48), (50, 64), (21, 100), (33, 128), (17, 200), (35, 256), (18, 66)])
+@pytest.mark.parametrize("o", range(len(OPTIONS)))
+def test_gradient_edges_in_rows(T, E, o):
+    """Repeated indices, indices outside the experts, rows of -inf, and
+    scores of 0, at sizes of every layout."""
+    print("route grad edges", T, E, o, flush=True)
+    r = np.random.default_rng(T * 3 + E)
+    k = min(8, E)
+    x = (r.normal(size=(T, E)) * 2).astype(np.float32)
+    idx = r.integers(0, E, size=(T, k)).astype(np.int32)   # with repetitions
+    dw = r.normal(size=(T, k)).astype(np.float32)
+    x[T // 3] = -np.inf
+    x[T // 2, 1:] = -np.inf
+    x[T - 1] = -800.0
+    idx[T // 4] = idx[T // 4, 0]
+    t = [torch.from_numpy(v).to(DEV) for v in (x, idx, dw)]
+    g = moe_route_backward(*t, OPTIONS[o]).cpu().numpy()
+    want = ref.dlogits(x, idx, dw, OPTIONS[o])
+    np.testing.assert_allclose(g, want, rtol=1e-7, atol=1e-12 * max(1e-20, np.abs(dw).max() * OPTIONS[o].scale * k))
+    bad = idx.copy()
+    bad[:, 0], bad[:, -1] = -1, E
+    bad[T // 5] = np.iinfo(np.int32).min
+    t[1] = torch.from_numpy(bad).to(DEV)
+    g = moe_route_backward(*t, OPTIONS[o]).cpu().numpy()
+    assert np.all(g[T // 5] == 0) and np.isfinite(g).all()
+    if k > 2:   # the others as without those slots
+        t = [torch.from_numpy(np.ascontiguousarray(v)).to(DEV) for v in (x, bad[:, 1:-1], dw[:, 1:-1])]
+        np.testing.assert_allclose(g, moe_route_backward(*t, OPTIONS[o]).cpu().numpy(), rtol=1e-6, atol=1e-11)
+
+
 def test_runs_repeat_and_replay():
     """The same bits twice, from another stream, and from a captured graph
     replayed on new logits."""
