@@ -1029,11 +1029,17 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
   }
 }
 
-// X's codes fit the LDS of the one-launch form.
-bool fp8_fused_fits(int64_t M, int64_t K) { return M <= 16 && M * fp8_pitch(K) <= FUSED_BYTES; }
+// The one-launch form: X's codes fit its LDS, and rounding them in every
+// workgroup costs less than a launch of its own (5760 x 2880 from HBM, us: 5
+// rows 9.1 against about 10, 8 rows 10.9, 9.8; 2880 x 5760, 5 rows 11.0, 9.5).
+// With few columns, whose product also joins K parts, it may cost more (512 x
+// 2880, 8 rows 7.4, 9.0).
+bool fp8_fused_fits(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 && M * fp8_pitch(K) <= (N < 1024 ? FUSED_BYTES : FUSED_BYTES / 2);
+}
 
 hipError_t launch_fp8_fused(const Fp8Gemm& g, const uint16_t* x, hipStream_t s) {
-  if (!fp8_fused_fits(g.M, g.K)) return hipErrorInvalidValue;
+  if (!fp8_fused_fits(g.M, g.N, g.K)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * SK_NW);
   const bool vec = g.K % 8 == 0 && (reinterpret_cast<uintptr_t>(x) % 16) == 0;
   if (g.out_f32) {

@@ -41,7 +41,7 @@ struct Fp8Gemm {
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32);
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s);
 // the same from bf16 rows x (rounded inside) for few rows
-bool fp8_fused_fits(int64_t M, int64_t K);
+bool fp8_fused_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_fp8_fused(const Fp8Gemm& g, const uint16_t* x, hipStream_t s);
 
 }  // namespace mxmoe

@@ -127,7 +127,7 @@ struct Fp8Layout {
 };
 Fp8Layout fp8_layout(int64_t M, int64_t N, int64_t K, bool w, int out_f32) {
   Fp8Layout L{};
-  if (!w && mxmoe::fp8_fused_fits(M, K)) {   // X never leaves the product's launch
+  if (!w && mxmoe::fp8_fused_fits(M, N, K)) {   // X never leaves the product's launch
     L.total = ALIGN;
     return L;
   }
@@ -327,7 +327,7 @@ int mxmoe_fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const u
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const mxmoe::Fp8Gemm g{M, N, K, ws, ws + L.xs, w_codes, w_scales, 0, bias, out,
                          out_dtype == MXMOE_F32, reinterpret_cast<float*>(ws + L.part)};
-  if (mxmoe::fp8_fused_fits(M, K)) {
+  if (mxmoe::fp8_fused_fits(M, N, K)) {
     LAUNCH(mxmoe::launch_fp8_fused(g, x, s), "fp8_linear");
     return ok();
   }

@@ -140,7 +140,7 @@ def test_integer_products_are_exact(M, N, K):
 # in parts of K, and a product whose last round alone is in parts
 TILES = [(4099, 2881, 100), (2050, 4101, 100), (4097, 1001, 640), (4100, 1001, 99), (2050, 1001, 1300),
          (2049, 1001, 100), (130, 8201, 100), (1030, 1001, 100), (33, 1001, 2881), (20, 2881, 2881),
-         (3, 1030, 384), (16, 2049, 140), (2050, 7250, 2881), (3000, 5500, 2881), (1030, 7250, 5000)]
+         (3, 1030, 384), (16, 2049, 140), (5, 1100, 2880), (8, 1100, 2880), (2050, 7250, 2881), (3000, 5500, 2881), (1030, 7250, 5000)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
@@ -162,6 +162,8 @@ def test_tiles_are_exact(M, N, K):
         W = fp8_quantize(w, rows)
         want = x.double() @ w.double().t()
         assert torch.equal(fp8_matmul(q, W, dtype=torch.float32).double(), want)
+        if rows == 128:
+            assert torch.equal(fp8_linear(x.bfloat16(), W, dtype=torch.float32).double(), want)
         # bf16: a K block's products of a row and a column share a scale and
         # are integers up to 9, of which the scaled matrix core drops nothing
         assert torch.equal(fp8_matmul(q, W), want.float().bfloat16())
