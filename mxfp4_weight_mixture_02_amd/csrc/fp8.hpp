@@ -20,6 +20,10 @@ hipError_t launch_fp8_quantize_rows(const void* x, int x_f32, int64_t rows, int6
 // pitch(rows)], scales [row blocks, scale_pitch(K)]
 hipError_t launch_fp8_quantize_cols(const void* x, int x_f32, int64_t rows, int64_t K,
                                     uint8_t* codes, uint8_t* scales, hipStream_t s);
+// the same of two bf16 matrices of as many rows
+hipError_t launch_fp8_quantize_cols_pair(const uint16_t* x, int64_t K, uint8_t* codes, uint8_t* scales,
+                                         const uint16_t* x2, int64_t K2, uint8_t* codes2,
+                                         uint8_t* scales2, int64_t rows, hipStream_t s);
 // blocks of 128 x 128 -> codes [rows, pitch(K)], scales [K blocks, row blocks]
 hipError_t launch_fp8_quantize_blocks(const void* x, int x_f32, int64_t rows, int64_t K,
                                       uint8_t* codes, uint8_t* scales, hipStream_t s);

@@ -348,8 +348,8 @@ int mxmoe_fp8_linear_dw(int64_t M, int64_t N, int64_t K, const uint16_t* dy, con
   if (rc) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  LAUNCH(mxmoe::launch_fp8_quantize_cols(dy, 0, M, N, ws, ws + L.xs, s), "fp8_quantize_cols");
-  LAUNCH(mxmoe::launch_fp8_quantize_cols(x, 0, M, K, ws + L.w, ws + L.ws, s), "fp8_quantize_cols");
+  LAUNCH(mxmoe::launch_fp8_quantize_cols_pair(dy, N, ws, ws + L.xs, x, K, ws + L.w, ws + L.ws, M, s),
+         "fp8_quantize_cols");
   const mxmoe::Fp8Gemm g{N, K, M, ws, ws + L.xs, ws + L.w, ws + L.ws, 1, nullptr, dw, 1,
                          reinterpret_cast<float*>(ws + L.part)};
   LAUNCH(mxmoe::launch_fp8_gemm(g, s), "fp8_matmul");
