@@ -215,3 +215,18 @@ def test_unaligned_rows_give_the_same(T, E, k):
         for n in ("topk_idx", "topk_w", "expert_offsets", "sorted_rows"):
             assert torch.equal(getattr(a, n), getattr(b, n)), n
         assert torch.equal(moe_route_backward(logits, a.topk_idx, dw, o), moe_route_backward(off, a.topk_idx, dw, o))
+
+
+@pytest.mark.parametrize("E,k", [(32, 4), (64, 8), (100, 6), (128, 8), (200, 8), (256, 8), (130, 3)])
+@pytest.mark.parametrize("o", [RouteOptions(), RouteOptions(renorm=False), RouteOptions(score="sigmoid", scale=2.5)])
+def test_a_tokens_routing_and_gradient_are_its_own(E, k, o):
+    """The same bits for a token among few and among many."""
+    print("batch", E, k, o, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(E)
+    x, dw = torch.randn(4200, E, generator=g, device=DEV) * 3, torch.randn(4200, k, generator=g, device=DEV)
+    many = moe_route(x, k, o)
+    d = moe_route_backward(x, many.topk_idx, dw, o)
+    for n in (1, 32, 33, 500):
+        few = moe_route(x[:n].contiguous(), k, o)
+        assert torch.equal(few.topk_idx, many.topk_idx[:n]) and torch.equal(few.topk_w, many.topk_w[:n])
+        assert torch.equal(moe_route_backward(x[:n].contiguous(), few.topk_idx, dw[:n].contiguous(), o), d[:n])
