@@ -685,11 +685,32 @@ __global__ __launch_bounds__(256) void gate_scatter_kernel(RouteArgs a, int per_
   }
 }
 
-// dlogits of one token per wave.  With w = scale * s / S (renorm) the
-// chosen scores' gradients are ds_j = scale (dw_j - sum_i dw_i s_i / S) / S,
-// else ds_j = scale dw_j; sigmoid dl = ds s (1 - s), softmax dl_e =
-// s_e (ds_e - sum_j ds_j s_j).  Scores in fp64, as in the choice, which bounds
-// it: 2048 tokens x 256 experts in 4.5 us, 16384 in 17.7 (1.9 TB/s).
+// A slot's share of the gradient.  With w = scale * s the chosen scores'
+// gradients are ds_j = scale dw_j; sigmoid dl = ds s (1 - s), softmax dl_e =
+// s_e (ds_e - sum_j ds_j s_j).  Renormalised weights w_j = s_j / S take p_j =
+// ds_j s_j = scale w_j (dw_j - sum_i dw_i w_i) instead: ds_j itself has a
+// division by S and is infinite where the chosen scores are below 2^-1022
+// though the weights are ordinary.  Sigmoid dl = p (1 - s), softmax dl_e = p_e
+// - s_e sum_j p_j, and that sum is 0 since the w_j add up to 1.  Returns ds_j,
+// or p_j with renorm (0 in slots that are not `on`); slots are the first 8
+// lanes of a row.
+__device__ __forceinline__ double slot_gradient(const RouteArgs& a, bool on, double sc, float dw) {
+  const double d = on ? (double)a.scale * (double)dw : 0.0;
+  if (!a.renorm) return d;
+  const double total = sum8(sc), w = total == 0.0 ? 0.0 : sc / total, dot = sum8(d * w);
+  return on ? w * (d - dot) : 0.0;
+}
+// The gradient of an expert with score s and slot sum g; mean = sum_j ds_j s_j,
+// 0 with renorm.  A NaN score's gradient is NaN, chosen or not.  (g = 0: s
+// (0 - mean) in both forms.)
+template <bool RENORM>
+__device__ __forceinline__ float expert_gradient(int sigmoid, double g, double s, double mean) {
+  if (RENORM) return (float)(sigmoid ? g * (1.0 - s) : g - s * mean);
+  return (float)(sigmoid ? g * s * (1.0 - s) : s * (g - mean));
+}
+
+// dlogits of one token per wave.  Scores in fp64, as in the choice, which
+// bounds it: 2048 tokens x 256 experts in 4.5 us, 16384 in 17.7 (1.9 TB/s).
 template <int NQ>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_t* __restrict__ idx,
                                                        const float* __restrict__ dw,
@@ -710,12 +731,8 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
   wave_lds_sync();
   const bool on = e >= 0 && e < a.E;
   const double sc = on ? lds[wave].score[e] : 0.0;
-  double ds = on ? (double)a.scale * (double)d : 0.0;
-  if (a.renorm) {
-    const double total = sum8(sc), dot = sum8(ds * sc);   // slots are the first 8 lanes
-    ds = on && total != 0.0 ? (ds - dot / total) / total : 0.0;
-  }
-  const double mean = a.sigmoid ? 0.0 : wave_sum(ds * sc);   // 0 past the slots
+  const double ds = slot_gradient(a, on, sc, d);
+  const double mean = a.sigmoid || a.renorm ? 0.0 : wave_sum(ds * sc);   // 0 past the slots
   double g[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) g[q] = 0.0;
@@ -730,9 +747,13 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
     for (int q = 0; q < NQ; ++q) g[q] += NQ * lane + q == ej ? dj : 0.0;
   }
   Floats<NQ> o;
+  if (a.renorm) {
 #pragma unroll
-  for (int q = 0; q < NQ; ++q)
-    o[q] = (float)(a.sigmoid ? g[q] * s[q] * (1.0 - s[q]) : s[q] * (g[q] - mean));
+    for (int q = 0; q < NQ; ++q) o[q] = expert_gradient<true>(a.sigmoid, g[q], s[q], mean);
+  } else {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) o[q] = expert_gradient<false>(a.sigmoid, g[q], s[q], mean);
+  }
   float* out = dlogits + t * a.E + NQ * lane;
   if (a.wide) {
     if (NQ * lane < a.E) *reinterpret_cast<Floats<NQ>*>(out) = o;
@@ -767,13 +788,9 @@ __global__ __launch_bounds__(256) void gate_bwd_rows_kernel(RouteArgs a, const i
   float m = 0.0f;
   if (!a.sigmoid) inv = row_softmax<NQ>(v, a.E, r, m, s);
   const double sc = on ? one_score(a.sigmoid, l, m, inv) : 0.0;
-  double ds = on ? (double)a.scale * (double)d : 0.0;
-  if (a.renorm) {
-    const double total = sum8(sc), dot = sum8(ds * sc);   // slots are the first 8 lanes
-    ds = on && total != 0.0 ? (ds - dot / total) / total : 0.0;
-  }
+  const double ds = slot_gradient(a, on, sc, d);
   double mean = 0.0;
-  if (!a.sigmoid) {
+  if (!a.sigmoid && !a.renorm) {
     mean = sum8(ds * sc);
     mean += dpp_swap<8>(mean);   // 0 past the slots
   }
@@ -791,7 +808,7 @@ __global__ __launch_bounds__(256) void gate_bwd_rows_kernel(RouteArgs a, const i
     *reinterpret_cast<Floats<4>*>(mine + NQ * r + q) = o;
   }
   wave_lds_sync();
-  if (on) mine[e] = (float)(a.sigmoid ? g * sc * (1.0 - sc) : sc * (g - mean));
+  if (on) mine[e] = a.renorm ? expert_gradient<true>(a.sigmoid, g, sc, mean) : expert_gradient<false>(a.sigmoid, g, sc, mean);
   wave_lds_sync();
   if (t0 >= a.T) return;
   float* out = dlogits + t * a.E;
