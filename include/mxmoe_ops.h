@@ -186,7 +186,8 @@ int mxmoe_swiglu8_backward(const uint8_t* codes, const uint8_t* scales, const ui
                            int64_t R, int64_t I, float alpha, float limit, uint16_t* dh,
                            uint16_t* a, void* stream);
 /* h bf16 [R, 2I], the checkpoint's values (exact unless below bf16's
- * subnormals), and their activation a bf16 [R, I]; either may be NULL. */
+ * subnormals; a magnitude from 2^128 - 2^123 on has rounded to 2^128 and is an
+ * infinity), and their activation a bf16 [R, I]; either may be NULL. */
 int mxmoe_swiglu8_restore(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t I,
                           float alpha, float limit, uint16_t* h, uint16_t* a, void* stream);
 

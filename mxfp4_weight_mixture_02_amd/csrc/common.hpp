@@ -106,12 +106,15 @@ __device__ __forceinline__ float swiglu(float g, float u, float alpha, float lim
 // sigmoid factor is 0 times an infinity, gets none too); the clamps are
 // single median-of-three operations, alpha * gc is shared by the
 // sigmoid and the gate derivative, and both (uc + 1) ds and
-// 1 + alpha gc (1 - s) are fused multiply-adds.
+// 1 + alpha gc (1 - s) are fused multiply-adds.  WIDE: gates up to the end of
+// the range, where alpha gc may be no finite float (for alpha 1.702 from 2e38
+// on): its infinity would be multiplied by the 0 of s or of 1 - s.
+template <bool WIDE = false>
 __device__ __forceinline__ void swiglu_grad(float g, float u, float da, float alpha, float limit,
                                             float* dg, float* du) {
   const float gc = __builtin_amdgcn_fmed3f(g, -3.402823466e38f, limit);
   const float uc = __builtin_amdgcn_fmed3f(u, -limit, limit);
-  const float ag = alpha * gc;
+  const float ag = WIDE ? __builtin_amdgcn_fmed3f(alpha * gc, -3.402823466e38f, 3.402823466e38f) : alpha * gc;
   const float sig = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(ag * -1.4426950408889634f));
   const float ds = da * sig;
   *dg = (gc == g) ? fmaf(ds, uc, ds) * fmaf(ag, 1.0f - sig, 1.0f) : 0.0f;

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(256) void swiglu8_bwd_kernel(const u32x2* __restric
   for (int p = 0; p < 4; ++p) {
     const float x = __uint_as_float((p & 1) ? (d[p >> 1] & 0xFFFF0000u) : (d[p >> 1] << 16));
     float dg, du;
-    swiglu_grad(v[2 * p], v[2 * p + 1], x, alpha, limit, &dg, &du);
+    swiglu_grad<true>(v[2 * p], v[2 * p + 1], x, alpha, limit, &dg, &du);
     o[p] = pack_bf16x2(dg, du);
   }
   dh[i] = o;
