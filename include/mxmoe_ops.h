@@ -42,7 +42,7 @@ extern "C" {
  * is scale * s (the bias takes part in the choice alone); with it, weights
  * of a token whose chosen scores are all 0 are 0.  A token whose logits are
  * all -inf has scores 0.  A token's routing and gradient have the same bits
- * whatever the other tokens and T are. */
+ * whatever the other tokens and T are (a NaN is 0x7FC00000). */
 typedef struct mxmoe_route_opts {
   int32_t score;
   int32_t groups;

@@ -95,6 +95,12 @@ __device__ __forceinline__ double wave_sum(double v) {
   return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
 
+// A result, with one NaN for all: the layouts reach a NaN by different
+// operands, whose signs and payloads it would keep.
+__device__ __forceinline__ float one_nan(float v) {
+  return (__float_as_uint(v) & 0x7FFFFFFFu) > 0x7F800000u ? __uint_as_float(0x7FC00000u) : v;
+}
+
 // LDS of one wave's token.
 struct TokenLds {
   double score[256];
@@ -302,7 +308,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const Lane<NQ>& mine_o
   const double total = a.renorm ? sum8(sc) : 1.0;
   if (lane < a.k) {
     a.topk_idx[t * a.k + lane] = mine;
-    a.topk_w[t * a.k + lane] = (float)(total == 0.0 ? 0.0 : sc / total * (double)a.scale);
+    a.topk_w[t * a.k + lane] = one_nan((float)(total == 0.0 ? 0.0 : sc / total * (double)a.scale));
   }
   return mine;
 }
@@ -499,7 +505,7 @@ __device__ __forceinline__ int choose_row(const RouteArgs& a, const float* bias,
   const double total = a.renorm ? sum8(sc) : 1.0;
   if (r < k && on) {
     a.topk_idx[t * k + r] = mine;
-    a.topk_w[t * k + r] = (float)(total == 0.0 ? 0.0 : sc / total * (double)a.scale);
+    a.topk_w[t * k + r] = one_nan((float)(total == 0.0 ? 0.0 : sc / total * (double)a.scale));
   }
   return mine;
 }
@@ -754,6 +760,13 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(RouteArgs a, const int32_
 #pragma unroll
     for (int q = 0; q < NQ; ++q) o[q] = expert_gradient<false>(a.sigmoid, g[q], s[q], mean);
   }
+  float any = o[0];
+#pragma unroll
+  for (int q = 1; q < NQ; ++q) any += o[q];
+  if (any != any) {   // hardly ever
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) o[q] = one_nan(o[q]);
+  }
   float* out = dlogits + t * a.E + NQ * lane;
   if (a.wide) {
     if (NQ * lane < a.E) *reinterpret_cast<Floats<NQ>*>(out) = o;
@@ -804,11 +817,16 @@ __global__ __launch_bounds__(256) void gate_bwd_rows_kernel(RouteArgs a, const i
     Floats<4> o;
 #pragma unroll
     for (int i = 0; i < 4; ++i)   // a NaN's derivative is NaN, chosen or not
-      o[i] = a.sigmoid ? (v[q + i] != v[q + i] ? v[q + i] : 0.0f) : (float)(s[q + i] * inv * (0.0 - mean));
+      o[i] = a.sigmoid ? (v[q + i] != v[q + i] ? __uint_as_float(0x7FC00000u) : 0.0f) : (float)(s[q + i] * inv * (0.0 - mean));
     *reinterpret_cast<Floats<4>*>(mine + NQ * r + q) = o;
   }
+  if (!(inv - inv == 0.0 && mean - mean == 0.0))   // softmax: a row of NaN, or with some
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) mine[NQ * r + q] = one_nan(mine[NQ * r + q]);
   wave_lds_sync();
-  if (on) mine[e] = a.renorm ? expert_gradient<true>(a.sigmoid, g, sc, mean) : expert_gradient<false>(a.sigmoid, g, sc, mean);
+  if (on)
+    mine[e] = one_nan(a.renorm ? expert_gradient<true>(a.sigmoid, g, sc, mean)
+                               : expert_gradient<false>(a.sigmoid, g, sc, mean));
   wave_lds_sync();
   if (t0 >= a.T) return;
   float* out = dlogits + t * a.E;
