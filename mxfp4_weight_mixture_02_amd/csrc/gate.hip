@@ -910,6 +910,17 @@ hipError_t launch_gate_bwd(const RouteArgs& a, const int32_t* idx, const float* 
       hipLaunchKernelGGL(gate_bwd_rows_kernel<16>, grid, block, 0, s, a, idx, dw, dlogits);
     return hipGetLastError();
   }
+  // a launch has 2^32 - 1 threads, a token takes 64
+  constexpr int64_t PART = int64_t(1) << 25;
+  if (a.T > PART) {
+    RouteArgs b = a, rest = a;
+    b.T = PART;
+    rest.T = a.T - PART;
+    rest.logits += PART * a.E;
+    const hipError_t e = launch_gate_bwd(b, idx, dw, dlogits, s);
+    if (e != hipSuccess) return e;
+    return launch_gate_bwd(rest, idx + PART * a.k, dw + PART * a.k, dlogits + PART * a.E, s);
+  }
   GATE_LAUNCH(gate_bwd_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, idx, dw, dlogits);
 }
 
