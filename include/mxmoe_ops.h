@@ -77,7 +77,8 @@ int mxmoe_route_backward(const mxmoe_route_opts* opts, int64_t T, int32_t E, int
 /* Router logits as the expert block forms them: fp32 [T, E] = x W_r^T + b_r
  * with x bf16 [T, H], router_w fp32 [E, H], router_b fp32 [E] or NULL,
  * products summed in fp64 and rounded once.  H % 32 == 0, H <= 5120, E <=
- * 256, T * H < 2^31, T * E < 2^30; x and router_w 16-byte aligned. */
+ * 256, T * H < 2^31, ceil(T / 16) * ceil(E / 16) < 2^22; x and router_w 16-byte
+ * aligned. */
 int mxmoe_router_logits(int64_t T, int64_t H, int32_t E, const uint16_t* x, const float* router_w,
                         const float* router_b, float* logits, void* stream);
 
@@ -116,8 +117,9 @@ int mxmoe_backward_routed(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w
  * Scale of a block: the smallest 2^e with its largest finite magnitude at
  * most 448 * 2^e, e in [-127, 127] (all zeros: -127).  Element: the nearest
  * E4M3 value to x / 2^e, ties to even; a non-finite x has the NaN code.
- * rows and K are >= 1, K <= 2^22, rows < 2^27, rows * Kp < 2^35; a
- * product's M * N < 2^37. */
+ * rows and K are >= 1, K <= 2^22, rows < 2^27, (rows + 127) * Kp < 2^35; a
+ * product's M * N < 2^37 (both rounded up to 128), and N <= 2^27 - 16 where
+ * M <= 16. */
 
 /* Quantizers.  x [rows, K], dtype MXMOE_F32 or MXMOE_BF16 (any alignment of
  * the dtype's; 16 bytes and K % 8 == 0 run faster).  block_rows 1 or 128. */
@@ -174,7 +176,7 @@ size_t mxmoe_fp8_linear_dw_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * -limit or neither), so a backward pass from the checkpoint takes the
  * forward's clamp decisions.  Non-finite elements have the NaN code.
  * R >= 1, I % 16 == 0, alpha finite, limit > 0 and finite; tensors 16-byte
- * aligned; R * 2I < 2^35. */
+ * aligned; R * 2I <= 2^35 - 2048. */
 
 /* a bf16 [R, I] out (NULL: the checkpoint alone). */
 int mxmoe_swiglu8_forward(const uint16_t* h, int64_t R, int64_t I, float alpha, float limit,

@@ -734,7 +734,7 @@ int mxmoe_router_logits(int64_t T, int64_t H, int32_t E, const uint16_t* x, cons
                 (long long)H, E);
   if (T >= (int64_t(1) << 31) / H)
     return fail(MXFP4_EUNSUPPORTED, "T*H elements exceed int32 (T=%lld H=%lld)", (long long)T, (long long)H);
-  if (T * ((E + 15) / 16) >= (int64_t(1) << 26))   // 1024 threads for 16 x 16 logits, 2^32 in a launch
+  if (!mxmoe::launchable((T + 15) / 16 * ((E + 15) / 16), 1024))   // a workgroup for 16 x 16 logits
     return fail(MXFP4_EUNSUPPORTED, "T=%lld tokens of E=%d logits are too many", (long long)T, E);
   if (!x || !router_w || !logits) return fail(MXFP4_EINVAL, "x, router_w and logits are required");
   if (!aligned(x, 16) || !aligned(router_w, 16) || !aligned(router_b, 4) || !aligned(logits, 4))

@@ -20,6 +20,10 @@ inline int hip_status(hipError_t e, const char* what) {
   return MXFP4_OK;
 }
 
+// Whether a launch can have so many workgroups of `threads` threads: 2^32 - 1
+// threads in all.
+inline bool launchable(int64_t blocks, int threads) { return blocks <= ((int64_t(1) << 32) - 1) / threads; }
+
 // With mxfp4_moe_kernel_timing on, an event recorded on s before the launch
 // (else nullptr), and the one after it.
 hipEvent_t timing_begin(hipStream_t s);

@@ -14,6 +14,7 @@ namespace {
 
 using mxmoe::aligned;
 using mxmoe::fail;
+using mxmoe::launchable;
 using mxmoe::ok;
 
 constexpr size_t ALIGN = 256;
@@ -33,7 +34,6 @@ int check_route_sizes(int64_t T, int32_t E, int32_t k) {
     return fail(MXFP4_EINVAL, "T, E and k must be >= 1 (T=%lld E=%d k=%d)", (long long)T, E, k);
   if (E > 256) return fail(MXFP4_EUNSUPPORTED, "E=%d > 256", E);
   if (k > E || k > 8) return fail(MXFP4_EUNSUPPORTED, "k=%d must be <= min(E, 8)", k);
-  // the gradient launches 64 threads a token, and a launch has 2^32
   if (T >= (int64_t(1) << 26))
     return fail(MXFP4_EUNSUPPORTED, "T=%lld tokens (must be < 2^26)", (long long)T);
   return MXFP4_OK;
@@ -117,6 +117,10 @@ int check_product(int64_t M, int64_t N, int64_t K) {
   if (!rc) rc = check_fp8(N, K, "W");
   if (!rc && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 23))
     rc = fail(MXFP4_EUNSUPPORTED, "M=%lld N=%lld: too many tiles", (long long)M, (long long)N);
+  // few rows: a workgroup of 512 threads for 16 rows of W
+  if (!rc && M <= 16 && !launchable((N + 15) / 16, 512))
+    rc = fail(MXFP4_EUNSUPPORTED, "M=%lld N=%lld: N must be <= 2^27 - 16 for up to 16 rows", (long long)M,
+              (long long)N);
   return rc;
 }
 
@@ -148,9 +152,10 @@ int check_swiglu8(int64_t R, int64_t I, float alpha, float limit) {
   if (R < 1 || I < 1)
     return fail(MXFP4_EINVAL, "R and I must be >= 1 (R=%lld I=%lld)", (long long)R, (long long)I);
   if (I % 16) return fail(MXFP4_EUNSUPPORTED, "I=%lld is not a multiple of 16", (long long)I);
-  // a thread for 8 elements of h, and a launch has 2^32
-  if (I >= (int64_t(1) << 32) || R >= (int64_t(1) << 34) / I)
-    return fail(MXFP4_EUNSUPPORTED, "R=%lld I=%lld: R * 2I elements must be < 2^35", (long long)R, (long long)I);
+  // a thread for 8 elements of h
+  if (I >= (int64_t(1) << 32) || R >= (int64_t(1) << 34) / I || !launchable((R * I / 4 + 255) / 256, 256))
+    return fail(MXFP4_EUNSUPPORTED, "R=%lld I=%lld: R * 2I elements must be <= 2^35 - 2048", (long long)R,
+                (long long)I);
   if (!finite(alpha) || !finite(limit) || !(limit > 0.0f))
     return fail(MXFP4_EINVAL, "alpha must be finite and limit finite and > 0");
   return MXFP4_OK;
