@@ -320,8 +320,16 @@ class SavedState:
 
 
 def _bf16_state(saved):
-    if not isinstance(saved, SavedState):
+    """Refuse what has no buffers for a forward to write (a SavedState8 among
+    them); a program's own class with SavedState's methods will do."""
+    if not (hasattr(saved, "check_shapes") and hasattr(saved, "struct")):
         raise ValueError(f"saved: a forward writes a SavedState, got {type(saved).__name__}")
+
+
+def _restored(saved):
+    """The bf16 state that a backward reads: a SavedState8 makes one, a
+    program's own state without `restore` is one."""
+    return saved.restore() if hasattr(saved, "restore") else saved
 
 
 class Workspace:
@@ -438,7 +446,7 @@ def mxfp4_moe_backward_dx(layer: MoeLayer, saved: SavedState, dy: torch.Tensor,
     if dx is not None:
         _shape(dx, (T, layer.H), torch.bfloat16, "dx")
     saved.check_shapes(layer, T)
-    saved = saved.restore()
+    saved = _restored(saved)
     grads = {}
     for name, base, on in (("dA", layer.lora_A, True), ("dB", layer.lora_B, True),
                            ("dA_gu", layer.lora_gu_A, True), ("dB_gu", layer.lora_gu_B, True)):
@@ -495,7 +503,7 @@ def mxfp4_moe_backward(layer: MoeLayer, saved: SavedState, x: torch.Tensor, dy: 
     _shape(dy, (T, layer.H), torch.bfloat16, "dy")
     _shape(x, (T, layer.H), torch.bfloat16, "x")
     saved.check_shapes(layer, T)
-    saved = saved.restore()
+    saved = _restored(saved)
     _dev(dy, torch.bfloat16, "dy")
     _dev(x, torch.bfloat16, "x")
     E, H, I = layer.E, layer.H, layer.I

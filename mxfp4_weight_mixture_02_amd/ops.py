@@ -290,7 +290,7 @@ def mxfp4_moe_backward_routed(layer: MoeLayer, saved, dy: torch.Tensor, x: torch
     _shape(dy, (T, H), torch.bfloat16, "dy")
     _shape(x, (T, H), torch.bfloat16, "x", optional=not base and layer.lora_gu_A is None)
     saved.check_shapes(layer, T)
-    saved = saved.restore()
+    saved = native._restored(saved)
     dev = _layer_device(layer, dy=dy, x=x, h=saved.h, a=saved.a, lora_v=saved.lora_v, lora_vg=saved.lora_vg,
                         **_fields(saved))
     f32 = dict(dtype=torch.float32, device=dev)
