@@ -252,7 +252,10 @@ class MoeLayer:
             _shape(self.lora_gu_B, (E, 2 * I, r), bf, "lora_gu_B")
 
     def weights(self, routed=False):
-        self.check_shapes(routed)
+        if routed:
+            self.check_shapes(routed=True)
+        else:
+            self.check_shapes()
         _dev(self.router_w, torch.float32, "router_w")
         _dev(self.router_b, torch.float32, "router_b")
         for n in ("gu_codes", "gu_scales", "dn_codes", "dn_scales"):

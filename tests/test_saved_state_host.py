@@ -48,3 +48,17 @@ def test_states_that_a_forward_cannot_write():
                 call()
     with pytest.raises(ValueError, match="expert_offsets"):
         mxfp4_moe_forward(layer, x, saved=Own(th._saved(5, expert_offsets=st.expert_offsets[:-1])))
+
+
+def test_a_layers_own_check():
+    """A layer class whose check takes no argument, as before routed calls."""
+    class Layer(th.MoeLayer):
+        def check_shapes(self):
+            super().check_shapes()
+
+    base = th._layer()
+    layer = Layer(**{n: getattr(base, n) for n in base.__dataclass_fields__})
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        layer.weights()
+    with pytest.raises(ValueError, match="router_w is required"):
+        Layer(**{**{n: getattr(base, n) for n in base.__dataclass_fields__}, "router_w": None}).weights()
