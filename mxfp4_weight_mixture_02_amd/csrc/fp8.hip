@@ -368,19 +368,25 @@ struct Fp8Tile {
 // compiler makes every later LDS read wait for every such copy in flight
 // that it cannot prove to go elsewhere, and with a ring of stages it can
 // prove nothing.  The kernel waits itself (fp8_wait) before it reads a
-// stage.  A copy has no output register; its address is read at issue.
+// stage.  A copy has no output register; its address is read at issue.  m0
+// is a reserved register, which the compiler writes right before each use of
+// its own: the clobber keeps such a pair on one side of a copy (none of these
+// kernels has one), and its warning says only that m0 is not saved.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int BYTES>
 __device__ __forceinline__ void lds_copy(u32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
   if (BYTES == 16)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory");
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "m0", "memory");
   else if (BYTES == 4)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory");
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "m0", "memory");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory");
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "m0", "memory");
 }
+#pragma clang diagnostic pop
 // Raw buffer of `bytes` bytes at p (a wave-uniform pointer).
 __device__ __forceinline__ u32x4 buffer_of(const uint8_t* p, int64_t bytes) {
   const uint64_t a = (uint64_t)(uintptr_t)p;
