@@ -136,8 +136,9 @@ def test_integer_products_are_exact(M, N, K):
 
 
 
-# every tile of the products, with rows and columns past its edge, whole and
-# in parts of K, and a product whose last round alone is in parts
+# every tile of the products, with rows and columns past its edge, whole; parts
+# of K in the smaller tiles, and a product whose last round alone is in parts
+# (fp8_parts.py has every tile that is taken in parts)
 TILES = [(4099, 2881, 100), (2050, 4101, 100), (4097, 1001, 640), (4100, 1001, 99), (2050, 1001, 1300),
          (2049, 1001, 100), (130, 8201, 100), (1030, 1001, 100), (33, 1001, 2881), (20, 2881, 2881),
          (3, 1030, 384), (16, 2049, 140), (5, 1100, 2880), (8, 1100, 2880), (2050, 7250, 2881), (3000, 5500, 2881), (1030, 7250, 5000)]
