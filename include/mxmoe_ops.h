@@ -114,6 +114,8 @@ int mxmoe_backward_routed(const mxfp4_moe_dims* dims, const mxfp4_moe_weights* w
  *                             bytes past `rows` are not used
  *          block_rows == 128: [Kp / 128, ceil(rows / 128)], one scale for
  *                             128 x 128 elements
+ * Scales are powers of two alone: a matrix with fp32 scales has to be
+ * dequantized and quantized here again.
  * Scale of a block: the smallest 2^e with its largest finite magnitude at
  * most 448 * 2^e, e in [-127, 127] (all zeros: -127).  Element: the nearest
  * E4M3 value to x / 2^e, ties to even; a non-finite x has the NaN code.

@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256) void fp8_cols_kernel(const void* __restrict__ 
   fp8_cols<F32, VEC>(x, rows, K, pitch, spitch, ctiles, codes, scales, blockIdx.x, t);
 }
 // Two bf16 matrices of the same rows in one launch: the first `blocks`
-// workgroups have a.  A launch is 4.7 us at the least, whatever its size.
+// workgroups have a.  A launch of its own is 3 us more of a whole dW (5760 x
+// 2880 x 4093: 161 us, 158).
 struct Fp8Cols {
   const void* x;
   int64_t K, spitch;
@@ -556,11 +557,12 @@ __device__ __forceinline__ void fp8_tile_at(int item, int ntiles, int mtiles, in
 // 16-byte chunks, and chunk c of fragment row r sits at slot c ^ (r / 2 % 8):
 // the rows that a read touches in one cycle spread over all banks.
 //
-// 8192^3 in 256 x 256 tiles: 503 us, 2190 TFLOP/s of bf16 results and 1390 of
-// fp32 results (791 us); 4096^3 56 us, 2450.  What bounds it: a K block's
-// matrix instructions and its LDS traffic (192 KB of fragments, 64 KB of
-// copies) take 2048 cycles each, so the two have to overlap fully; the matrix
-// cores are busy 57% of the time at the 1.8 GHz that the card then holds.
+// 8192^3 in 256 x 256 tiles, bf16 results: 410 us (2680 TFLOP/s) on a cool card,
+// 465 to 503 (2190) at the clock it holds after other such work; fp32 results
+// 770 to 810 us; 4096^3 56 us, 2450.  The rest was measured at 503.  What
+// bounds it: a K block's matrix instructions and its LDS traffic (192 KB of
+// fragments, 64 KB of copies) take 2048 cycles each, so the two have to overlap
+// fully; the matrix cores are busy 57% of the time at the 1.8 GHz of that run.
 // Without the products the same loop takes 307 us, without the copies 413,
 // without the LDS reads 456.  Tried and dropped: four waves of 128 x 128 (537
 // us), fragments of the next K block read ahead (registers spill), workgroups
