@@ -1,7 +1,8 @@
 /*
  * mxmoe_ops.h -- C ABI of the operators beside the MXFP4 expert block of
  * mxfp4_moe.h: routing with its gradient and the block on a given routing,
- * dense products in 8-bit floating point, and 8-bit activation checkpoints.
+ * dense products in 8-bit floating point, 8-bit activation checkpoints, and
+ * the norm before a layer.
  *
  * Conventions as in mxfp4_moe.h: dense row-major tensors in device memory
  * owned by the caller, bf16 as uint16_t bit patterns, `stream` a
@@ -194,6 +195,33 @@ int mxmoe_swiglu8_backward(const uint8_t* codes, const uint8_t* scales, const ui
  * infinity), and their activation a bf16 [R, I]; either may be NULL. */
 int mxmoe_swiglu8_restore(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t I,
                           float alpha, float limit, uint16_t* h, uint16_t* a, void* stream);
+
+/* ---------------------------------------------------- the norm before a layer */
+
+/* Root-mean-square norm of the rows of x [T, H], dtype MXMOE_F32 or
+ * MXMOE_BF16, with the residual's addition:
+ *  s = x + residual, rounded to dtype, written to sum (both in dtype, [T, H],
+ *  and both NULL without a residual: s = x); rstd fp32 [T] = 1 / sqrt(mean of
+ *  s^2 + eps); y = s rstd weight, formed in fp32: bf16 [T, H], or an 8-bit
+ *  matrix with block_rows 1 (codes [T, Hp], scales [Hp / 128, T rounded up to
+ *  16]), or both, each rounded once; what is not wanted is NULL.
+ * weight [H] in w_dtype.  sum may be x or residual.  1 <= H <= 32768, T >= 1,
+ * (T + 15) * Hp < 2^35, eps > 0 and finite; tensors aligned to their elements
+ * (16 bytes and H % 8 == 0 run faster), codes 16-byte aligned. */
+int mxmoe_rms_norm(const void* x, const void* residual, int dtype, const void* weight, int w_dtype, int64_t T,
+                   int64_t H, float eps, void* sum, uint16_t* y, uint8_t* codes, uint8_t* scales, float* rstd,
+                   void* stream);
+
+/* Its gradients from s [T, H] in dtype, rstd and dy bf16 [T, H], the gradient
+ * of y (in whatever form it was used); dsum [T, H] in dtype, the gradient that
+ * reaches s from elsewhere, or NULL.  dx [T, H] in dtype is the gradient of x
+ * and of the residual alike (it may be dsum); dweight fp32 [H], summed in an
+ * order that depends on T and H alone.  workspace:
+ * mxmoe_rms_norm_backward_workspace_bytes. */
+int mxmoe_rms_norm_backward(const void* s, const float* rstd, const void* weight, int w_dtype, const uint16_t* dy,
+                            const void* dsum, int dtype, int64_t T, int64_t H, void* dx, float* dweight,
+                            void* workspace, size_t workspace_bytes, void* stream);
+size_t mxmoe_rms_norm_backward_workspace_bytes(int64_t T, int64_t H);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@
 #include "abi_util.hpp"
 #include "fp8.hpp"
 #include "gate.hpp"
+#include "norm.hpp"
 #include "swiglu8.hpp"
 
 namespace {
@@ -158,6 +159,17 @@ int check_swiglu8(int64_t R, int64_t I, float alpha, float limit) {
                 (long long)I);
   if (!finite(alpha) || !finite(limit) || !(limit > 0.0f))
     return fail(MXFP4_EINVAL, "alpha must be finite and limit finite and > 0");
+  return MXFP4_OK;
+}
+
+int check_norm(int64_t T, int64_t H) {
+  if (T < 1 || H < 1) return fail(MXFP4_EINVAL, "T and H must be >= 1 (T=%lld H=%lld)", (long long)T, (long long)H);
+  if (H > mxmoe::NORM_MAX_H)
+    return fail(MXFP4_EUNSUPPORTED, "H=%lld > %lld", (long long)H, (long long)mxmoe::NORM_MAX_H);
+  // the codes are an 8-bit matrix, and a launch has up to 1024 threads a row
+  if (T >= (int64_t(1) << 35) || (T + 15) * mxmoe::fp8_pitch(H) >= (int64_t(1) << 35) ||
+      !launchable(mxmoe::norm_blocks(T, H), mxmoe::norm_threads(T, H)))
+    return fail(MXFP4_EUNSUPPORTED, "T=%lld H=%lld: too many elements", (long long)T, (long long)H);
   return MXFP4_OK;
 }
 
@@ -397,6 +409,85 @@ int mxmoe_swiglu8_restore(const uint8_t* codes, const uint8_t* scales, int64_t R
     return fail(MXFP4_EINVAL, "codes, h and a must be 16-byte aligned");
   hipStream_t s = static_cast<hipStream_t>(stream);
   LAUNCH(mxmoe::launch_swiglu8_restore(codes, scales, R * I / 4, alpha, limit, h, a, s), "swiglu8_restore");
+  return ok();
+}
+
+int mxmoe_rms_norm(const void* x, const void* residual, int dtype, const void* weight, int w_dtype, int64_t T,
+                   int64_t H, float eps, void* sum, uint16_t* y, uint8_t* codes, uint8_t* scales, float* rstd,
+                   void* stream) {
+  int rc = check_norm(T, H);
+  if (rc) return rc;
+  if (!x || !weight || !rstd || (!y && !codes))
+    return fail(MXFP4_EINVAL, "x, weight, rstd and one of y and codes are required");
+  if (!residual != !sum) return fail(MXFP4_EINVAL, "residual and sum go together");
+  if (!codes != !scales) return fail(MXFP4_EINVAL, "codes and scales go together");
+  rc = check_dtype(dtype, x, "x");
+  if (!rc) rc = check_dtype(dtype, residual, "residual");
+  if (!rc) rc = check_dtype(dtype, sum, "sum");
+  if (!rc) rc = check_dtype(w_dtype, weight, "weight");
+  if (!rc) rc = check_dtype(MXMOE_BF16, y, "y");
+  if (rc) return rc;
+  if (!aligned(codes, 16) || !aligned(rstd, 4))
+    return fail(MXFP4_EINVAL, "codes must be 16-byte, rstd 4-byte aligned");
+  if (!finite(eps) || !(eps > 0.0f)) return fail(MXFP4_EINVAL, "eps must be finite and > 0");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  mxmoe::NormArgs a{};
+  a.T = T;
+  a.H = H;
+  a.f32 = dtype == MXMOE_F32;
+  a.w_f32 = w_dtype == MXMOE_F32;
+  a.eps = eps;
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.sum = sum;
+  a.y = y;
+  a.codes = codes;
+  a.scales = scales;
+  a.rstd = rstd;
+  LAUNCH(mxmoe::launch_norm(a, s), "rms_norm");
+  return ok();
+}
+
+size_t mxmoe_rms_norm_backward_workspace_bytes(int64_t T, int64_t H) {
+  if (check_norm(T, H) != MXFP4_OK) return 0;
+  ok();
+  return up(mxmoe::norm_part_bytes(T, H), ALIGN) + ALIGN;
+}
+
+int mxmoe_rms_norm_backward(const void* x, const float* rstd, const void* weight, int w_dtype, const uint16_t* dy,
+                            const void* dsum, int dtype, int64_t T, int64_t H, void* dx, float* dweight,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_norm(T, H);
+  if (rc) return rc;
+  if (!x || !rstd || !weight || !dy || !dx || !dweight)
+    return fail(MXFP4_EINVAL, "s, rstd, weight, dy, dx and dweight are required");
+  rc = check_dtype(dtype, x, "s");
+  if (!rc) rc = check_dtype(dtype, dsum, "dsum");
+  if (!rc) rc = check_dtype(dtype, dx, "dx");
+  if (!rc) rc = check_dtype(w_dtype, weight, "weight");
+  if (!rc) rc = check_dtype(MXMOE_BF16, dy, "dy");
+  if (rc) return rc;
+  if (!aligned(rstd, 4) || !aligned(dweight, 4))
+    return fail(MXFP4_EINVAL, "rstd and dweight must be 4-byte aligned");
+  rc = check_workspace(workspace, workspace_bytes, mxmoe_rms_norm_backward_workspace_bytes(T, H));
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  mxmoe::NormArgs a{};
+  a.T = T;
+  a.H = H;
+  a.f32 = dtype == MXMOE_F32;
+  a.w_f32 = w_dtype == MXMOE_F32;
+  a.x = x;
+  a.residual = dsum;
+  a.w = weight;
+  a.sum = dx;
+  a.rstd = const_cast<float*>(rstd);
+  a.dy = dy;
+  a.dw = dweight;
+  a.part = static_cast<float*>(workspace);
+  LAUNCH(mxmoe::launch_norm_bwd(a, s), "rms_norm_bwd");
+  if (mxmoe::norm_part_bytes(T, H)) LAUNCH(mxmoe::launch_norm_join(a, s), "rms_norm_join");
   return ok();
 }
 

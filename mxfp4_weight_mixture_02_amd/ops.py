@@ -1,6 +1,6 @@
 """ctypes binding of the operators in include/mxmoe_ops.h: routing with its
-gradient, dense products in 8-bit floating point and 8-bit activation
-checkpoints.
+gradient, dense products in 8-bit floating point, 8-bit activation
+checkpoints and the norm before a layer.
 
 Argument marshalling only, as in native.py.  Each call runs on its tensors'
 device and that device's current stream, whatever device is current; scratch
@@ -58,9 +58,13 @@ def lib() -> ctypes.CDLL:
         L.mxmoe_swiglu8_forward.argtypes = [vp, i64, i64, f32, f32, vp, vp, vp, vp]
         L.mxmoe_swiglu8_backward.argtypes = [vp, vp, vp, i64, i64, f32, f32, vp, vp, vp]
         L.mxmoe_swiglu8_restore.argtypes = [vp, vp, i64, i64, f32, f32, vp, vp, vp]
+        L.mxmoe_rms_norm.argtypes = [vp, vp, ci, vp, ci, i64, i64, f32] + [vp] * 6
+        L.mxmoe_rms_norm_backward.argtypes = [vp, vp, vp, ci, vp, vp, ci, i64, i64, vp, vp, vp, sz, vp]
+        L.mxmoe_rms_norm_backward_workspace_bytes.restype = sz
+        L.mxmoe_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
         for n in ("route", "route_backward", "router_logits", "forward_routed", "backward_routed", "fp8_quantize",
                   "fp8_quantize_t", "fp8_transpose", "fp8_matmul", "fp8_linear", "fp8_linear_dw",
-                  "swiglu8_forward", "swiglu8_backward", "swiglu8_restore"):
+                  "swiglu8_forward", "swiglu8_backward", "swiglu8_restore", "rms_norm", "rms_norm_backward"):
             getattr(L, "mxmoe_" + n).restype = ci
         _lib = L
     return _lib
@@ -558,3 +562,60 @@ class SavedState8:
         """The bf16 state that a backward reads."""
         h, a = swiglu_mxfp8_restore(self.checkpoint)
         return SavedState(**_fields(self), h=h, a=a, lora_v=self.lora_v, lora_vg=self.lora_vg)
+
+
+# ------------------------------------------------------ the norm before a layer
+
+@dataclass
+class Normed:
+    """A norm's results: what a layer's consumers read, and what the backward
+    does."""
+    y: torch.Tensor | None        # bf16 [T, H]
+    y8: Fp8Matrix | None          # the same values in 8 bits, block_rows 1
+    sum: torch.Tensor             # x + residual (x itself without one) [T, H]
+    rstd: torch.Tensor            # fp32 [T]
+
+
+def _norm_weight(weight, H):
+    if weight.dtype not in _DTYPES:
+        raise ValueError(f"weight must be fp32 or bf16, got {weight.dtype}")
+    _shape(weight, (H,), weight.dtype, "weight")
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-5,
+             bf16: bool = True, fp8: bool = False) -> Normed:
+    """Root-mean-square norm of the rows of x + residual [T, H] (fp32 or bf16;
+    the sum is rounded to their type) times weight [H] (fp32 or bf16): in
+    bf16, with ``fp8`` as an 8-bit matrix that fp8_matmul reads, or both."""
+    T, H = _matrix(x, "x")
+    _norm_weight(weight, H)
+    _shape(residual, (T, H), x.dtype, "residual", optional=True)
+    if not (bf16 or fp8):
+        raise ValueError("one of bf16 and fp8 is needed")
+    dev = _same_device(x=x, weight=weight, residual=residual)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None
+    q = Fp8Matrix.empty(T, H, 1, dev) if fp8 else None
+    n = Normed(y, q, x if residual is None else torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=dev))
+    _call("mxmoe_rms_norm", dev, _p(x), _p(residual), _DTYPES[x.dtype], _p(weight), _DTYPES[weight.dtype], T, H, eps,
+          None if residual is None else _p(n.sum), _p(y), _p(q.codes) if fp8 else None,
+          _p(q.scales) if fp8 else None, _p(n.rstd))
+    return n
+
+
+def rms_norm_backward(dy: torch.Tensor, sum: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                      dsum: torch.Tensor | None = None):
+    """(dx, dweight fp32 [H]) from dy bf16 [T, H], the gradient of the norm's
+    result, with sum and rstd of its Normed and dsum, the gradient that
+    reaches sum from elsewhere (the residual stream's).  dx, in sum's type, is
+    the gradient of x and of the residual alike."""
+    T, H = _matrix(sum, "sum")
+    _norm_weight(weight, H)
+    _shape(dy, (T, H), torch.bfloat16, "dy")
+    _shape(rstd, (T,), torch.float32, "rstd")
+    _shape(dsum, (T, H), sum.dtype, "dsum", optional=True)
+    dev = _same_device(dy=dy, sum=sum, rstd=rstd, weight=weight, dsum=dsum)
+    ws, nbytes = _workspace("mxmoe_rms_norm_backward_workspace_bytes", dev, T, H)
+    dx, dw = torch.empty_like(sum), torch.empty(H, dtype=torch.float32, device=dev)
+    _call("mxmoe_rms_norm_backward", dev, _p(sum), _p(rstd), _p(weight), _DTYPES[weight.dtype], _p(dy), _p(dsum),
+          _DTYPES[sum.dtype], T, H, _p(dx), _p(dw), _p(ws), nbytes)
+    return dx, dw
