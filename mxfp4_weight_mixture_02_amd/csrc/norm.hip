@@ -115,14 +115,18 @@ __device__ __forceinline__ V row_sum(V v, V* slots, int wave, int lane) {
 template <int NW, int C>
 __device__ __forceinline__ float row_rstd(const float (&v)[C][8], int64_t H, float eps, double* slots, int wave,
                                           int lane) {
+  // sums of 8, of the chunks, then in fp64 over the lanes: the reciprocal's
+  // own error decides how many 8-bit elements round the other way
   float ss = 0.0f;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
-  ss = row_sum<NW>(ss, reinterpret_cast<float*>(slots), wave, lane);
-  const float m = ss / (float)H + eps;
-  if (m > 1e-30f && m < 3e38f) return 1.0f / sqrtf(m);
+    for (int i = 0; i < 8; ++i) t = fmaf(v[c][i], v[c][i], t);
+    ss += t;
+  }
+  const double m = row_sum<NW>((double)ss, slots, wave, lane) / (double)H + (double)eps;
+  if (m > 1e-30 && m < 3e38) return (float)(1.0 / sqrt(m));
   double sd = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c)
@@ -132,7 +136,9 @@ __device__ __forceinline__ float row_rstd(const float (&v)[C][8], int64_t H, flo
   return (float)(1.0 / sqrt(sd / (double)H + (double)eps));
 }
 
-// A row for NW waves; four waves a workgroup, or NW where that is more.
+// A row for NW waves; four waves a workgroup, or NW where that is more.  Bound
+// by HBM: 16381 x 2880 bf16 with the residual, both results: 85 us, 5.0 TB/s;
+// 2047 x 2880 fp32, bf16 result: 15.6 us, 5.3 TB/s.  One row: 3.7 us.
 template <bool F32, bool VEC, int NW, int C>
 __global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_kernel(NormArgs a) {
   __shared__ double slots[NW];
@@ -205,7 +211,8 @@ __global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_kernel(NormArgs a
 // Gradients.  Workgroup b takes the row groups b, b + gridDim.x, ..; each lane
 // sums its columns' part of dw over its rows, the workgroup's waves add theirs
 // in order through LDS, and the parts [workgroups][H] are joined by another
-// launch (one workgroup writes dw itself).
+// launch (one workgroup writes dw itself).  Bound by HBM: 16384 x 2880 bf16
+// with the sum's own gradient in 77.8 us (4.8 TB/s), the join 5.5.
 template <bool F32, bool VEC, int NW, int C>
 __global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_bwd_kernel(NormArgs a) {
   constexpr int ROWS = NW < 4 ? 4 / NW : 1;   // rows at a time
@@ -320,57 +327,61 @@ static bool norm_vec(const NormArgs& a) {
   return a.H % 8 == 0 && ok(a.x) && ok(a.residual) && ok(a.w) && ok(a.sum) && ok(a.y) && ok(a.dy);
 }
 
-// Waves of a row and chunks of a lane.  One wave a row moves most bytes while
-// rows fill the card; fewer rows, or longer ones, take more waves.
-static void norm_shape(int64_t T, int64_t H, int* nw, int* c) {
-  const int64_t w = (H + 511) / 512;   // chunks of one wave
-  *nw = w <= 6 && T >= 1024 ? 1 : w <= 16 ? 4 : 16;
-  *c = (int)((w + *nw - 1) / *nw);
-}
-int64_t norm_blocks(int64_t T, int64_t H) {
+// Waves of a row and chunks of a lane, forward.  One wave a row moves most
+// bytes while rows fill the card; fewer rows, or longer ones, take more waves.
+struct NormShape {
   int nw, c;
-  norm_shape(T, H, &nw, &c);
-  return nw == 1 ? (T + 3) / 4 : T;
+};
+static NormShape norm_shape(int64_t T, int64_t H) {
+  const int w = (int)((H + 511) / 512);   // chunks of one wave
+  if (w <= 6 && T >= 1024) return {1, w <= 2 ? 2 : w <= 4 ? 4 : 6};
+  if (w <= 16) return {4, w <= 4 ? 1 : w <= 8 ? 2 : 4};
+  return {16, w <= 32 ? 2 : 4};
 }
-int norm_threads(int64_t T, int64_t H) {
-  int nw, c;
-  norm_shape(T, H, &nw, &c);
-  return nw == 16 ? 1024 : 256;
+// Backward: a lane also holds the weight and its part of dw, so rows are split
+// wider, to 16 waves on a CU (16384 x 2880: one wave a row, 4 on a CU, 138 us;
+// four waves, 105 registers, 8 on a CU 109 us, 16 on a CU 84; twice as many
+// workgroups and parts 91).
+static NormShape norm_bwd_shape(int64_t H) {
+  const int w = (int)((H + 511) / 512);
+  if (w <= 2) return {1, w};
+  if (w <= 8) return {4, w <= 4 ? 1 : 2};
+  if (w <= 16) return {8, 2};
+  return {16, w <= 32 ? 2 : 4};
 }
+int64_t norm_blocks(int64_t T, int64_t H) { return norm_shape(T, H).nw == 1 ? (T + 3) / 4 : T; }
+int norm_threads(int64_t T, int64_t H) { return norm_shape(T, H).nw == 16 ? 1024 : 256; }
 static unsigned norm_bwd_grid(int64_t T, int64_t H) {
-  const int64_t groups = norm_blocks(T, H);
-  return (unsigned)(groups < 512 ? groups : 512);
+  const int nw = norm_bwd_shape(H).nw;
+  const int64_t groups = nw == 1 ? (T + 3) / 4 : T, most = nw <= 4 ? 1024 : 4096 / nw;
+  return (unsigned)(groups < most ? groups : most);
 }
 
-#define NORM_SHAPES(kernel, grid)                                                         \
-  do {                                                                                    \
-    int nw, c;                                                                            \
-    norm_shape(a.T, a.H, &nw, &c);                                                        \
-    const bool vec = norm_vec(a);                                                         \
-    if (nw == 1) {                                                                        \
-      if (c <= 2) NORM_TYPES(kernel, grid, 1, 2);                                         \
-      if (c <= 4) NORM_TYPES(kernel, grid, 1, 4);                                         \
-      NORM_TYPES(kernel, grid, 1, 6);                                                     \
-    }                                                                                     \
-    if (nw == 4) {                                                                        \
-      if (c <= 1) NORM_TYPES(kernel, grid, 4, 1);                                         \
-      if (c <= 2) NORM_TYPES(kernel, grid, 4, 2);                                         \
-      NORM_TYPES(kernel, grid, 4, 4);                                                     \
-    }                                                                                     \
-    if (c <= 2) NORM_TYPES(kernel, grid, 16, 2);                                          \
-    NORM_TYPES(kernel, grid, 16, 4);                                                      \
-  } while (0)
-#define NORM_TYPES(kernel, grid, NW, C)                                                   \
+#define NORM_LAUNCH(kernel, grid, NW, C)                                                  \
   do {                                                                                    \
     const dim3 g_((unsigned)(grid)), b_(64 * (NW < 4 ? 4 : NW));                          \
-    if (a.f32 && vec) hipLaunchKernelGGL((kernel<true, true, NW, C>), g_, b_, 0, s, a);   \
+    const bool vec_ = norm_vec(a);                                                        \
+    if (a.f32 && vec_) hipLaunchKernelGGL((kernel<true, true, NW, C>), g_, b_, 0, s, a);  \
     else if (a.f32) hipLaunchKernelGGL((kernel<true, false, NW, C>), g_, b_, 0, s, a);    \
-    else if (vec) hipLaunchKernelGGL((kernel<false, true, NW, C>), g_, b_, 0, s, a);      \
+    else if (vec_) hipLaunchKernelGGL((kernel<false, true, NW, C>), g_, b_, 0, s, a);     \
     else hipLaunchKernelGGL((kernel<false, false, NW, C>), g_, b_, 0, s, a);              \
     return hipGetLastError();                                                             \
   } while (0)
 
-hipError_t launch_norm(const NormArgs& a, hipStream_t s) { NORM_SHAPES(norm_kernel, norm_blocks(a.T, a.H)); }
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  const int64_t grid = norm_blocks(a.T, a.H);
+  const NormShape n = norm_shape(a.T, a.H);
+  switch (100 * n.nw + n.c) {
+    case 102: NORM_LAUNCH(norm_kernel, grid, 1, 2);
+    case 104: NORM_LAUNCH(norm_kernel, grid, 1, 4);
+    case 106: NORM_LAUNCH(norm_kernel, grid, 1, 6);
+    case 401: NORM_LAUNCH(norm_kernel, grid, 4, 1);
+    case 402: NORM_LAUNCH(norm_kernel, grid, 4, 2);
+    case 404: NORM_LAUNCH(norm_kernel, grid, 4, 4);
+    case 1602: NORM_LAUNCH(norm_kernel, grid, 16, 2);
+    default: NORM_LAUNCH(norm_kernel, grid, 16, 4);
+  }
+}
 
 size_t norm_part_bytes(int64_t T, int64_t H) {
   const unsigned g = norm_bwd_grid(T, H);
@@ -379,7 +390,17 @@ size_t norm_part_bytes(int64_t T, int64_t H) {
 
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
   if (norm_part_bytes(a.T, a.H) && !a.part) return hipErrorInvalidValue;
-  NORM_SHAPES(norm_bwd_kernel, norm_bwd_grid(a.T, a.H));
+  const unsigned grid = norm_bwd_grid(a.T, a.H);
+  const NormShape n = norm_bwd_shape(a.H);
+  switch (100 * n.nw + n.c) {
+    case 101: NORM_LAUNCH(norm_bwd_kernel, grid, 1, 1);
+    case 102: NORM_LAUNCH(norm_bwd_kernel, grid, 1, 2);
+    case 401: NORM_LAUNCH(norm_bwd_kernel, grid, 4, 1);
+    case 402: NORM_LAUNCH(norm_bwd_kernel, grid, 4, 2);
+    case 802: NORM_LAUNCH(norm_bwd_kernel, grid, 8, 2);
+    case 1602: NORM_LAUNCH(norm_bwd_kernel, grid, 16, 2);
+    default: NORM_LAUNCH(norm_bwd_kernel, grid, 16, 4);
+  }
 }
 
 hipError_t launch_norm_join(const NormArgs& a, hipStream_t s) {
