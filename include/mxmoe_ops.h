@@ -1,8 +1,8 @@
 /*
  * mxmoe_ops.h -- C ABI of the operators beside the MXFP4 expert block of
  * mxfp4_moe.h: routing with its gradient and the block on a given routing,
- * dense products in 8-bit floating point, 8-bit activation checkpoints, and
- * the norm before a layer.
+ * dense products in 8-bit floating point, 8-bit activation checkpoints,
+ * the router's balance losses, and the norm before a layer.
  *
  * Conventions as in mxfp4_moe.h: dense row-major tensors in device memory
  * owned by the caller, bf16 as uint16_t bit patterns, `stream` a
@@ -82,6 +82,40 @@ int mxmoe_route_backward(const mxmoe_route_opts* opts, int64_t T, int32_t E, int
  * aligned. */
 int mxmoe_router_logits(int64_t T, int64_t H, int32_t E, const uint16_t* x, const float* router_w,
                         const float* router_b, float* logits, void* stream);
+
+/* Losses that keep a router balanced, over S sequences of the T tokens.
+ *  score     MXMOE_SCORE_*: p = softmax of the logits, or their sigmoids
+ *            divided by their sum (a token of -inf alone has p = 0)
+ *  logits fp32 [T, E], topk_idx int32 [T, k] as mxmoe_route takes and gives
+ *            them (E <= 256, k <= min(E, 8), T < 2^26); an index outside [0,
+ *            E) is not counted
+ *  mask      [T] bytes or NULL: tokens with 0 are left out
+ *  offsets   int32 [S + 1], ascending: sequence s has the tokens offsets[s] ..
+ *            offsets[s + 1] - 1 (values are clamped to 0 .. T; tokens before
+ *            the first or behind the last belong to none).  NULL: S is 1 and
+ *            the sequence has all tokens.  1 <= S <= 65536
+ * With N_s tokens in sequence s, N in all, S+ sequences with any:
+ *  counts    int32 [S, E], choices of an expert; prob fp32 [S, E], the mean of
+ *            p; tokens int32 [S], N_s
+ *  losses    fp32 [2]: the mean over the S+ sequences of E sum_e counts / (k
+ *            N_s) prob (1 when all is even), and the mean over the N tokens of
+ *            logsumexp(logits)^2 (0 for a token of -inf alone)
+ * Without tokens all are 0.  Counts are exact, sums in a fixed order.
+ * workspace: mxmoe_balance_workspace_bytes. */
+int mxmoe_balance(int score, int64_t T, int32_t E, int32_t k, int32_t S, const float* logits,
+                  const int32_t* topk_idx, const uint8_t* mask, const int32_t* offsets, float* losses,
+                  int32_t* counts, float* prob, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                  void* stream);
+/* Bytes of workspace mxmoe_balance needs (0 if a size is out of range). */
+size_t mxmoe_balance_workspace_bytes(int64_t T, int32_t E, int32_t k, int32_t S);
+/* dlogits fp32 [T, E] (every element written) from dlosses fp32 [2], with
+ * counts and tokens of the forward, the counts held fixed; plus add fp32 [T, E]
+ * (what mxmoe_route_backward gives, say; it may be dlogits) or NULL.  Tokens
+ * that are left out have add's values, or 0. */
+int mxmoe_balance_backward(int score, int64_t T, int32_t E, int32_t k, int32_t S, const float* logits,
+                           const uint8_t* mask, const int32_t* offsets, const int32_t* counts,
+                           const int32_t* tokens, const float* dlosses, const float* add, float* dlogits,
+                           void* stream);
 
 /* The expert block (mxfp4_moe_forward) on a given routing: `saved` names
  * its topk_idx, topk_w, expert_offsets and sorted_rows as mxmoe_route fills

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "abi_util.hpp"
+#include "balance.hpp"
 #include "fp8.hpp"
 #include "gate.hpp"
 #include "norm.hpp"
@@ -86,6 +87,40 @@ mxmoe::RouteArgs route_args(const mxmoe_route_opts& o, int64_t T, int32_t E, int
   a.logits = logits;
   a.bias = bias;
   return a;
+}
+
+int check_balance(int64_t T, int32_t E, int32_t k, int32_t S) {
+  const int rc = check_route_sizes(T, E, k);
+  if (rc) return rc;
+  if (S < 1) return fail(MXFP4_EINVAL, "S must be >= 1 (S=%d)", S);
+  if (S > 65536) return fail(MXFP4_EUNSUPPORTED, "S=%d > 65536", S);
+  return MXFP4_OK;
+}
+
+// What both directions take.
+int balance_args(int score, int64_t T, int32_t E, int32_t k, int32_t S, const float* logits, const uint8_t* mask,
+                 const int32_t* offsets, const int32_t* counts, const int32_t* tokens, mxmoe::BalanceArgs* a) {
+  const int rc = check_balance(T, E, k, S);
+  if (rc) return rc;
+  if (score != MXMOE_SCORE_SOFTMAX && score != MXMOE_SCORE_SIGMOID)
+    return fail(MXFP4_EINVAL, "score=%d unknown", score);
+  if (!offsets && S != 1) return fail(MXFP4_EINVAL, "S=%d sequences need offsets", S);
+  if (!logits || !counts || !tokens) return fail(MXFP4_EINVAL, "logits, counts and tokens are required");
+  if (!aligned(logits, 4) || !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(tokens, 4))
+    return fail(MXFP4_EINVAL, "tensors must be 4-byte aligned");
+  *a = mxmoe::BalanceArgs{};
+  a->T = T;
+  a->E = E;
+  a->k = k;
+  a->S = S;
+  a->sigmoid = score == MXMOE_SCORE_SIGMOID;
+  a->wide = E % 4 == 0 && aligned(logits, 16);
+  a->logits = logits;
+  a->mask = mask;
+  a->offsets = offsets;
+  a->counts = const_cast<int32_t*>(counts);
+  a->tokens = const_cast<int32_t*>(tokens);
+  return MXFP4_OK;
 }
 
 constexpr int64_t FP8_MAX_K = int64_t(1) << 22;
@@ -230,6 +265,49 @@ int mxmoe_route_backward(const mxmoe_route_opts* opts, int64_t T, int32_t E, int
   hipStream_t s = static_cast<hipStream_t>(stream);
   LAUNCH(mxmoe::launch_gate_bwd(route_args(*opts, T, E, k, logits, nullptr, dlogits), topk_idx, dw, dlogits, s),
          "gate_bwd");
+  return ok();
+}
+
+size_t mxmoe_balance_workspace_bytes(int64_t T, int32_t E, int32_t k, int32_t S) {
+  if (check_balance(T, E, k, S) != MXFP4_OK) return 0;
+  ok();
+  return mxmoe::balance_ws_bytes(T, E, S) + ALIGN;
+}
+
+int mxmoe_balance(int score, int64_t T, int32_t E, int32_t k, int32_t S, const float* logits,
+                  const int32_t* topk_idx, const uint8_t* mask, const int32_t* offsets, float* losses,
+                  int32_t* counts, float* prob, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  mxmoe::BalanceArgs a;
+  int rc = balance_args(score, T, E, k, S, logits, mask, offsets, counts, tokens, &a);
+  if (rc) return rc;
+  if (!topk_idx || !losses || !prob) return fail(MXFP4_EINVAL, "topk_idx, losses and prob are required");
+  if (!aligned(topk_idx, 4) || !aligned(losses, 4) || !aligned(prob, 4))
+    return fail(MXFP4_EINVAL, "tensors must be 4-byte aligned");
+  rc = check_workspace(workspace, workspace_bytes, mxmoe_balance_workspace_bytes(T, E, k, S));
+  if (rc) return rc;
+  a.topk_idx = topk_idx;
+  a.losses = losses;
+  a.prob = prob;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  static const char* const NAMES[] = {"balance_part", "balance_seq", "balance_join"};
+  for (int i = 0; i < mxmoe::balance_launches(T, S); ++i) LAUNCH(mxmoe::launch_balance(a, i, workspace, s), NAMES[i]);
+  return ok();
+}
+
+int mxmoe_balance_backward(int score, int64_t T, int32_t E, int32_t k, int32_t S, const float* logits,
+                           const uint8_t* mask, const int32_t* offsets, const int32_t* counts,
+                           const int32_t* tokens, const float* dlosses, const float* add, float* dlogits,
+                           void* stream) {
+  mxmoe::BalanceArgs a;
+  const int rc = balance_args(score, T, E, k, S, logits, mask, offsets, counts, tokens, &a);
+  if (rc) return rc;
+  if (!dlosses || !dlogits) return fail(MXFP4_EINVAL, "dlosses and dlogits are required");
+  if (!aligned(dlosses, 4) || !aligned(add, 4) || !aligned(dlogits, 4))
+    return fail(MXFP4_EINVAL, "tensors must be 4-byte aligned");
+  a.wide = a.wide && aligned(add, 16) && aligned(dlogits, 16);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_balance_bwd(a, dlosses, add, dlogits, s), "balance_bwd");
   return ok();
 }
 

@@ -1,6 +1,6 @@
 """ctypes binding of the operators in include/mxmoe_ops.h: routing with its
 gradient, dense products in 8-bit floating point, 8-bit activation
-checkpoints and the norm before a layer.
+checkpoints, the router's balance losses and the norm before a layer.
 
 Argument marshalling only, as in native.py.  Each call runs on its tensors'
 device and that device's current stream, whatever device is current; scratch
@@ -58,13 +58,18 @@ def lib() -> ctypes.CDLL:
         L.mxmoe_swiglu8_forward.argtypes = [vp, i64, i64, f32, f32, vp, vp, vp, vp]
         L.mxmoe_swiglu8_backward.argtypes = [vp, vp, vp, i64, i64, f32, f32, vp, vp, vp]
         L.mxmoe_swiglu8_restore.argtypes = [vp, vp, i64, i64, f32, f32, vp, vp, vp]
+        L.mxmoe_balance_workspace_bytes.restype = sz
+        L.mxmoe_balance_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.mxmoe_balance.argtypes = [ci, i64, i32, i32, i32] + [vp] * 9 + [sz, vp]
+        L.mxmoe_balance_backward.argtypes = [ci, i64, i32, i32, i32] + [vp] * 9
         L.mxmoe_rms_norm.argtypes = [vp, vp, ci, vp, ci, i64, i64, f32] + [vp] * 6
         L.mxmoe_rms_norm_backward.argtypes = [vp, vp, vp, ci, vp, vp, ci, i64, i64, vp, vp, vp, sz, vp]
         L.mxmoe_rms_norm_backward_workspace_bytes.restype = sz
         L.mxmoe_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
         for n in ("route", "route_backward", "router_logits", "forward_routed", "backward_routed", "fp8_quantize",
                   "fp8_quantize_t", "fp8_transpose", "fp8_matmul", "fp8_linear", "fp8_linear_dw",
-                  "swiglu8_forward", "swiglu8_backward", "swiglu8_restore", "rms_norm", "rms_norm_backward"):
+                  "swiglu8_forward", "swiglu8_backward", "swiglu8_restore", "rms_norm", "rms_norm_backward",
+                  "balance", "balance_backward"):
             getattr(L, "mxmoe_" + n).restype = ci
         _lib = L
     return _lib
@@ -217,6 +222,77 @@ def moe_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, dw: torch.T
     out = torch.empty_like(logits)
     _call("mxmoe_route_backward", dev, options.struct, T, E, k, _p(logits), _p(topk_idx), _p(dw),
           _p(out))
+    return out
+
+
+@dataclass
+class BalanceLoss:
+    """Losses that keep a router balanced, what a training loop watches beside
+    them, and what their backward needs."""
+    losses: torch.Tensor          # fp32 [2]: the balance loss (1: even), the mean of logsumexp^2
+    counts: torch.Tensor          # int32 [S, E], choices of each expert
+    prob: torch.Tensor            # fp32 [S, E], mean probabilities
+    tokens: torch.Tensor          # int32 [S], tokens that count
+    k: int
+    score: str = "softmax"
+    mask: torch.Tensor | None = None
+    offsets: torch.Tensor | None = None
+
+
+def _sequences(score, T, mask, offsets):
+    """The number of sequences, and the arguments' shapes."""
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    _shape(mask, (T,), torch.bool, "mask", optional=True)
+    if offsets is None:
+        return 1
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"offsets must be [sequences + 1], got {tuple(offsets.shape)}")
+    _shape(offsets, tuple(offsets.shape), torch.int32, "offsets")
+    return offsets.shape[0] - 1
+
+
+def moe_balance(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = "softmax",
+                mask: torch.Tensor | None = None, offsets: torch.Tensor | None = None) -> BalanceLoss:
+    """Per-expert counts, mean probabilities (softmax, or sigmoids divided by
+    their sum), the balance loss and the mean of logsumexp^2 of logits [T, E]
+    with the choice topk_idx [T, k] (moe_route's), over the tokens that mask
+    (bool [T]) leaves, in the sequences that offsets (int32 [S + 1], ascending)
+    bounds; the balance loss is the mean of the sequences' own."""
+    T, E = _logits(logits)
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx must be [T, k], got {tuple(topk_idx.shape)}")
+    k = topk_idx.shape[1]
+    _shape(topk_idx, (T, k), torch.int32, "topk_idx")
+    S = _sequences(score, T, mask, offsets)
+    dev = _same_device(logits=logits, topk_idx=topk_idx, mask=mask, offsets=offsets)
+    ws, nbytes = _workspace("mxmoe_balance_workspace_bytes", dev, T, E, k, S)
+    # one allocation for the four
+    f, counts, prob, tokens = torch.unsafe_split_with_sizes(
+        torch.empty(2 + 2 * S * E + S, dtype=torch.int32, device=dev), (2, S * E, S * E, S))
+    b = BalanceLoss(f.view(torch.float32), counts.view(S, E), prob.view(torch.float32).view(S, E), tokens, k, score,
+                    mask, offsets)
+    _call("mxmoe_balance", dev, SCORES[score], T, E, k, S, _p(logits), _p(topk_idx), _p(mask), _p(offsets),
+          _p(b.losses), _p(b.counts), _p(b.prob), _p(b.tokens), _p(ws), nbytes)
+    return b
+
+
+def moe_balance_backward(logits: torch.Tensor, saved: BalanceLoss, dlosses: torch.Tensor,
+                         add: torch.Tensor | None = None) -> torch.Tensor:
+    """dlogits fp32 [T, E] from dlosses fp32 [2], the gradient of saved.losses
+    (the losses' weights in the whole loss), with the counts held fixed; plus
+    add [T, E], moe_route_backward's gradient, say."""
+    T, E = _logits(logits)
+    S = _sequences(saved.score, T, saved.mask, saved.offsets)
+    _shape(saved.counts, (S, E), torch.int32, "saved.counts")
+    _shape(saved.tokens, (S,), torch.int32, "saved.tokens")
+    _shape(dlosses, (2,), torch.float32, "dlosses")
+    _shape(add, (T, E), torch.float32, "add", optional=True)
+    dev = _same_device(logits=logits, counts=saved.counts, tokens=saved.tokens, dlosses=dlosses, add=add,
+                       mask=saved.mask, offsets=saved.offsets)
+    out = torch.empty_like(logits)
+    _call("mxmoe_balance_backward", dev, SCORES[saved.score], T, E, saved.k, S, _p(logits), _p(saved.mask),
+          _p(saved.offsets), _p(saved.counts), _p(saved.tokens), _p(dlosses), _p(add), _p(out))
     return out
 
 
