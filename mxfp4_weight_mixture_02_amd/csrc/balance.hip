@@ -13,8 +13,11 @@
 // A token is a row of 16 lanes, four tokens a wave: lane l has the experts 64 j
 // + 4 l .. + 3, so a row's sums are four DPP rotations and its loads whole
 // 256-byte pieces.  Scores are formed in fp32 relative to the largest of the
-// token (of the sigmoids too: logits below -88 keep their ratios), sums over
-// a workgroup's tokens in fp32, over workgroups in fp64, in a fixed order.
+// token (of the sigmoids too: logits below -88 keep their ratios), with the
+// hardware's base-2 exponential and reciprocal (1 ulp each; the argument's
+// rounding is 2^-24 of it, which the largest scores do not see): the library's
+// exponential and division took three quarters of the time.  Sums over a
+// workgroup's tokens are fp32, over workgroups fp64, in a fixed order.
 #include "balance.hpp"
 #include "common.hpp"
 
@@ -51,6 +54,18 @@ __device__ __forceinline__ f32x4 four(const float* row, int e, int E, float fill
   return v;
 }
 
+// A lane's logits of a token; -inf past E.
+template <int J>
+struct Logits {
+  f32x4 x[J];
+};
+template <int J, bool WIDE>
+__device__ __forceinline__ void logits16(const float* row, int E, int l, Logits<J>& v) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) v.x[j] = four<WIDE>(row, 64 * j + 4 * l, E, -__builtin_inff());
+}
+__device__ __forceinline__ float exp_hw(float v) { return __builtin_amdgcn_exp2f(v * 1.4426950408889634f); }
+
 // A token's normalised scores p and softmax (the same without SIG), its
 // logsumexp and, with SIG, 1 - sigmoid of each logit.  A token of -inf alone
 // has p, softmax and logsumexp 0.
@@ -59,32 +74,31 @@ struct Scores {
   float p[J][4], soft[J][4], rest[J][4];
   float lse;
 };
-template <int J, bool SIG, bool WIDE>
-__device__ __forceinline__ void scores(const float* row, int E, int l, Scores<J, SIG>& s) {
+template <int J, bool SIG>
+__device__ __forceinline__ void scores(const Logits<J>& in, Scores<J, SIG>& s) {
   constexpr float INF = __builtin_inff();
-  f32x4 x[J];
   float m = -INF;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    x[j] = four<WIDE>(row, 64 * j + 4 * l, E, -INF);
+  for (int j = 0; j < J; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, x[j][i]);
-  }
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, in.x[j][i]);
   m = row16_max(m);
   if (m == -INF) m = 0.0f;
   float sum = 0.0f, total = 0.0f;
-  const float top = fminf(m, 0.0f);   // of min(logit, 0)
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float v = x[j][i];
-      s.soft[j][i] = expf(v - m);
+      const float v = in.x[j][i];
+      s.soft[j][i] = exp_hw(v - m);
       sum += s.soft[j][i];
       if (SIG) {
-        const float a = expf(-fabsf(v)), r = 1.0f / (1.0f + a);
-        s.p[j][i] = expf(fminf(v, 0.0f) - top) * r;   // a NaN is in r
-        s.rest[j][i] = v >= 0.0f ? a * r : r;
+        // sigmoid over the largest one's exp(min(m, 0)): exp(min(v, 0)) or
+        // exp(v - m), over 1 + exp(-|v|)
+        const float a = exp_hw(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + a);
+        const float g = v < 0.0f ? a : 1.0f;   // a NaN is in r
+        s.p[j][i] = (m < 0.0f ? s.soft[j][i] : g) * r;
+        s.rest[j][i] = v < 0.0f ? r : a * r;
         total += s.p[j][i];
       }
     }
@@ -111,15 +125,17 @@ __device__ __forceinline__ int64_t clamped(const BalanceArgs& a, int s) {
 }
 __device__ __forceinline__ int64_t seq_begin(const BalanceArgs& a, int s) { return a.offsets ? clamped(a, s) : 0; }
 __device__ __forceinline__ int64_t seq_end(const BalanceArgs& a, int s) { return a.offsets ? clamped(a, s + 1) : a.T; }
-// The first sequence that ends behind token t (S: none does).
+// The first sequence that ends behind token t (S: none does), by the whole
+// wave: 64 places at a time, where a search by halves waits for a load each.
 __device__ __forceinline__ int seq_after(const BalanceArgs& a, int64_t t) {
-  int lo = 0, hi = a.S;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = a.S;   // the answer's range
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_end(a, mid) > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+    const int step = (hi - lo + 63) / 64, at = lo + lane * step;
+    const uint64_t behind = __ballot(at >= hi || seq_end(a, at) > t);
+    const int f = behind ? __builtin_ctzll(behind) : 64;
+    hi = min(hi, lo + f * step);
+    if (f) lo += (f - 1) * step + 1;
   }
   return lo;
 }
@@ -136,8 +152,12 @@ struct BalanceWs {
   float* z;         // [slots] sums of lse^2
   int32_t* n;       // [slots] tokens
   double* seq;      // [S, 2] balance of a sequence, sum of lse^2
+  int32_t* done;    // sequences that are finished: 0 from the parts' launch
 };
 
+// 16384 tokens x 256 experts in 13 sequences, sigmoid, masked: 12.5 us, 1.3 TB/s:
+// a workgroup's 64 KB are asked for at once, and then it computes.
+//
 // Partial sums of tokens block * per .. + per - 1, sequence by sequence.  ONE:
 // all tokens are one sequence and this workgroup's, which also finishes.
 template <int J, bool SIG, bool WIDE, bool ONE>
@@ -149,6 +169,18 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
   __shared__ double fin[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, row = tid >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * per, t1 = min(t0 + per, a.T);
+  if (!ONE && blockIdx.x == 0 && tid == 0) *ws.done = 0;
+  // A token's loads are issued a round ahead, the first ones before its
+  // sequence is known.
+  Logits<J> x;
+  int live = 1, pick = -1;
+  int64_t have = -1;   // the token they are of
+  auto fetch = [&](int64_t t, Logits<J>& y, int& on, int& e) {
+    logits16<J, WIDE>(a.logits + t * a.E, a.E, l, y);
+    on = a.mask ? a.mask[t] : 1;
+    e = l < a.k ? a.topk_idx[t * a.k + l] : -1;
+  };
+  if (t0 + row < t1) fetch(have = t0 + row, x, live, pick);
   for (int s = ONE || !a.offsets ? 0 : seq_after(a, t0); s < a.S; ++s) {
     const int64_t from = seq_begin(a, s), lo = max(from, t0), hi = min(seq_end(a, s), t1);   // uniform
     if (!ONE && from >= t1) break;
@@ -159,19 +191,25 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
     float z = 0.0f;
     int n = 0;
     for (int64_t t = lo + row; t < hi; t += 4 * BAL_WAVES) {   // a row's 16 lanes go together
-      if (a.mask && !a.mask[t]) continue;
-      Scores<J, SIG> q;
-      scores<J, SIG, WIDE>(a.logits + t * a.E, a.E, l, q);
+      if (t != have) fetch(t, x, live, pick);
+      Logits<J> next;
+      int next_live = 1, next_pick = -1;
+      have = t + 4 * BAL_WAVES;
+      if (have < t1) fetch(have, next, next_live, next_pick);
+      if (live) {
+        Scores<J, SIG> q;
+        scores<J, SIG>(x, q);
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] += q.p[j][i];
-      if (l < a.k) {
-        const int e = a.topk_idx[t * a.k + l];
-        if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+          for (int i = 0; i < 4; ++i) acc[j][i] += q.p[j][i];
+        if (pick >= 0 && pick < a.E) atomicAdd(&hist[pick], 1);
+        z = fmaf(q.lse, q.lse, z);
+        ++n;
       }
-      z = fmaf(q.lse, q.lse, z);
-      ++n;
+      x = next;
+      live = next_live;
+      pick = next_pick;
     }
     // the wave's four rows, then the waves, in order
 #pragma unroll
@@ -234,48 +272,54 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
 }
 
 template <class V>
-__device__ __forceinline__ V all_sum(V v, V* slots, int waves) {
+__device__ __forceinline__ V wave_add(V v) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = slots[0];
-  for (int i = 1; i < waves; ++i) v += slots[i];
   return v;
 }
 
-// A sequence per workgroup: its parts' sums.  1024 threads are EP experts by
-// slices of the parts.
+// A sequence per workgroup: its parts' sums; 1024 threads are EP experts by
+// slices of the parts.  With several sequences, the workgroup that ends last
+// joins their losses, in the sequences' order (a launch of its own takes 4 us).
+// A chain of dependent loads: 9 us for 13 sequences of 20 parts.
 template <int EP>
 __global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceArgs a, BalanceWs ws, int per) {
   constexpr int SL = 1024 / EP;
   __shared__ double sums[1024];
   __shared__ int cs[1024];
-  __shared__ double slots[16];
-  __shared__ int islots[16];
-  const int tid = threadIdx.x, e = tid % EP, sl = tid / EP, s = blockIdx.x;
+  __shared__ double zs[16], wsum[16], ns[16], some[16];
+  __shared__ int is[16], last;
+  const int tid = threadIdx.x, e = tid % EP, sl = tid / EP, s = blockIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t lo = seq_begin(a, s), hi = seq_end(a, s);
   const int64_t b0 = lo / per, b1 = hi > lo ? (hi - 1) / per + 1 : b0;   // its workgroups
-  double p = 0.0;
-  int c = 0;
+  double p = 0.0, z = 0.0;
+  int c = 0, n = 0;
+  for (int64_t b = b0 + tid; b < b1; b += 1024) {
+    z += (double)ws.z[b + s];
+    n += ws.n[b + s];
+  }
   if (e < a.E) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t b = b0 + sl; b < b1; b += SL) {
       p += (double)ws.p[(b + s) * a.E + e];
       c += ws.c[(b + s) * a.E + e];
     }
   }
-  double z = 0.0;
-  int n = 0;
-  for (int64_t b = b0 + tid; b < b1; b += 1024) {
-    z += (double)ws.z[b + s];
-    n += ws.n[b + s];
-  }
+  z = wave_add(z);
+  n = wave_add(n);
   sums[tid] = p;
   cs[tid] = c;
-  z = all_sum(z, slots, 16);
-  n = all_sum(n, islots, 16);
+  if (lane == 0) {
+    zs[wave] = z;
+    is[wave] = n;
+  }
+  __syncthreads();
+  z = 0.0;
+  n = 0;
+  for (int u = 0; u < 16; ++u) {
+    z += zs[u];
+    n += is[u];
+  }
   const double div = n ? (double)n : 1.0;
   double w = 0.0;
   if (sl == 0 && e < a.E) {
@@ -288,65 +332,99 @@ __global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceArgs a, Balanc
     a.prob[(int64_t)s * a.E + e] = (float)mean;
     w = c * mean;
   }
-  w = all_sum(w, slots, 16) * a.E / (a.k * div);
+  if (tid < EP) w = wave_add(w);
+  if (lane == 0) wsum[wave] = w;
+  __syncthreads();
+  if (tid == 0) {
+    w = 0.0;
+    for (int u = 0; u < EP / 64; ++u) w += wsum[u];
+    w = w * a.E / (a.k * div);
+    a.tokens[s] = n;
+    if (a.S == 1) {
+      a.losses[0] = (float)w;
+      a.losses[1] = (float)(z / div);
+    } else {
+      ws.seq[2 * s] = w;
+      ws.seq[2 * s + 1] = z;
+      // what this workgroup wrote is seen by whoever sees the count
+      last = __hip_atomic_fetch_add(ws.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == a.S - 1;
+    }
+  }
+  if (a.S == 1) return;
+  __syncthreads();
+  if (!last) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  double some_ = 0.0, n_ = 0.0;
+  w = z = 0.0;
+  for (int i = tid; i < a.S; i += 1024) {
+    const int t = a.tokens[i];
+    w += ws.seq[2 * i];   // 0 without tokens
+    z += ws.seq[2 * i + 1];
+    n_ += t;
+    some_ += t > 0;
+  }
+  w = wave_add(w);
+  z = wave_add(z);
+  n_ = wave_add(n_);
+  some_ = wave_add(some_);
+  if (lane == 0) {
+    wsum[wave] = w;
+    zs[wave] = z;
+    ns[wave] = n_;
+    some[wave] = some_;
+  }
+  __syncthreads();
   if (tid) return;
-  a.tokens[s] = n;
-  if (a.S == 1) {
-    a.losses[0] = (float)w;
-    a.losses[1] = (float)(z / div);
-  } else {
-    ws.seq[2 * s] = w;
-    ws.seq[2 * s + 1] = z;
+  for (int u = 1; u < 16; ++u) {
+    w += wsum[u];
+    z += zs[u];
+    n_ += ns[u];
+    some_ += some[u];
   }
+  a.losses[0] = (float)(some_ > 0.0 ? w / some_ : 0.0);
+  a.losses[1] = (float)(n_ > 0.0 ? z / n_ : 0.0);
 }
 
-// Both losses from the sequences' own.
-__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, BalanceWs ws) {
-  __shared__ double slots[16];
-  double w = 0.0, z = 0.0, n = 0.0, some = 0.0;
-  for (int s = threadIdx.x; s < a.S; s += 1024) {
-    const int t = a.tokens[s];
-    w += ws.seq[2 * s];   // 0 without tokens
-    z += ws.seq[2 * s + 1];
-    n += t;
-    some += t > 0;
-  }
-  w = all_sum(w, slots, 16);
-  z = all_sum(z, slots, 16);
-  n = all_sum(n, slots, 16);
-  some = all_sum(some, slots, 16);
-  if (threadIdx.x) return;
-  a.losses[0] = (float)(some > 0.0 ? w / some : 0.0);
-  a.losses[1] = (float)(n > 0.0 ? z / n : 0.0);
-}
-
+// 8192 x 128, softmax, added to another gradient: 5.4 us, 2.3 TB/s.
+//
 // dlogits: 16 tokens at a time in a workgroup, `per` in all.  A row of lanes
 // looks its first token's sequence up and walks on from there.
 template <int J, bool SIG, bool WIDE>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const float* __restrict__ dlosses,
                                                           const float* __restrict__ add,
                                                           float* __restrict__ dlogits, int per) {
-  __shared__ double slots[4];
+  __shared__ int all[4], some[4];
   const int tid = threadIdx.x, l = tid & 15, row = tid >> 4;
-  double all = 0.0, some = 0.0;
+  const int64_t t0 = (int64_t)blockIdx.x * per + row, t1 = min((int64_t)(blockIdx.x + 1) * per, a.T);
+  // the first token's logits are under way while the sequences are counted
+  Logits<J> x;
+  if (t0 < t1) logits16<J, WIDE>(a.logits + t0 * a.E, a.E, l, x);
+  int n_ = 0, some_ = 0;   // N <= T < 2^26
   for (int s = tid; s < a.S; s += 256) {
     const int n = a.tokens[s];
-    all += n;
-    some += n > 0;
+    n_ += n;
+    some_ += n > 0;
   }
-  all = all_sum(all, slots, 4);
-  some = all_sum(some, slots, 4);
-  const float da = dlosses[0] * (float)a.E / (float)a.k, db = all > 0.0 ? 2.0f * dlosses[1] / (float)all : 0.0f;
-  const int64_t t0 = (int64_t)blockIdx.x * per + row, t1 = min((int64_t)(blockIdx.x + 1) * per, a.T);
-  int s = a.offsets && t0 < t1 ? seq_after(a, t0) : 0;
+  n_ = wave_add(n_);
+  some_ = wave_add(some_);
+  if ((tid & 63) == 0) {
+    all[tid >> 6] = n_;
+    some[tid >> 6] = some_;
+  }
+  int s = a.offsets ? seq_after(a, (int64_t)blockIdx.x * per) : 0;   // of the workgroup's first token
+  __syncthreads();
+  n_ = all[0] + all[1] + all[2] + all[3];
+  some_ = some[0] + some[1] + some[2] + some[3];
+  const float da = dlosses[0] * (float)a.E / (float)a.k, db = n_ > 0 ? 2.0f * dlosses[1] / (float)n_ : 0.0f;
   for (int64_t t = t0; t < t1; t += 16) {
+    if (t > t0) logits16<J, WIDE>(a.logits + t * a.E, a.E, l, x);
     while (s < a.S && seq_end(a, s) <= t) ++s;
     const bool live = s < a.S && seq_begin(a, s) <= t && !(a.mask && !a.mask[t]);
     float d[J][4] = {};
     if (live) {
       Scores<J, SIG> q;
-      scores<J, SIG, WIDE>(a.logits + t * a.E, a.E, l, q);
-      const float n = (float)a.tokens[s], f = n > 0.0f ? da / (n * n * (float)some) : 0.0f;
+      scores<J, SIG>(x, q);
+      const float n = (float)a.tokens[s], f = n > 0.0f ? da / (n * n * (float)some_) : 0.0f;
       const int32_t* counts = a.counts + (int64_t)s * a.E;
       float c[J][4], dot = 0.0f;
 #pragma unroll
@@ -387,18 +465,17 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const f
 
 // ------------------------------------------------------------------ launchers
 
-// Tokens of a workgroup: 128, or 32 where sequences are shorter than that
-// (each is a round of its own); more while workgroups are many, whose parts
-// are then read again.
-static int balance_per(int64_t T, int S) {
-  int per = (int64_t)S * 128 > T && S > 1 ? 32 : 128;
+// Tokens of a workgroup: its 32 at a time, and more of them while workgroups
+// are many, whose parts are read again.
+static int balance_per(int64_t T) {
+  int per = 32;
   while (per < 1024 && (T + per - 1) / per > 256) per *= 2;
   return per;
 }
 static bool balance_one(int64_t T, int S) { return S == 1 && T <= BAL_ONE; }
 
 static size_t balance_layout(int64_t T, int E, int S, void* base, BalanceWs* ws) {
-  const int per = balance_per(T, S);
+  const int per = balance_per(T);
   const size_t slots = (size_t)((T + per - 1) / per) + S;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   char* p = static_cast<char*>(base);
@@ -410,6 +487,7 @@ static size_t balance_layout(int64_t T, int E, int S, void* base, BalanceWs* ws)
   };
   BalanceWs w;
   w.seq = reinterpret_cast<double*>(take((size_t)S * 16));
+  w.done = reinterpret_cast<int32_t*>(take(4));
   w.p = reinterpret_cast<float*>(take(slots * E * 4));
   w.c = reinterpret_cast<int32_t*>(take(slots * E * 4));
   w.z = reinterpret_cast<float*>(take(slots * 4));
@@ -420,7 +498,7 @@ static size_t balance_layout(int64_t T, int E, int S, void* base, BalanceWs* ws)
 size_t balance_ws_bytes(int64_t T, int E, int S) {
   return balance_one(T, S) ? 0 : balance_layout(T, E, S, nullptr, nullptr);
 }
-int balance_launches(int64_t T, int S) { return balance_one(T, S) ? 1 : S == 1 ? 2 : 3; }
+int balance_launches(int64_t T, int S) { return balance_one(T, S) ? 1 : 2; }
 
 template <int J, bool ONE>
 static void part(const BalanceArgs& a, const BalanceWs& ws, int per, hipStream_t s) {
@@ -451,7 +529,7 @@ hipError_t launch_balance(const BalanceArgs& a, int which, void* base, hipStream
   }
   if (!base) return hipErrorInvalidValue;
   balance_layout(a.T, a.E, a.S, base, &ws);
-  const int per = balance_per(a.T, a.S);
+  const int per = balance_per(a.T);
   if (which == 0) {
     if (a.E <= 64)
       part<1, false>(a, ws, per, s);
@@ -459,15 +537,13 @@ hipError_t launch_balance(const BalanceArgs& a, int which, void* base, hipStream
       part<2, false>(a, ws, per, s);
     else
       part<4, false>(a, ws, per, s);
-  } else if (which == 1) {
+  } else {
     if (a.E <= 64)
       hipLaunchKernelGGL(balance_seq_kernel<64>, dim3(a.S), dim3(1024), 0, s, a, ws, per);
     else if (a.E <= 128)
       hipLaunchKernelGGL(balance_seq_kernel<128>, dim3(a.S), dim3(1024), 0, s, a, ws, per);
     else
       hipLaunchKernelGGL(balance_seq_kernel<256>, dim3(a.S), dim3(1024), 0, s, a, ws, per);
-  } else {
-    hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, s, a, ws);
   }
   return hipGetLastError();
 }

@@ -290,7 +290,7 @@ int mxmoe_balance(int score, int64_t T, int32_t E, int32_t k, int32_t S, const f
   a.losses = losses;
   a.prob = prob;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  static const char* const NAMES[] = {"balance_part", "balance_seq", "balance_join"};
+  static const char* const NAMES[] = {"balance_part", "balance_seq"};
   for (int i = 0; i < mxmoe::balance_launches(T, S); ++i) LAUNCH(mxmoe::launch_balance(a, i, workspace, s), NAMES[i]);
   return ok();
 }
