@@ -1,7 +1,7 @@
 /*
  * mxmoe_ops.h -- C ABI of the operators beside the MXFP4 expert block of
  * mxfp4_moe.h: routing with its gradient and the block on a given routing,
- * dense products in 8-bit floating point, 8-bit activation checkpoints,
+ * dense products in 8- and 4-bit floating point, 8-bit activation checkpoints,
  * the router's balance losses, and the norm before a layer.
  *
  * Conventions as in mxfp4_moe.h: dense row-major tensors in device memory
@@ -202,6 +202,57 @@ int mxmoe_fp8_linear_dw(int64_t M, int64_t N, int64_t K, const uint16_t* dy, con
 size_t mxmoe_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
 size_t mxmoe_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
 size_t mxmoe_fp8_linear_dw_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* ------------------------------------------------- 4-bit dense products */
+
+/* A matrix of `rows` rows and K columns in MXFP4, the expert block's format:
+ *  codes   uint8 [rows, pitch], two E2M1 codes a byte (element 2m in the low
+ *          nibble), 16-byte aligned.  pitch is K / 2 (mxfp4_quantize's codes as
+ *          they are; K % 32 == 0) or Kp / 2, Kp = K rounded up to 256, with
+ *          zeros past K
+ *  scales  uint8 UE8M0 [Kp / 256, 4, rows rounded up to 16, 2], 16-byte
+ *          aligned: block b of 32 of row r at [b / 8][b / 2 % 4][r][b % 2]; 0
+ *          past K, not used past the rows
+ * Scale of a block: the smallest 2^e with its largest magnitude at most 6 *
+ * 2^e, e in [-127, 127].  Element: the nearest E2M1 value to x / 2^e, ties to
+ * even.  A block with a non-finite element has the scale NaN (255) and codes 0;
+ * a product with it is NaN.
+ * rows and K are >= 1, K <= 2^22, rows < 2^27, (rows + 255) * Kp < 2^35; a
+ * product's M * N < 2^37 (both rounded up to 128), and N <= 2^27 - 16 where
+ * M <= 16. */
+
+/* x [rows, K], dtype MXMOE_F32 or MXMOE_BF16 (any alignment of the dtype's; 16
+ * bytes and K % 8 == 0 run faster), any K: codes [rows, Kp / 2] and scales. */
+int mxmoe_fp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
+                       void* stream);
+/* The scales [rows, K / 32] of mxfp4_quantize in the order above; K % 32 == 0. */
+int mxmoe_fp4_scales(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* ordered, void* stream);
+
+/* out [M, N] = X W^T + bias for X [M, K] (pitch Kp / 2) and W [N, K] (either
+ * pitch); bias bf16 [N] or NULL; out bf16 or fp32 (out_dtype), 16-byte aligned,
+ * rounded once.  Products are exact and summed in fp32 (values below 2^-126 may
+ * count as 0).  The order of the sums, and so the result's last bits, depend on
+ * M, N and K alone. */
+int mxmoe_fp4_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
+                     const uint8_t* w_codes, int64_t w_pitch, const uint8_t* w_scales, const uint16_t* bias,
+                     int out_dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
+/* The same from bf16 rows x [M, K], which are quantized (in the product's own
+ * launch for few rows, else into the workspace). */
+int mxmoe_fp4_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const uint8_t* w_codes, int64_t w_pitch,
+                     const uint8_t* w_scales, const uint16_t* bias, int out_dtype, void* out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+/* The input's gradient of a linear layer with these weights: dx [M, K] = dy W
+ * with dy bf16 [M, N] as it is and W's values in bf16 (exact from 2^-126 on; a
+ * magnitude of 2^128 or more is an infinity), products and sums in fp32, dx in
+ * out_dtype, 16-byte aligned.  N <= 2^22, (M + 255) * N and (K + 255) * N < 2^35
+ * with N rounded up to 64, M * K < 2^37 (both rounded up to 128). */
+int mxmoe_fp4_linear_dx(int64_t M, int64_t N, int64_t K, const uint16_t* dy, const uint8_t* w_codes,
+                        int64_t w_pitch, const uint8_t* w_scales, int out_dtype, void* dx, void* workspace,
+                        size_t workspace_bytes, void* stream);
+/* Bytes of workspace of the three; 0 if a size is out of range. */
+size_t mxmoe_fp4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
+size_t mxmoe_fp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
+size_t mxmoe_fp4_linear_dx_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
 
 /* ------------------------------------------- 8-bit activation checkpoints */
 

@@ -1,0 +1,767 @@
+// Dense products in microscaled 4-bit floating point (gfx950): E2M1 elements,
+// a UE8M0 scale for each 32 of K, as the expert block's weights have them.
+//
+// out = X W^T with X rounded to MXFP4 and W as stored, on the scaled matrix
+// core: v_mfma_scale_f32_16x16x128_f8f6f4 takes both operands' codes and
+// scales, its products are exact and its sums fp32 (with elements of 4 bits
+// nothing is dropped: sums of blocks 2^24 apart came out as in fp32).  The
+// input's gradient dX = dY W sums along W's rows, where a block of 32 has as
+// many scales: no scaled product.  dY stays in bf16 and W is decoded, exactly,
+// to a transposed bf16 copy that the bf16 matrix core reads.
+//
+// Storage: W's codes stay where they are ([N, K / 2]); X's rows are padded
+// with zeros to 256, so whatever a row of W is followed by is multiplied by 0.
+// Scales are ordered for the matrix core's lanes: lane (r, q) of a fragment
+// feeds row r's elements 64 q .. 64 q + 63 of a block of 256, in two
+// instructions, so [K block][q][row][2] puts the two scales of all rows of a
+// lane side by side.
+#include "common.hpp"
+#include "fp4.hpp"
+#include "ring.hpp"
+
+namespace mxmoe {
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------- quantizer
+
+// Scale exponent of a block whose largest magnitude has these bits: the
+// smallest e with amax <= 6 * 2^e, at least -127.
+__device__ __forceinline__ int e2m1_exponent(uint32_t amax_bits) {
+  const int E = (int)(amax_bits >> 23);
+  return E == 0 ? -127 : max(E - 129 + ((amax_bits & 0x7FFFFFu) > 0x400000u), -127);
+}
+
+// A lane's eight elements of a block of 32 (four lanes side by side) -> their
+// codes; the block's scale byte.  A block with an infinity or a NaN has the
+// scale NaN (255) and codes 0.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));   // lanes ^ 1
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));   // lanes ^ 2
+}
+__device__ __forceinline__ uint32_t fp4_codes(const float (&v)[8], uint32_t& scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  m = quad_max(m);
+  if (m >= 0x7F800000u) {
+    scale = 255;
+    return 0;
+  }
+  scale = (uint32_t)(e2m1_exponent(m) + 127);
+  const float f = scale_operand(scale);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], f, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], f, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], f, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], f, 3);
+}
+// the same of eight bf16 as they are stored
+__device__ __forceinline__ uint32_t fp4_codes(const u32x4& x, uint32_t& scale) {
+  u16x2 t = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, x[i] & 0x7FFF7FFFu));
+  const uint32_t m = quad_max(max((uint32_t)t[0], (uint32_t)t[1])) << 16;
+  if (m >= 0x7F800000u) {
+    scale = 255;
+    return 0;
+  }
+  scale = (uint32_t)(e2m1_exponent(m) + 127);
+  const float f = scale_operand(scale);
+  // (a bit cast of a vector's element itself takes the first one's bits)
+  const uint32_t x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x0), f, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x1), f, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x2), f, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x3), f, 3);
+}
+
+// Eight consecutive elements of a row as bf16 pairs, zeros from `left` on.
+template <bool VEC>
+__device__ __forceinline__ u32x4 bf16x8_at(const uint16_t* x, int64_t at, int64_t left) {
+  u32x4 r = {0u, 0u, 0u, 0u};
+  if (VEC) {
+    if (left > 0) r = *reinterpret_cast<const u32x4*>(x + at);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) r[i >> 1] |= (uint32_t)x[at + i] << (16 * (i & 1));
+  }
+  return r;
+}
+
+// One K block of 256 of 16 rows per workgroup: 32 lanes a row, 8 elements
+// each, two rounds of 8 rows; the scales leave by LDS in their order.
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(256) void fp4_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t K,
+                                                       int64_t pitch, int64_t srows, int kblocks,
+                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  __shared__ __align__(16) uint8_t sc[128];   // [4][16 rows][2]
+  const int kb = blockIdx.x % kblocks, tid = threadIdx.x, l = tid & 31;
+  const int64_t r0 = (int64_t)(blockIdx.x / kblocks) * 16, k0 = (int64_t)kb * 256 + 8 * l;
+  uint32_t c[2], s[2];
+  if (F32) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int64_t row = r0 + 8 * p + (tid >> 5), left = row < rows ? K - k0 : 0;
+      float v[8];
+      if (VEC) {
+        f32x4 a = {0, 0, 0, 0}, b = a;
+        if (left > 0) {
+          const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(x) + row * K + k0);
+          a = q[0];
+          b = q[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = a[i];
+          v[i + 4] = b[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? static_cast<const float*>(x)[row * K + k0 + i] : 0.0f;
+      }
+      c[p] = fp4_codes(v, s[p]);
+    }
+  } else {
+    u32x4 v[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int64_t row = r0 + 8 * p + (tid >> 5);
+      v[p] = bf16x8_at<VEC>(static_cast<const uint16_t*>(x), row * K + k0, row < rows ? K - k0 : 0);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) c[p] = fp4_codes(v[p], s[p]);
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int at = 8 * p + (tid >> 5);
+    const int64_t row = r0 + at;
+    if (row < rows) *reinterpret_cast<uint32_t*>(codes + row * pitch + k0 / 2) = c[p];
+    if ((l & 3) == 0) sc[(l >> 3) * 32 + at * 2 + ((l >> 2) & 1)] = (uint8_t)s[p];   // block l / 4: pair l / 8
+  }
+  __syncthreads();
+  if (tid < 8)   // 16 rows' two bytes: 32 a pair
+    *reinterpret_cast<u32x4*>(scales + ((int64_t)kb * 4 + (tid >> 1)) * srows * 2 + r0 * 2 + 16 * (tid & 1)) =
+        *reinterpret_cast<const u32x4*>(sc + 16 * tid);
+}
+
+// Scales [rows, K / 32] into that order; zeros (2^-127) past K and past the rows.
+__global__ __launch_bounds__(256) void fp4_scales_kernel(const uint8_t* __restrict__ scales, int64_t rows, int64_t k32,
+                                                         int64_t srows, int64_t total, uint8_t* __restrict__ ordered) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // a pair of bytes: (K block * 4 + q) * srows + row
+  if (i >= total) return;
+  const int64_t row = i % srows, b = i / srows * 2;
+  uint32_t v = 0;
+  if (row < rows) {
+    if (b < k32) v = scales[row * k32 + b];
+    if (b + 1 < k32) v |= (uint32_t)scales[row * k32 + b + 1] << 8;
+  }
+  reinterpret_cast<uint16_t*>(ordered)[i] = (uint16_t)v;
+}
+
+// ------------------------------------------------------------------- products
+
+template <int SEL_A, int SEL_B>
+__device__ __forceinline__ f32x4 fp4_mfma(const i32x8& a, const i32x8& b, f32x4 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, SEL_A, sa, SEL_B, sb);
+}
+__device__ __forceinline__ f32x4 fp4_mfma(const i32x8& a, const i32x8& b, f32x4 c, int sel_a, int sa, int sel_b,
+                                          int sb) {
+  // the selectors are constants after unrolling
+  switch (sel_a * 4 + sel_b) {
+    case 0: return fp4_mfma<0, 0>(a, b, c, sa, sb);
+    case 1: return fp4_mfma<0, 1>(a, b, c, sa, sb);
+    case 2: return fp4_mfma<0, 2>(a, b, c, sa, sb);
+    case 3: return fp4_mfma<0, 3>(a, b, c, sa, sb);
+    case 4: return fp4_mfma<1, 0>(a, b, c, sa, sb);
+    case 5: return fp4_mfma<1, 1>(a, b, c, sa, sb);
+    case 6: return fp4_mfma<1, 2>(a, b, c, sa, sb);
+    case 7: return fp4_mfma<1, 3>(a, b, c, sa, sb);
+    case 8: return fp4_mfma<2, 0>(a, b, c, sa, sb);
+    case 9: return fp4_mfma<2, 1>(a, b, c, sa, sb);
+    case 10: return fp4_mfma<2, 2>(a, b, c, sa, sb);
+    case 11: return fp4_mfma<2, 3>(a, b, c, sa, sb);
+    case 12: return fp4_mfma<3, 0>(a, b, c, sa, sb);
+    case 13: return fp4_mfma<3, 1>(a, b, c, sa, sb);
+    case 14: return fp4_mfma<3, 2>(a, b, c, sa, sb);
+    default: return fp4_mfma<3, 3>(a, b, c, sa, sb);
+  }
+}
+// 16 bytes of codes as an operand (4-bit formats read its first four registers)
+__device__ __forceinline__ i32x8 fp4_operand(const u32x4& v) {
+  return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+}
+
+// A workgroup's tile: WN x WM waves of (16 FN) x (16 FM), and NST LDS stages.
+// A stage holds one K block, 128 bytes of each of BN rows of W and BM rows of
+// X (256 elements in 4 bits, 64 in bf16), and in 4 bits their scales: 8 bytes
+// a row, [4][rows][2], in copies of 1 KB.
+template <int WN_, int WM_, int FN_, int FM_, int NST_, bool FP4_>
+struct Fp4Tile {
+  static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, NST = NST_;
+  static constexpr bool FP4 = FP4_;
+  static constexpr int NW = WN * WM;
+  static constexpr int BN = WN * FN * 16, BM = WM * FM * 16;
+  static constexpr int CX = FP4 ? (BM + 127) / 128 : 0, CW = FP4 ? (BN + 127) / 128 : 0;   // scale copies
+  static constexpr int SX = (BN + BM) * 128, SW = SX + CX * 1024, STAGE = SW + CW * 1024;
+  static constexpr int LOADS = (BN + BM) / 8 / NW;   // 1 KB copies of rows per wave and step
+  static constexpr int COPIES = LOADS + (FP4 ? 1 : 0);
+  static_assert(LOADS <= 8 && LOADS * NW * 8 == BN + BM && CX + CW <= NW, "copies");
+  static_assert(BN <= 256 && BM <= 256 && NST >= 2 && NST * STAGE <= 160 * 1024, "LDS");
+  static_assert((NST - 1) * COPIES < 64, "vector-memory counter");
+  static constexpr bool SPREAD = 2 * NST * STAGE > 160 * 1024;   // one workgroup on a CU
+  // words with the scale pairs of a lane's rows: two rows a word, or with odd F one
+  static constexpr int XW = FM % 2 ? FM : FM / 2, WW = FN / 2;
+  static_assert(FN % 2 == 0, "pairs of scales");
+};
+
+// A wave's part of a tile's main loop.
+struct Fp4Wave {
+  u32x4 rw, rx, rs;            // W's and X's rows of the tile, and this wave's scales
+  uint32_t off[8];             // this lane's 16 bytes of each copy, at K block 0
+  uint32_t soff, sstep;        // its scale copy, and the step to the next K block
+  uint32_t sdst;               // where in a stage its scales go
+  uint32_t lds;                // LDS address of the stages
+  int wave, lane, woff, xoff, s0;   // fragment addresses in a stage: row, first chunk
+  int sxoff, swoff;            // scale addresses in a stage
+  int tail;                    // the K block in which W's rows end early, or -1
+  uint32_t left;               // their bytes in it
+};
+
+// Copies of K block kb into the stage at LDS offset st: this wave's 1 KB
+// pieces (piece p is rows 8 p .. 8 p + 7 of the W tile, then of the X tile)
+// and one of the scales' (several waves write the same bytes, so that every
+// wave has as many copies in flight).  Where W's rows end inside the block, a
+// lane past the end brings bytes of its own row's, which meet zeros of X.
+template <class T>
+__device__ __forceinline__ void fp4_copy_piece(const Fp4Wave& g, uint32_t st, int kb, int i) {
+  if (i < T::LOADS) {
+    const int p = g.wave * T::LOADS + i;   // uniform
+    const bool isw = p < T::BN / 8;
+    uint32_t off = g.off[i];
+    if (T::FP4 && isw && kb == g.tail) {   // uniform
+      const uint32_t chunk = ((g.lane & 7) ^ (((8 * (p & 1) + (g.lane >> 3)) >> 1) & 7)) << 4;
+      off -= chunk < g.left ? 0 : chunk;
+    }
+    lds_copy<16>(isw ? g.rw : g.rx, g.lds + st + p * 1024, off, kb * 128);
+  } else {
+    lds_copy<16>(g.rs, g.lds + st + g.sdst, g.soff, kb * g.sstep);
+  }
+}
+
+// The scale pairs of a K block of this lane's rows.
+template <class T>
+struct Fp4Scales {
+  uint32_t x[T::XW], w[T::WW];
+};
+template <class T>
+__device__ __forceinline__ Fp4Scales<T> fp4_scales(const Fp4Wave& g, const uint8_t* st) {
+  Fp4Scales<T> s;
+#pragma unroll
+  for (int i = 0; i < T::XW; ++i)
+    s.x[i] = T::FM % 2 ? *reinterpret_cast<const uint16_t*>(st + g.sxoff + 2 * i)
+                       : *reinterpret_cast<const uint32_t*>(st + g.sxoff + 4 * i);
+#pragma unroll
+  for (int i = 0; i < T::WW; ++i) s.w[i] = *reinterpret_cast<const uint32_t*>(st + g.swoff + 4 * i);
+  return s;
+}
+
+// The K loop: wait for the block's copies, meet the others (which ends their
+// reads of the previous block's stage), start the copies of block kb + NST -
+// 1 there, multiply: two instructions for each pair of fragments.
+template <class T>
+__device__ __forceinline__ void fp4_loop(const Fp4Wave& g, int kblocks, const uint8_t* lds,
+                                         f32x4 (&acc)[T::FN][T::FM]) {
+  constexpr int FN = T::FN, FM = T::FM, LAST = T::NST * T::STAGE;
+#pragma unroll
+  for (int k = 0; k < T::NST - 1; ++k)
+    if (k < kblocks) {
+#pragma unroll
+      for (int i = 0; i < T::COPIES; ++i) fp4_copy_piece<T>(g, k * T::STAGE, k, i);
+    }
+  int st = 0;
+  for (int kb = 0; kb < kblocks; ++kb) {
+    fp8_wait<T>(min(T::NST - 1, kblocks - kb) - 1);
+    barrier_only();
+    const uint32_t prev = st == 0 ? LAST - T::STAGE : st - T::STAGE;
+    const bool more = kb + T::NST - 1 < kblocks;
+    // with one workgroup on a CU the copies are spread over the rows of
+    // products, with two they go first
+    constexpr int PER = T::SPREAD ? (T::COPIES + FN - 1) / FN : T::COPIES;
+    auto copies = [&](int i) {
+      if (more) {
+#pragma unroll
+        for (int c = i * PER; c < (i + 1) * PER && c < T::COPIES; ++c)
+          fp4_copy_piece<T>(g, prev, kb + T::NST - 1, c);
+      }
+    };
+    const uint8_t* cur = lds + st;
+    if (!T::SPREAD) copies(0);
+    Fp4Scales<T> c;
+    if (T::FP4) c = fp4_scales<T>(g, cur);
+    u32x4 b[FM][2];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      b[j][0] = *reinterpret_cast<const u32x4*>(cur + g.xoff + j * 2048 + g.s0);
+      b[j][1] = *reinterpret_cast<const u32x4*>(cur + g.xoff + j * 2048 + (g.s0 ^ 16));
+    }
+    u32x4 a[2][2];
+    auto frag = [&](int i) {
+      a[i & 1][0] = *reinterpret_cast<const u32x4*>(cur + g.woff + i * 2048 + g.s0);
+      a[i & 1][1] = *reinterpret_cast<const u32x4*>(cur + g.woff + i * 2048 + (g.s0 ^ 16));
+    };
+    frag(0);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      // one workgroup: the next row's fragment is read a row ahead
+      if (T::SPREAD && i + 1 < FN) frag(i + 1);
+      if (!T::SPREAD && i > 0) frag(i);
+      if (T::SPREAD) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+          if constexpr (T::FP4)
+            acc[i][j] = fp4_mfma(fp4_operand(a[i & 1][t]), fp4_operand(b[j][t]), acc[i][j], 2 * (i & 1) + t,
+                                 (int)c.w[i >> 1], FM % 2 ? t : 2 * (j & 1) + t, (int)c.x[FM % 2 ? j : j >> 1]);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[i & 1][t]), as_bf16x8(b[j][t]),
+                                                                acc[i][j], 0, 0, 0);
+        }
+      if (T::SPREAD) {
+        __builtin_amdgcn_sched_barrier(0);
+        copies(i);
+      }
+    }
+    st = st + T::STAGE == LAST ? 0 : st + T::STAGE;
+  }
+}
+
+// One BN x BM tile per workgroup.  In LDS an operand's 16-row fragments follow
+// each other, a row is 128 bytes in 16-byte chunks, and chunk c of fragment row
+// r sits at slot c ^ (r / 2 % 8): the rows that a read touches in one cycle
+// spread over all banks.  W is the MFMA's A operand (D rows n), its rows
+// interleaved over a wave's fragments so that the values of a lane are
+// consecutive n.
+template <class T, bool F32>
+__global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t xp, int ntiles, int mtiles, int first,
+                                                              int count, int splits) {
+  constexpr int FN = T::FN, FM = T::FM, WM = T::WM;
+  __shared__ __align__(1024) uint8_t lds[T::NST * T::STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  Fp4Wave v;
+  v.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  v.lane = lane;
+  // Tiles `first` .. `first + count - 1`: XCD x takes a contiguous range of
+  // them (with splits, every tile's parts one after the other).
+  int nt, mt, split, tile;
+  {
+    const int L = count * splits, b = blockIdx.x;
+    const int x = b & 7, base = L >> 3, extra = L & 7;
+    const int item = x * base + min(x, extra) + (b >> 3);
+    split = item % splits;
+    tile = item / splits;
+    fp8_tile_at(first + tile, ntiles, mtiles, nt, mt);
+  }
+  const int64_t n0 = (int64_t)nt * T::BN, m0 = (int64_t)mt * T::BM;
+  const int all = (int)(xp / 128);   // X's rows are whole K blocks
+  const int kb0 = (int)((int64_t)all * split / splits), kblocks = (int)((int64_t)all * (split + 1) / splits) - kb0;
+  // copies: lane l brings slot l % 8 of row l / 8 of a piece.  Rows past the
+  // matrix repeat its last row (their results are dropped).
+  const int nrows = (int)min((int64_t)T::BN, g.N - n0), mrows = (int)min((int64_t)T::BM, g.M - m0);
+  v.rw = buffer_of(g.w + n0 * g.wp, nrows * g.wp);
+  v.rx = buffer_of(g.x + m0 * xp, mrows * xp);
+  v.lds = (uint32_t)(uintptr_t)(lptr_t)lds;
+  v.tail = g.wp < xp ? all - 1 - kb0 : -1;   // past this part's blocks where it does not have the last one
+  v.left = (uint32_t)(g.wp - (int64_t)(all - 1) * 128);
+#pragma unroll
+  for (int i = 0; i < T::LOADS; ++i) {
+    const int p = v.wave * T::LOADS + i;
+    const bool isw = p < T::BN / 8;
+    const int at = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);   // LDS row of the operand
+    const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
+    const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
+    v.off[i] = (uint32_t)min(row, (isw ? nrows : mrows) - 1) * (uint32_t)(isw ? g.wp : xp) + (uint32_t)kb0 * 128 +
+               (((lane & 7) ^ ((fr >> 1) & 7)) << 4);
+  }
+  if (T::FP4) {
+    // scale copies: 16 bytes a lane, 8 rows' pairs of one q; rows past the
+    // scales repeat their last 16 bytes
+    const int c = v.wave % (T::CX + T::CW);   // uniform
+    const bool isw = c >= T::CX;
+    const int rows = isw ? T::BN : T::BM;
+    const int64_t srows = fp4_scale_rows(isw ? g.N : g.M), at = isw ? n0 : m0;
+    const int chunk = min(64 * (isw ? c - T::CX : c) + lane, rows / 2 - 1);
+    const int q = chunk / (rows / 8), o = 16 * (chunk % (rows / 8));
+    const int left = (int)min((srows - at) * 2, (int64_t)2 * rows);   // bytes of a q, >= 32
+    v.soff = (uint32_t)(q * 2 * srows) + (uint32_t)min(o, left - 16);
+    v.sstep = (uint32_t)(8 * srows);
+    v.sdst = T::SX + c * 1024;
+    v.rs = buffer_of((isw ? g.sw : g.sx) + kb0 * 8 * srows + at * 2, (kblocks - 1) * 8 * srows + 6 * srows + left);
+  }
+  const int wn = v.wave / WM, wm = v.wave % WM;
+  const int r = lane & 15, q = lane >> 4;
+  v.woff = (wn * 16 * FN + r) * 128;
+  v.xoff = (T::BN + wm * 16 * FM + r) * 128;
+  v.s0 = ((2 * q) ^ ((r >> 1) & 7)) << 4;
+  v.sxoff = T::SX + q * 2 * T::BM + 2 * (wm * 16 * FM + r * FM);
+  v.swoff = T::SW + q * 2 * T::BN + 2 * (wn * 16 * FN + fp8_pi(r) * FN);
+  f32x4 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  fp4_loop<T>(v, kblocks, lds, acc);
+  const int64_t nw0 = n0 + wn * 16 * FN;
+  const bool wide = g.N % FN == 0;
+  if (splits > 1) {   // the tile's part, the rows that exist, as [BM][BN] fp32
+    float* part = g.part + ((int64_t)split * count + tile) * (T::BN * T::BM);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      if (wm * 16 * FM + r * FM + j >= mrows) break;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float* d = part + (wm * 16 * FM + r * FM + j) * T::BN + wn * 16 * FN + (4 * t + q) * FN;
+#pragma unroll
+        for (int i = 0; i < FN; i += FN < 4 ? FN : 4) {
+          if constexpr (FN < 4)
+            *reinterpret_cast<f32x2*>(d) = f32x2{acc[0][j][t], acc[1][j][t]};
+          else
+            *reinterpret_cast<f32x4*>(d + i) = f32x4{acc[i][j][t], acc[i + 1][j][t], acc[i + 2][j][t], acc[i + 3][j][t]};
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < FM; ++j)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float o[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) o[i] = acc[i][j][t];
+      fp8_store<FN, F32>(g, m0 + wm * 16 * FM + r * FM + j, nw0 + (4 * t + q) * FN, o, wide);
+    }
+}
+
+// Few rows: a workgroup takes 16 rows of W and its waves split K in units of
+// 128; every wave streams its part of W straight into fragments (lane (r, q):
+// block 4 u + q of row r), and the partial sums meet in LDS in wave order.
+constexpr int FK_NW = 8, FK_CH = 3;   // waves; units in flight per wave
+
+struct SkinnyW4 {
+  u32x4 c[FK_CH];
+  uint32_t s[FK_CH];
+};
+// W's units c0 .. of this lane's row (past u1 - 1 that unit again, not
+// multiplied; chunks past the row's end its last chunk, which meets zeros).
+__device__ __forceinline__ void skinny4_load(const uint8_t* w, int64_t wp, const uint8_t* sw, int64_t srows, int q,
+                                             int c0, int u1, SkinnyW4& f) {
+#pragma unroll
+  for (int i = 0; i < FK_CH; ++i) {
+    const int64_t u = min(c0 + i, u1 - 1);
+    f.c[i] = gload16(w + min(u * 64 + 16 * q, wp - 16));
+    f.s[i] = sw[(u >> 1) * 8 * srows + (2 * (u & 1) + (q >> 1)) * 2 * srows + (q & 1)];
+  }
+}
+// The waves' sums in their order, plus the bias, by the first wave.  Lane l
+// holds D rows 4 (l / 16) .. + 3 (n) of column l % 16 (m).
+template <bool F32>
+__device__ __forceinline__ void skinny4_store(const Fp4Gemm& g, f32x4 (*part)[64], int64_t n0, int wave, int lane) {
+  if (wave) return;
+  f32x4 sum = part[0][lane];
+#pragma unroll
+  for (int u = 1; u < FK_NW; ++u) sum += part[u][lane];
+  float o[4] = {sum[0], sum[1], sum[2], sum[3]};
+  fp8_store<4, F32>(g, lane & 15, n0 + 4 * (lane >> 4), o, g.N % 4 == 0);
+}
+
+// 4-bit X, up to 16 rows.
+template <bool F32>
+__global__ __launch_bounds__(64 * FK_NW) void fp4_skinny_kernel(Fp4Gemm g) {
+  __shared__ f32x4 part[FK_NW][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t xp = fp4_pitch(g.K);
+  const int units = (int)((g.K + 127) / 128);
+  const int u0 = wave * units / FK_NW, u1 = (wave + 1) * units / FK_NW;
+  const int64_t n = min(n0 + r, g.N - 1), m = min((int64_t)r, g.M - 1);
+  const int64_t srw = fp4_scale_rows(g.N), srx = fp4_scale_rows(g.M);
+  const uint8_t *w = g.w + n * g.wp, *x = g.x + m * xp;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c0 = u0; c0 < u1; c0 += FK_CH) {
+    SkinnyW4 fx, fw;
+    skinny4_load(x, xp, g.sx + 2 * m, srx, q, c0, u1, fx);
+    skinny4_load(w, g.wp, g.sw + 2 * n, srw, q, c0, u1, fw);
+#pragma unroll
+    for (int i = 0; i < FK_CH; ++i)
+      if (c0 + i < u1)
+        acc = fp4_mfma<0, 0>(fp4_operand(fw.c[i]), fp4_operand(fx.c[i]), acc, (int)fw.s[i], (int)fx.s[i]);
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  skinny4_store<F32>(g, part, n0, wave, lane);
+}
+
+// bf16 X of up to 16 rows, rounded here: every workgroup rounds all of X into
+// LDS (4 lanes a block) while its first W loads are under way.  LDS unit u of
+// row m is 64 bytes at (u M + m) * 64, its four scales at (u M + m) * 4.
+constexpr int FUSED4_BYTES = 24576, FUSED4_ROUNDS = FUSED4_BYTES / 4 / (64 * FK_NW);
+
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(64 * FK_NW) void fp4_fused_kernel(Fp4Gemm g, const uint16_t* __restrict__ xb) {
+  __shared__ __align__(16) uint8_t xs[FUSED4_BYTES];
+  __shared__ uint8_t sxs[FUSED4_BYTES / 16];
+  __shared__ f32x4 part[FK_NW][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int M = (int)g.M, units = (int)((g.K + 127) / 128);
+  const int u0 = wave * units / FK_NW, u1 = (wave + 1) * units / FK_NW;
+  const int64_t n = min(n0 + r, g.N - 1);
+  const int64_t srw = fp4_scale_rows(g.N);
+  const uint8_t* w = g.w + n * g.wp;
+  // the 8 elements of X of each of this thread's turns, then W's first units
+  const int groups = M * units * 16, turns = (groups + 64 * FK_NW - 1) / (64 * FK_NW);   // turns <= FUSED4_ROUNDS
+  u32x4 xv[FUSED4_ROUNDS];
+#pragma unroll
+  for (int i = 0; i < FUSED4_ROUNDS; ++i) {
+    if (i < turns) {
+      const int id = min(tid + i * 64 * FK_NW, groups - 1), m = id / (units * 16), k0 = 8 * (id % (units * 16));
+      xv[i] = bf16x8_at<VEC>(xb, m * g.K + k0, g.K - k0);
+    }
+  }
+  SkinnyW4 f;
+  if (u0 < u1) skinny4_load(w, g.wp, g.sw + 2 * n, srw, q, u0, u1, f);
+#pragma unroll
+  for (int i = 0; i < FUSED4_ROUNDS; ++i) {
+    const int id = tid + i * 64 * FK_NW, m = id / (units * 16), l = id % (units * 16);
+    if (id < groups) {   // whole blocks: the four lanes of one go together
+      uint32_t s;
+      const uint32_t c = fp4_codes(xv[i], s);
+      const int at = (l >> 4) * M + m;   // its unit
+      *reinterpret_cast<uint32_t*>(xs + at * 64 + 4 * (l & 15)) = c;
+      if ((l & 3) == 0) sxs[at * 4 + ((l >> 2) & 3)] = (uint8_t)s;
+    }
+  }
+  wave_lds_sync();
+  barrier_only();   // leaves W's loads under way
+  const int m = min(r, M - 1);
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c0 = u0; c0 < u1; c0 += FK_CH) {
+    if (c0 > u0) skinny4_load(w, g.wp, g.sw + 2 * n, srw, q, c0, u1, f);
+#pragma unroll
+    for (int i = 0; i < FK_CH; ++i) {
+      if (c0 + i >= u1) continue;
+      const int at = (c0 + i) * M + m;
+      const u32x4 x = *reinterpret_cast<const u32x4*>(xs + at * 64 + 16 * q);
+      acc = fp4_mfma<0, 0>(fp4_operand(f.c[i]), fp4_operand(x), acc, (int)f.s[i], (int)sxs[at * 4 + q]);
+    }
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  skinny4_store<F32>(g, part, n0, wave, lane);
+}
+
+// ------------------------------------------------------------- input's gradient
+
+// W [N, K] decoded and transposed: 64 rows x 128 elements a workgroup, a thread
+// two rows x 8 elements, pairs of rows through LDS as words.
+__global__ __launch_bounds__(256) void fp4_dequant_t_kernel(const uint8_t* __restrict__ w, int64_t wp,
+                                                            const uint8_t* __restrict__ sw, int64_t N, int64_t K,
+                                                            int ktiles, int64_t np, uint16_t* __restrict__ wt) {
+  __shared__ uint32_t t[128][33];
+  const int tid = threadIdx.x;
+  const int64_t n0 = (int64_t)(blockIdx.x / ktiles) * 64, k0 = (int64_t)(blockIdx.x % ktiles) * 128;
+  const int64_t srows = fp4_scale_rows(N);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int pair = tid & 31, grp = 8 * p + (tid >> 5);   // grp: 8 elements
+    const int64_t k = k0 + 8 * grp, b = k >> 5;
+    u32x4 v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = n0 + 2 * pair + h;
+      v[h] = u32x4{0u, 0u, 0u, 0u};
+      if (n < N && k < K) {
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(w + n * wp + k / 2);
+        const uint32_t s = sw[((b >> 3) * 4 + ((b >> 1) & 3)) * srows * 2 + 2 * n + (b & 1)];
+        v[h] = dequant8_bf16(c, scale_operand(s));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t[8 * grp + 2 * i][pair] = (v[0][i] & 0xFFFFu) | (v[1][i] << 16);
+      t[8 * grp + 2 * i + 1][pair] = (v[0][i] >> 16) | (v[1][i] & 0xFFFF0000u);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int k = 32 * p + (tid >> 3), c = 4 * (tid & 7);
+    if (k0 + k < K)
+      *reinterpret_cast<u32x4*>(wt + (k0 + k) * np + n0 + 2 * c) = u32x4{t[k][c], t[k][c + 1], t[k][c + 2], t[k][c + 3]};
+  }
+}
+
+__global__ __launch_bounds__(256) void bf16_pad_kernel(const uint16_t* __restrict__ x, int64_t K, int64_t kp,
+                                                       int64_t total, uint16_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // 8 elements of the result
+  if (i >= total) return;
+  const int64_t row = i / (kp / 8), k = i % (kp / 8) * 8;
+  reinterpret_cast<u32x4*>(out)[i] = bf16x8_at<false>(x, row * K + k, K - k);
+}
+
+// ------------------------------------------------------------------ launchers
+
+hipError_t launch_fp4_quantize(const void* x, int x_f32, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
+                               hipStream_t s) {
+  const int64_t kb = fp4_kblocks(K);
+  const dim3 grid((unsigned)(kb * ((rows + 15) / 16)));
+  const bool vec = K % 8 == 0 && (reinterpret_cast<uintptr_t>(x) % 16) == 0;
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, rows, K, fp4_pitch(K), fp4_scale_rows(rows), (int)kb, codes,
+                       scales);
+    return hipGetLastError();
+  };
+  if (x_f32) return vec ? launch(fp4_rows_kernel<true, true>) : launch(fp4_rows_kernel<true, false>);
+  return vec ? launch(fp4_rows_kernel<false, true>) : launch(fp4_rows_kernel<false, false>);
+}
+
+hipError_t launch_fp4_scales(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* ordered, hipStream_t s) {
+  const int64_t total = fp4_scale_bytes(rows, K) / 2;
+  hipLaunchKernelGGL(fp4_scales_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s, scales, rows, K / 32,
+                     fp4_scale_rows(rows), total, ordered);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp4_dequant_t(const uint8_t* w, int64_t wp, const uint8_t* sw, int64_t N, int64_t K, uint16_t* wt,
+                                hipStream_t s) {
+  const int64_t kt = (K + 127) / 128, nt = (N + 63) / 64;
+  hipLaunchKernelGGL(fp4_dequant_t_kernel, dim3((unsigned)(kt * nt)), dim3(256), 0, s, w, wp, sw, N, K, (int)kt,
+                     fp8_up(N, 64), wt);
+  return hipGetLastError();
+}
+
+hipError_t launch_bf16_pad(const uint16_t* x, int64_t rows, int64_t K, uint16_t* out, hipStream_t s) {
+  const int64_t kp = fp8_up(K, 64), total = rows * kp / 8;
+  hipLaunchKernelGGL(bf16_pad_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s, x, K, kp, total, out);
+  return hipGetLastError();
+}
+
+static constexpr GemmShape FP4_SHAPE[] = {
+    {256, 256, 1, {1.40f, 1.40f}, {1.40f, 1.40f}, {7.5f, 10.3f}},
+    {256, 192, 1, {1.33f, 1.33f}, {1.33f, 1.33f}, {7.2f, 9.3f}},
+    {128, 192, 1, {0.73f, 0.73f}, {0.73f, 0.73f}, {7.0f, 7.4f}},
+    {128, 128, 2, {0.90f, 0.90f}, {0.59f, 0.59f}, {4.9f, 5.8f}},
+    {128, 128, 1, {0.60f, 0.60f}, {0.60f, 0.60f}, {5.7f, 5.8f}},
+    {64, 128, 2, {0.46f, 0.46f}, {0.38f, 0.38f}, {4.4f, 4.6f}},
+    {64, 64, 2, {0.37f, 0.37f}, {0.27f, 0.27f}, {3.9f, 4.0f}},
+    {32, 64, 3, {0.28f, 0.28f}, {0.22f, 0.22f}, {3.7f, 3.8f}},
+    {32, 32, 4, {0.24f, 0.24f}, {0.13f, 0.13f}, {3.5f, 3.5f}},
+};
+constexpr int FP4_SHAPES = (int)(sizeof(FP4_SHAPE) / sizeof(FP4_SHAPE[0]));
+
+static GemmPlan fp4_plan(int64_t M, int64_t N, int64_t K, bool f32) {
+  if (M <= 16 && N >= 1024) return {-1, 0, 0, 1, 0, 0};
+  return gemm_plan(FP4_SHAPE, FP4_SHAPES, M, N, fp4_kblocks(K), f32);
+}
+static GemmPlan bf16_plan(int64_t M, int64_t N, int64_t K, bool f32) {
+  return gemm_plan(FP4_SHAPE, FP4_SHAPES, M, N, K / 64, f32);
+}
+size_t fp4_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
+  return gemm_part_bytes(fp4_plan(M, N, K, out_f32 != 0));
+}
+size_t bf16_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
+  return gemm_part_bytes(bf16_plan(M, N, K, out_f32 != 0));
+}
+
+// Tiles first .. first + count - 1, in `splits` parts of K.
+template <class T>
+static hipError_t gemm_tiles(const Fp4Gemm& g, int64_t xp, int first, int count, int splits, hipStream_t s) {
+  const int nt = (int)((g.N + T::BN - 1) / T::BN), mt = (int)((g.M + T::BM - 1) / T::BM);
+  const dim3 grid((unsigned)((int64_t)count * splits)), block(64 * T::NW);
+  if (g.out_f32)
+    hipLaunchKernelGGL((fp4_gemm_kernel<T, true>), grid, block, 0, s, g, xp, nt, mt, first, count, splits);
+  else
+    hipLaunchKernelGGL((fp4_gemm_kernel<T, false>), grid, block, 0, s, g, xp, nt, mt, first, count, splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  Fp8Gemm j{};
+  j.M = g.M;
+  j.N = g.N;
+  j.K = g.K;
+  j.bias = g.bias;
+  j.out = g.out;
+  j.out_f32 = g.out_f32;
+  j.part = g.part;
+  return launch_gemm_join(j, T::BN, T::BM, first, count, splits, s);
+}
+template <class T>
+static hipError_t gemm(const Fp4Gemm& g, int64_t xp, const GemmPlan& p, hipStream_t s) {
+  if (p.rest && !g.part) return hipErrorInvalidValue;
+  if (p.whole) {
+    const hipError_t e = gemm_tiles<T>(g, xp, 0, p.whole, 1, s);
+    if (e != hipSuccess) return e;
+  }
+  return p.rest ? gemm_tiles<T>(g, xp, p.whole, p.rest, p.splits, s) : hipSuccess;
+}
+template <bool FP4>
+static hipError_t gemm_of(const Fp4Gemm& g, int64_t xp, const GemmPlan& p, hipStream_t s) {
+  switch (p.tile) {
+    case 0: return gemm<Fp4Tile<2, 4, 8, 4, 2, FP4>>(g, xp, p, s);
+    case 1: return gemm<Fp4Tile<2, 4, 8, 3, 2, FP4>>(g, xp, p, s);
+    case 2: return gemm<Fp4Tile<2, 4, 4, 3, 3, FP4>>(g, xp, p, s);
+    case 3: return gemm<Fp4Tile<2, 2, 4, 4, 2, FP4>>(g, xp, p, s);
+    case 4: return gemm<Fp4Tile<2, 2, 4, 4, 3, FP4>>(g, xp, p, s);
+    case 5: return gemm<Fp4Tile<1, 4, 4, 2, 3, FP4>>(g, xp, p, s);
+    case 6: return gemm<Fp4Tile<1, 4, 4, 1, 4, FP4>>(g, xp, p, s);
+    case 7: return gemm<Fp4Tile<1, 4, 2, 1, FP4 ? 3 : 4, FP4>>(g, xp, p, s);
+    default: return gemm<Fp4Tile<1, 2, 2, 1, 4, FP4>>(g, xp, p, s);
+  }
+}
+
+hipError_t launch_fp4_gemm(const Fp4Gemm& g, hipStream_t s) {
+  const GemmPlan p = fp4_plan(g.M, g.N, g.K, g.out_f32 != 0);
+  if (p.tile >= 0) return gemm_of<true>(g, fp4_pitch(g.K), p, s);
+  const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * FK_NW);
+  if (g.out_f32)
+    hipLaunchKernelGGL(fp4_skinny_kernel<true>, grid, block, 0, s, g);
+  else
+    hipLaunchKernelGGL(fp4_skinny_kernel<false>, grid, block, 0, s, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_bf16_gemm(const Fp4Gemm& g, hipStream_t s) {
+  if (g.K % 64) return hipErrorInvalidValue;
+  Fp4Gemm b = g;
+  b.wp = 2 * g.K;
+  return gemm_of<false>(b, 2 * g.K, bf16_plan(g.M, g.N, g.K, g.out_f32 != 0), s);
+}
+
+bool fp4_fused_fits(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 && M * ((K + 127) / 128 * 64) <= FUSED4_BYTES;
+}
+
+hipError_t launch_fp4_fused(const Fp4Gemm& g, const uint16_t* x, hipStream_t s) {
+  if (!fp4_fused_fits(g.M, g.N, g.K)) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * FK_NW);
+  const bool vec = g.K % 8 == 0 && (reinterpret_cast<uintptr_t>(x) % 16) == 0;
+  if (g.out_f32) {
+    if (vec)
+      hipLaunchKernelGGL((fp4_fused_kernel<true, true>), grid, block, 0, s, g, x);
+    else
+      hipLaunchKernelGGL((fp4_fused_kernel<true, false>), grid, block, 0, s, g, x);
+  } else {
+    if (vec)
+      hipLaunchKernelGGL((fp4_fused_kernel<false, true>), grid, block, 0, s, g, x);
+    else
+      hipLaunchKernelGGL((fp4_fused_kernel<false, false>), grid, block, 0, s, g, x);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mxmoe

@@ -14,10 +14,10 @@
 // tile have theirs side by side.
 #include "common.hpp"
 #include "fp8.hpp"
+#include "ring.hpp"
 
 namespace mxmoe {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------- quantizers
 
@@ -250,8 +250,6 @@ __global__ __launch_bounds__(256) void fp8_transpose_kernel(
 // are consecutive n (one wide store), and the four lanes q side by side
 // fill 64-byte pieces.  X: fragment j, column c is row c * F_M + j, so a
 // lane's F_M scale bytes are one load, picked by op_sel.
-__device__ __forceinline__ int fp8_pi(int r) { return 4 * (r & 3) + (r >> 2); }
-
 template <int SEL_A, int SEL_B>
 __device__ __forceinline__ f32x4 fp8_mfma(const i32x8& a, const i32x8& b, f32x4 c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, SEL_A, sa, SEL_B, sb);
@@ -302,50 +300,6 @@ __device__ __forceinline__ void fp8_to_bf16(const i32x8& c, uint32_t scale, bf16
 }
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
 
-// F consecutive outputs out[m][n ..], plus the bias; whole vectors where
-// the row allows it.
-template <int F, bool F32>
-__device__ __forceinline__ void fp8_store(const Fp8Gemm& g, int64_t m, int64_t n, float (&v)[F],
-                                          bool wide) {
-  if (m >= g.M || n >= g.N) return;
-  if (g.bias) {
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-      if (n + i < g.N) v[i] += bf16_to_f32(g.bias[n + i]);
-  }
-  const int64_t at = m * g.N + n;
-  if (wide) {   // N % F == 0: the F values exist and are aligned
-    if constexpr (F == 2) {
-      if (F32)
-        *reinterpret_cast<f32x2*>(static_cast<float*>(g.out) + at) = f32x2{v[0], v[1]};
-      else
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + at) = pack_bf16x2(v[0], v[1]);
-    } else if constexpr (F32) {
-      f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
-#pragma unroll
-      for (int i = 0; i < F / 4; ++i) d[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-    } else {
-      u32x2* d = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + at);
-      if (F == 8)
-        *reinterpret_cast<u32x4*>(d) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                             pack_bf16x2(v[F - 4], v[F - 3]), pack_bf16x2(v[F - 2], v[F - 1])};
-      else
-        d[0] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < F; ++i)
-    if (n + i < g.N) {
-      if (F32)
-        static_cast<float*>(g.out)[at + i] = v[i];
-      else
-        static_cast<uint16_t*>(g.out)[at + i] = (uint16_t)f32_to_bf16(v[i]);
-    }
-}
-
-constexpr int FP8_RSRC_W3 = 0x00020000;   // raw buffer, untyped
-
 // A workgroup's tile: WN x WM waves of (16 FN) x (16 FM), and NST LDS stages.
 // A stage holds one K block: BN rows of W and BM rows of X (128 bytes each),
 // X's BM scale bytes (room for 256) and W's scales (256 bytes).
@@ -356,6 +310,7 @@ struct Fp8Tile {
   static constexpr int BN = WN * FN * 16, BM = WM * FM * 16;
   static constexpr int SX = (BN + BM) * 128, SW = SX + 256, STAGE = SW + 256;
   static constexpr int LOADS = (BN + BM) / 8 / NW;   // 1 KB copies per wave and step
+  static constexpr int COPIES = LOADS + 1;           // and one of scales
   static_assert(LOADS <= 8 && LOADS * NW * 8 == BN + BM && NW % 2 == 0, "copies");
   static_assert(BN <= 256 && BM <= 256 && NST >= 2 && NST * STAGE <= 160 * 1024, "LDS");
   static_assert((NST - 1) * (LOADS + 1) < 64, "vector-memory counter");
@@ -363,38 +318,6 @@ struct Fp8Tile {
   // scale bytes of X and W are read four at a time, or with F % 4 one by one
   static constexpr int XW = FM % 4 ? FM : FM / 4, WW = FN % 4 ? FN : FN / 4;
 };
-
-// Copy from global memory to LDS: 16, 4 or 1 bytes a lane from base + off +
-// soff to LDS address lds + (16, 4, 4) * lane.  As assembly, because the
-// compiler makes every later LDS read wait for every such copy in flight
-// that it cannot prove to go elsewhere, and with a ring of stages it can
-// prove nothing.  The kernel waits itself (fp8_wait) before it reads a
-// stage.  A copy has no output register; its address is read at issue.  m0
-// is a reserved register, which the compiler writes right before each use of
-// its own: the clobber keeps such a pair on one side of a copy (none of these
-// kernels has one), and its warning says only that m0 is not saved.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-template <int BYTES>
-__device__ __forceinline__ void lds_copy(u32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
-  if (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "m0", "memory");
-  else if (BYTES == 4)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "m0", "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "m0", "memory");
-}
-#pragma clang diagnostic pop
-// Raw buffer of `bytes` bytes at p (a wave-uniform pointer).
-__device__ __forceinline__ u32x4 buffer_of(const uint8_t* p, int64_t bytes) {
-  const uint64_t a = (uint64_t)(uintptr_t)p;
-  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)FP8_RSRC_W3};
-}
 
 // A wave's part of a tile's main loop.
 struct Fp8Wave {
@@ -427,27 +350,6 @@ template <class T, bool WROWS>
 __device__ __forceinline__ void fp8_copy(const Fp8Wave& g, uint32_t st, int kb) {
 #pragma unroll
   for (int i = 0; i <= T::LOADS; ++i) fp8_copy_piece<T, WROWS>(g, st, kb, i);
-}
-
-// Wait until at most `blocks` K blocks' copies of this wave are under way,
-// and for all its LDS reads.
-template <class T>
-__device__ __forceinline__ void fp8_wait(int blocks) {
-  // a constant for every count that a ring of up to 4 stages has
-  if (blocks <= 0)
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-  else if (blocks == 1 || T::NST <= 2)
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(T::LOADS + 1, 0));
-  else if (blocks == 2 || T::NST <= 3)
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * (T::LOADS + 1), 0));
-  else
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * (T::LOADS + 1), 0));
-}
-
-__device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p, int s0) {
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(p + s0);
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(p + (s0 ^ 16));
-  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
 // A K block's scales of this lane's rows: words of four bytes, or bytes.
@@ -541,15 +443,6 @@ __device__ __forceinline__ void fp8_loop(const Fp8Wave& g, int kblocks, const ui
     }
     st = st + T::STAGE == LAST ? 0 : st + T::STAGE;
   }
-}
-
-// Tile `item` of the order in which bands of 8 m-tiles run through all
-// n-tiles, m fastest.
-__device__ __forceinline__ void fp8_tile_at(int item, int ntiles, int mtiles, int& nt, int& mt) {
-  const int band = item / (8 * ntiles), rows = min(8, mtiles - 8 * band);
-  const int local = item - band * 8 * ntiles;
-  mt = band * 8 + local % rows;
-  nt = local / rows;
 }
 
 // One BN x BM tile per workgroup; K in steps of one scale block (128).  In
@@ -921,6 +814,16 @@ hipError_t launch_fp8_transpose(const uint8_t* codes, const uint8_t* scales, int
   return hipGetLastError();
 }
 
+hipError_t launch_gemm_join(const Fp8Gemm& g, int bn, int bm, int first, int count, int splits, hipStream_t s) {
+  const int nt = (int)((g.N + bn - 1) / bn), mt = (int)((g.M + bm - 1) / bm);
+  const dim3 join((unsigned)((int64_t)count * (bn * bm / 1024)));
+  if (g.out_f32)
+    hipLaunchKernelGGL(fp8_join_kernel<true>, join, dim3(256), 0, s, g, nt, mt, first, count, splits, bn, bm);
+  else
+    hipLaunchKernelGGL(fp8_join_kernel<false>, join, dim3(256), 0, s, g, nt, mt, first, count, splits, bn, bm);
+  return hipGetLastError();
+}
+
 // Tiles first .. first + count - 1, in `splits` parts of K.
 template <class T>
 static hipError_t gemm_tiles(const Fp8Gemm& g, int first, int count, int splits, hipStream_t s) {
@@ -937,14 +840,8 @@ static hipError_t gemm_tiles(const Fp8Gemm& g, int first, int count, int splits,
     else
       hipLaunchKernelGGL((fp8_gemm_kernel<T, false, false>), grid, block, 0, s, g, nt, mt, first, count, splits);
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  const dim3 join((unsigned)((int64_t)count * (T::BN * T::BM / 1024)));
-  if (g.out_f32)
-    hipLaunchKernelGGL(fp8_join_kernel<true>, join, dim3(256), 0, s, g, nt, mt, first, count, splits, T::BN, T::BM);
-  else
-    hipLaunchKernelGGL(fp8_join_kernel<false>, join, dim3(256), 0, s, g, nt, mt, first, count, splits, T::BN, T::BM);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || splits == 1 ? e : launch_gemm_join(g, T::BN, T::BM, first, count, splits, s);
 }
 
 static hipError_t skinny(const Fp8Gemm& g, hipStream_t s) {
@@ -963,16 +860,7 @@ static hipError_t skinny(const Fp8Gemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-// How a product runs: a tile (-1: few rows), the tiles that are computed
-// whole, and the parts of K in which the others are.
-struct Fp8Plan {
-  int tile, whole, rest, splits;
-};
-
-// The tiles, W rows x X rows, with what a launch of each takes, for bf16 and
-// for fp32 results: `lat` us for a K block while a CU has one workgroup, `thr`
-// us for each workgroup that a CU has when it has more, and `c` us for every
-// `res` of them (launch, first copies, stores).  Fitted to launches of 64 to
+// The tiles' times (GemmShape), for bf16 and for fp32 results.  Fitted to launches of 64 to
 // 2048 rows by 5760 x 2880, 2880 x 5760, 4096 x 4096 and 8192 x 1024 whose W
 // comes from HBM; over 170 sizes of 1 to 2048 rows the choice is 1% slower on
 // average than the best of all tiles and parts, at most 20%.
@@ -988,11 +876,7 @@ struct Fp8Plan {
 //   64 x 64    12.2  12.6   17.8   26.6   44.2   84.1
 //   32 x 64    10.1  14.1   18.7   31.0   54.8   99.5
 //   32 x 32    10.5  12.8   22.6   35.6   64.7    121   (32 rows: 8.9)
-struct Fp8Shape {
-  int bn, bm, res;
-  float lat[2], thr[2], c[2];
-};
-static constexpr Fp8Shape FP8_SHAPE[] = {
+static constexpr GemmShape FP8_SHAPE[] = {
     {256, 256, 1, {1.40f, 2.52f}, {1.40f, 2.52f}, {7.5f, 10.3f}},
     {256, 192, 1, {1.33f, 2.12f}, {1.33f, 2.12f}, {7.2f, 9.3f}},
     {128, 192, 1, {0.73f, 1.28f}, {0.73f, 1.28f}, {7.0f, 7.4f}},
@@ -1008,16 +892,11 @@ static constexpr Fp8Shape FP8_SHAPE[] = {
 // may be split over K, in parts of 3 blocks or more; another launch joins the
 // fp32 parts, which costs the launches and the parts' bytes (written and read
 // at 4 TB/s).
-static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
-  // one fragment of rows: streaming W in 16-row groups over K, while there are
-  // enough of these (16 rows, 5760 x 2880: 8.4 us against 8.9 in 32 x 32
-  // tiles; 4096 x 4096: 7.4, 9.6; 512 x 8192: 10.7, 7.8)
-  if (M <= 16 && N >= 1024) return {-1, 0, 0, 1};
-  const int64_t kb = fp8_pitch(K) / 128;
-  Fp8Plan best{};
+GemmPlan gemm_plan(const GemmShape* shapes, int count, int64_t M, int64_t N, int64_t kb, bool f32) {
+  GemmPlan best{};
   float least = -1.0f;
-  for (int i = 0; i < (int)(sizeof(FP8_SHAPE) / sizeof(FP8_SHAPE[0])); ++i) {
-    const Fp8Shape& t = FP8_SHAPE[i];
+  for (int i = 0; i < count; ++i) {
+    const GemmShape& t = shapes[i];
     const int64_t tiles = ((N + t.bn - 1) / t.bn) * ((M + t.bm - 1) / t.bm);
     if (tiles > 1 << 23) continue;   // more than a launch takes; the wide ones of such a product are fewer
     auto launch = [&](int64_t groups, int64_t blocks) {
@@ -1028,7 +907,7 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
     const float us = launch(tiles, kb);
     if (least < 0.0f || us < least) {
       least = us;
-      best = {i, (int)tiles, 0, 1};
+      best = {i, (int)tiles, 0, 1, 0, 0};
     }
     const int64_t rest = tiles % (256 * t.res);
     if (rest == 0 || rest > 128) continue;
@@ -1039,19 +918,28 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
     const float split = launch(tiles - rest, kb) + launch(rest * s, (kb + s - 1) / s) + join;
     if (split < least) {
       least = split;
-      best = {i, (int)(tiles - rest), (int)rest, (int)s};
+      best = {i, (int)(tiles - rest), (int)rest, (int)s, 0, 0};
     }
   }
+  best.bn = shapes[best.tile].bn;
+  best.bm = shapes[best.tile].bm;
   return best;
 }
 
+static GemmPlan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32) {
+  // one fragment of rows: streaming W in 16-row groups over K, while there are
+  // enough of these (16 rows, 5760 x 2880: 8.4 us against 8.9 in 32 x 32
+  // tiles; 4096 x 4096: 7.4, 9.6; 512 x 8192: 10.7, 7.8)
+  if (M <= 16 && N >= 1024) return {-1, 0, 0, 1, 0, 0};
+  return gemm_plan(FP8_SHAPE, (int)(sizeof(FP8_SHAPE) / sizeof(FP8_SHAPE[0])), M, N, fp8_pitch(K) / 128, f32);
+}
+
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
-  const Fp8Plan p = fp8_plan(M, N, K, out_f32 != 0);
-  return p.rest ? (size_t)p.splits * p.rest * FP8_SHAPE[p.tile].bn * FP8_SHAPE[p.tile].bm * sizeof(float) : 0;
+  return gemm_part_bytes(fp8_plan(M, N, K, out_f32 != 0));
 }
 
 template <class T>
-static hipError_t gemm(const Fp8Gemm& g, const Fp8Plan& p, hipStream_t s) {
+static hipError_t gemm(const Fp8Gemm& g, const GemmPlan& p, hipStream_t s) {
   if (p.rest && !g.part) return hipErrorInvalidValue;
   if (p.whole) {
     const hipError_t e = gemm_tiles<T>(g, 0, p.whole, 1, s);
@@ -1061,7 +949,7 @@ static hipError_t gemm(const Fp8Gemm& g, const Fp8Plan& p, hipStream_t s) {
 }
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
-  const Fp8Plan p = fp8_plan(g.M, g.N, g.K, g.out_f32 != 0);
+  const GemmPlan p = fp8_plan(g.M, g.N, g.K, g.out_f32 != 0);
   switch (p.tile) {
     case 0: return gemm<Fp8Tile<2, 4, 8, 4, 2>>(g, p, s);
     case 1: return gemm<Fp8Tile<2, 4, 8, 3, 2>>(g, p, s);

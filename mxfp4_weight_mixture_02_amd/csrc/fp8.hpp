@@ -41,6 +41,27 @@ struct Fp8Gemm {
   int out_f32;
   float* part;              // fp8_part_bytes of scratch
 };
+// Tiles of a product, W rows x X rows, with what a launch of them takes (bf16
+// and fp32 results): `lat` us for a K block (128 bytes of a row) while a CU has
+// one workgroup, `thr` us for each workgroup that a CU has when it has more,
+// and `c` us for every `res` of them (launch, first copies, stores).
+struct GemmShape {
+  int bn, bm, res;
+  float lat[2], thr[2], c[2];
+};
+// How a product runs: a tile (-1: few rows), the tiles that are computed
+// whole, and the parts of K in which the others are.
+struct GemmPlan {
+  int tile, whole, rest, splits, bn, bm;
+};
+GemmPlan gemm_plan(const GemmShape* shapes, int count, int64_t M, int64_t N, int64_t kblocks, bool f32);
+inline size_t gemm_part_bytes(const GemmPlan& p) {
+  return p.rest ? (size_t)p.splits * p.rest * p.bn * p.bm * sizeof(float) : 0;
+}
+// the sum of the parts of tiles first .. first + count - 1 (of g: M, N, bias,
+// out, out_f32, part)
+hipError_t launch_gemm_join(const Fp8Gemm& g, int bn, int bm, int first, int count, int splits, hipStream_t s);
+
 // out = X W^T + bias
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32);
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s);

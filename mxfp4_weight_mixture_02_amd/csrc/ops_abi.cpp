@@ -7,6 +7,7 @@
 
 #include "abi_util.hpp"
 #include "balance.hpp"
+#include "fp4.hpp"
 #include "fp8.hpp"
 #include "gate.hpp"
 #include "norm.hpp"
@@ -182,6 +183,78 @@ Fp8Layout fp8_layout(int64_t M, int64_t N, int64_t K, bool w, int out_f32) {
 
 size_t matmul_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
   return up(mxmoe::fp8_part_bytes(M, N, K, out_dtype == MXMOE_F32), ALIGN) + ALIGN;
+}
+
+// A 4-bit matrix, and the pitch of its codes (0: not given).
+int check_fp4(int64_t rows, int64_t K, int64_t pitch, const char* what) {
+  if (rows < 1 || K < 1)
+    return fail(MXFP4_EINVAL, "%s: sizes must be >= 1 (%lld x %lld)", what, (long long)rows, (long long)K);
+  if (rows >= (int64_t(1) << 27) || K > FP8_MAX_K)
+    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld (rows must be < 2^27, K <= 2^22)", what, (long long)rows,
+                (long long)K);
+  // the scales of a K block are reached by 32-bit offsets
+  if ((rows + 255) * 2 * mxmoe::fp4_pitch(K) >= (int64_t(1) << 35))
+    return fail(MXFP4_EUNSUPPORTED, "%s: %lld x %lld elements (must be < 2^35)", what, (long long)rows, (long long)K);
+  if (pitch && pitch != mxmoe::fp4_pitch(K) && (pitch != K / 2 || K % 32))
+    return fail(MXFP4_EINVAL, "%s: rows of %lld bytes (%lld, or K / 2 with K a multiple of 32)", what, (long long)pitch,
+                (long long)mxmoe::fp4_pitch(K));
+  return MXFP4_OK;
+}
+
+int check_tiles(int64_t M, int64_t N) {
+  if (((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 23))
+    return fail(MXFP4_EUNSUPPORTED, "%lld x %lld: too many tiles", (long long)M, (long long)N);
+  return MXFP4_OK;
+}
+
+int check_product4(int64_t M, int64_t N, int64_t K, int64_t w_pitch) {
+  int rc = check_fp4(M, K, 0, "X");
+  if (!rc) rc = check_fp4(N, K, w_pitch, "W");
+  if (!rc) rc = check_tiles(M, N);
+  // few rows: a workgroup of 512 threads for 16 rows of W
+  if (!rc && M <= 16 && !launchable((N + 15) / 16, 512))
+    rc = fail(MXFP4_EUNSUPPORTED, "M=%lld N=%lld: N must be <= 2^27 - 16 for up to 16 rows", (long long)M, (long long)N);
+  return rc;
+}
+
+// dX [M, K] = dY W: a product of K rows of W's transpose, along N.
+int check_dx4(int64_t M, int64_t N, int64_t K, int64_t w_pitch) {
+  int rc = check_fp4(N, K, w_pitch, "W");
+  if (rc) return rc;
+  if (M < 1) return fail(MXFP4_EINVAL, "M=%lld must be >= 1", (long long)M);
+  const int64_t np = mxmoe::fp8_up(N, 64), most = int64_t(1) << 35;
+  if (M >= (int64_t(1) << 27) || N > FP8_MAX_K || (M + 255) * np >= most || (K + 255) * np >= most)
+    return fail(MXFP4_EUNSUPPORTED, "dY %lld x %lld, W %lld x %lld: too large", (long long)M, (long long)N, (long long)N,
+                (long long)K);
+  return check_tiles(M, K);
+}
+
+// Workspace of a linear layer: X's codes and scales, then the product's own;
+// of its dX: W transposed, dY with padded rows, then the product's own.
+struct Fp4Layout {
+  size_t second, part, total;
+};
+Fp4Layout fp4_layout(int64_t M, int64_t N, int64_t K, int out_f32) {
+  Fp4Layout L{};
+  if (mxmoe::fp4_fused_fits(M, N, K)) {   // X never leaves the product's launch
+    L.total = ALIGN;
+    return L;
+  }
+  L.second = up((size_t)M * mxmoe::fp4_pitch(K), ALIGN);
+  L.part = L.second + up((size_t)mxmoe::fp4_scale_bytes(M, K), ALIGN);
+  L.total = L.part + up(mxmoe::fp4_part_bytes(M, N, K, out_f32), ALIGN);
+  return L;
+}
+Fp4Layout dx4_layout(int64_t M, int64_t N, int64_t K, int out_f32) {
+  const size_t np = (size_t)mxmoe::fp8_up(N, 64);
+  Fp4Layout L{};
+  L.second = up((size_t)K * np * 2, ALIGN);
+  L.part = L.second + up((size_t)M * np * 2, ALIGN);
+  L.total = L.part + up(mxmoe::bf16_part_bytes(M, K, (int64_t)np, out_f32), ALIGN);
+  return L;
+}
+size_t matmul4_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  return up(mxmoe::fp4_part_bytes(M, N, K, out_dtype == MXMOE_F32), ALIGN) + ALIGN;
 }
 
 int check_swiglu8(int64_t R, int64_t I, float alpha, float limit) {
@@ -448,6 +521,140 @@ int mxmoe_fp8_linear_dw(int64_t M, int64_t N, int64_t K, const uint16_t* dy, con
   const mxmoe::Fp8Gemm g{N, K, M, ws, ws + L.xs, ws + L.w, ws + L.ws, 1, nullptr, dw, 1,
                          reinterpret_cast<float*>(ws + L.part)};
   LAUNCH(mxmoe::launch_fp8_gemm(g, s), "fp8_matmul");
+  return ok();
+}
+
+int mxmoe_fp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
+                       void* stream) {
+  int rc = check_fp4(rows, K, 0, "x");
+  if (rc) return rc;
+  if (!x || !codes || !scales) return fail(MXFP4_EINVAL, "x, codes and scales are required");
+  rc = check_dtype(dtype, x, "x");
+  if (rc) return rc;
+  if (!aligned(codes, 16) || !aligned(scales, 16))
+    return fail(MXFP4_EINVAL, "codes and scales must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_fp4_quantize(x, dtype == MXMOE_F32, rows, K, codes, scales, s), "fp4_quantize");
+  return ok();
+}
+
+int mxmoe_fp4_scales(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* ordered, void* stream) {
+  const int rc = check_fp4(rows, K, 0, "scales");
+  if (rc) return rc;
+  if (!scales || !ordered) return fail(MXFP4_EINVAL, "scales and ordered are required");
+  if (K % 32) return fail(MXFP4_EUNSUPPORTED, "K=%lld is not a multiple of 32", (long long)K);
+  if (!aligned(ordered, 16)) return fail(MXFP4_EINVAL, "ordered must be 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH(mxmoe::launch_fp4_scales(scales, rows, K, ordered, s), "fp4_scales");
+  return ok();
+}
+
+size_t mxmoe_fp4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  if (check_product4(M, N, K, 0) != MXFP4_OK || check_dtype(out_dtype, nullptr, "out") != MXFP4_OK) return 0;
+  ok();
+  return matmul4_bytes(M, N, K, out_dtype);
+}
+
+size_t mxmoe_fp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  if (check_product4(M, N, K, 0) != MXFP4_OK || check_dtype(out_dtype, nullptr, "out") != MXFP4_OK) return 0;
+  ok();
+  return fp4_layout(M, N, K, out_dtype == MXMOE_F32).total;
+}
+
+size_t mxmoe_fp4_linear_dx_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  if (check_dx4(M, N, K, 0) != MXFP4_OK || check_dtype(out_dtype, nullptr, "dx") != MXFP4_OK) return 0;
+  ok();
+  return dx4_layout(M, N, K, out_dtype == MXMOE_F32).total;
+}
+
+int mxmoe_fp4_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
+                     const uint8_t* w_codes, int64_t w_pitch, const uint8_t* w_scales, const uint16_t* bias,
+                     int out_dtype, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (w_pitch < 1) return fail(MXFP4_EINVAL, "w_pitch=%lld must be >= 1", (long long)w_pitch);
+  int rc = check_product4(M, N, K, w_pitch);
+  if (rc) return rc;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !out)
+    return fail(MXFP4_EINVAL, "codes, scales and out are required");
+  rc = check_dtype(out_dtype, out, "out");
+  if (rc) return rc;
+  if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) ||
+      !aligned(out, 16) || !aligned(bias, 2))
+    return fail(MXFP4_EINVAL, "codes, scales and out must be 16-byte aligned");
+  rc = check_workspace(workspace, workspace_bytes, matmul4_bytes(M, N, K, out_dtype));
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const mxmoe::Fp4Gemm g{M, N, K, x_codes, x_scales, w_codes, w_scales, w_pitch, bias, out, out_dtype == MXMOE_F32,
+                         static_cast<float*>(workspace)};
+  LAUNCH(mxmoe::launch_fp4_gemm(g, s), "fp4_matmul");
+  return ok();
+}
+
+int mxmoe_fp4_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, const uint8_t* w_codes, int64_t w_pitch,
+                     const uint8_t* w_scales, const uint16_t* bias, int out_dtype, void* out, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (w_pitch < 1) return fail(MXFP4_EINVAL, "w_pitch=%lld must be >= 1", (long long)w_pitch);
+  int rc = check_product4(M, N, K, w_pitch);
+  if (rc) return rc;
+  if (!x || !w_codes || !w_scales || !out)
+    return fail(MXFP4_EINVAL, "x, w_codes, w_scales and out are required");
+  rc = check_dtype(out_dtype, out, "out");
+  if (!rc) rc = check_dtype(MXMOE_BF16, x, "x");
+  if (rc) return rc;
+  if (!aligned(w_codes, 16) || !aligned(w_scales, 16) || !aligned(out, 16) || !aligned(bias, 2))
+    return fail(MXFP4_EINVAL, "w_codes, w_scales and out must be 16-byte aligned");
+  const Fp4Layout L = fp4_layout(M, N, K, out_dtype == MXMOE_F32);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const mxmoe::Fp4Gemm g{M, N, K, ws, ws + L.second, w_codes, w_scales, w_pitch, bias, out, out_dtype == MXMOE_F32,
+                         reinterpret_cast<float*>(ws + L.part)};
+  if (mxmoe::fp4_fused_fits(M, N, K)) {
+    LAUNCH(mxmoe::launch_fp4_fused(g, x, s), "fp4_linear");
+    return ok();
+  }
+  LAUNCH(mxmoe::launch_fp4_quantize(x, 0, M, K, ws, ws + L.second, s), "fp4_quantize");
+  LAUNCH(mxmoe::launch_fp4_gemm(g, s), "fp4_matmul");
+  return ok();
+}
+
+int mxmoe_fp4_linear_dx(int64_t M, int64_t N, int64_t K, const uint16_t* dy, const uint8_t* w_codes,
+                        int64_t w_pitch, const uint8_t* w_scales, int out_dtype, void* dx, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (w_pitch < 1) return fail(MXFP4_EINVAL, "w_pitch=%lld must be >= 1", (long long)w_pitch);
+  int rc = check_dx4(M, N, K, w_pitch);
+  if (rc) return rc;
+  if (!dy || !w_codes || !w_scales || !dx)
+    return fail(MXFP4_EINVAL, "dy, w_codes, w_scales and dx are required");
+  rc = check_dtype(out_dtype, dx, "dx");
+  if (!rc) rc = check_dtype(MXMOE_BF16, dy, "dy");
+  if (rc) return rc;
+  if (!aligned(w_codes, 16) || !aligned(w_scales, 16) || !aligned(dx, 16))
+    return fail(MXFP4_EINVAL, "w_codes, w_scales and dx must be 16-byte aligned");
+  const Fp4Layout L = dx4_layout(M, N, K, out_dtype == MXMOE_F32);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int64_t np = mxmoe::fp8_up(N, 64);
+  LAUNCH(mxmoe::launch_fp4_dequant_t(w_codes, w_pitch, w_scales, N, K, reinterpret_cast<uint16_t*>(ws), s),
+         "fp4_dequant_t");
+  const uint16_t* rows = dy;
+  if (N != np || !aligned(dy, 16)) {
+    uint16_t* pad = reinterpret_cast<uint16_t*>(ws + L.second);
+    LAUNCH(mxmoe::launch_bf16_pad(dy, M, N, pad, s), "bf16_pad");
+    rows = pad;
+  }
+  mxmoe::Fp4Gemm g{};
+  g.M = M;
+  g.N = K;
+  g.K = np;
+  g.x = reinterpret_cast<const uint8_t*>(rows);
+  g.w = ws;
+  g.out = dx;
+  g.out_f32 = out_dtype == MXMOE_F32;
+  g.part = reinterpret_cast<float*>(ws + L.part);
+  LAUNCH(mxmoe::launch_bf16_gemm(g, s), "bf16_matmul");
   return ok();
 }
 

@@ -1,5 +1,5 @@
 """ctypes binding of the operators in include/mxmoe_ops.h: routing with its
-gradient, dense products in 8-bit floating point, 8-bit activation
+gradient, dense products in 8- and 4-bit floating point, 8-bit activation
 checkpoints, the router's balance losses and the norm before a layer.
 
 Argument marshalling only, as in native.py.  Each call runs on its tensors'
@@ -50,6 +50,14 @@ def lib() -> ctypes.CDLL:
         L.mxmoe_fp8_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, ci, vp, ci, vp, vp, sz, vp]
         L.mxmoe_fp8_linear.argtypes = [i64, i64, i64, vp, vp, vp, vp, ci, vp, vp, sz, vp]
         L.mxmoe_fp8_linear_dw.argtypes = [i64, i64, i64, vp, vp, vp, vp, sz, vp]
+        for n in ("matmul", "linear", "linear_dx"):
+            f = getattr(L, f"mxmoe_fp4_{n}_workspace_bytes")
+            f.restype, f.argtypes = sz, [i64, i64, i64, ci]
+        L.mxmoe_fp4_quantize.argtypes = [vp, ci, i64, i64, vp, vp, vp]
+        L.mxmoe_fp4_scales.argtypes = [vp, i64, i64, vp, vp]
+        L.mxmoe_fp4_matmul.argtypes = [i64, i64, i64, vp, vp, vp, i64, vp, vp, ci, vp, vp, sz, vp]
+        L.mxmoe_fp4_linear.argtypes = [i64, i64, i64, vp, vp, i64, vp, vp, ci, vp, vp, sz, vp]
+        L.mxmoe_fp4_linear_dx.argtypes = [i64, i64, i64, vp, vp, i64, vp, ci, vp, vp, sz, vp]
         layer = [ctypes.POINTER(Dims), ctypes.POINTER(Weights)]
         L.mxmoe_router_logits.argtypes = [i64, i64, i32] + [vp] * 5
         L.mxmoe_forward_routed.argtypes = layer + [vp, vp, ctypes.POINTER(Saved), vp, sz, vp]
@@ -69,7 +77,8 @@ def lib() -> ctypes.CDLL:
         for n in ("route", "route_backward", "router_logits", "forward_routed", "backward_routed", "fp8_quantize",
                   "fp8_quantize_t", "fp8_transpose", "fp8_matmul", "fp8_linear", "fp8_linear_dw",
                   "swiglu8_forward", "swiglu8_backward", "swiglu8_restore", "rms_norm", "rms_norm_backward",
-                  "balance", "balance_backward"):
+                  "balance", "balance_backward", "fp4_quantize", "fp4_scales", "fp4_matmul", "fp4_linear",
+                  "fp4_linear_dx"):
             getattr(L, "mxmoe_" + n).restype = ci
         _lib = L
     return _lib
@@ -534,6 +543,118 @@ def fp8_linear_dw(dy: torch.Tensor, x: torch.Tensor) -> torch.Tensor:
     dw = torch.empty((N, K), dtype=torch.float32, device=dev)
     _call("mxmoe_fp8_linear_dw", dev, M, N, K, _p(dy), _p(x), _p(dw), _p(ws), nbytes)
     return dw
+
+
+# ------------------------------------------------------ 4-bit dense products
+
+@dataclass
+class Fp4Matrix:
+    """A [rows, K] matrix in MXFP4 (E2M1, a power-of-two scale for each 32 of
+    K), with its scales in the order of the products (layouts in mxmoe_ops.h).
+    Rows of codes are K / 2 bytes (a checkpoint's, K a multiple of 32) or
+    padded to 256 elements."""
+    codes: torch.Tensor      # uint8 [rows, K / 2 | K rounded up to 256, / 2]
+    scales: torch.Tensor     # uint8 [K blocks of 256, 4, rows rounded up to 16, 2]
+    K: int
+
+    @property
+    def rows(self):
+        return self.codes.shape[0]
+
+    @staticmethod
+    def empty(rows, K, device):
+        if rows < 1 or K < 1:
+            raise ValueError(f"a 4-bit matrix has at least one element, got {rows} x {K}")
+        Kp, u8 = _up(K, 256), dict(dtype=torch.uint8, device=device)
+        return Fp4Matrix(torch.empty((rows, Kp // 2), **u8), torch.empty((Kp // 256, 4, _up(rows, 16), 2), **u8), K)
+
+    def check_shapes(self, name="matrix", padded=False):
+        """``padded``: rows of K / 2 bytes will not do."""
+        if self.codes.dim() != 2 or self.K < 1:
+            raise ValueError(f"{name}: codes must be [rows, bytes]")
+        Kp, pitch = _up(self.K, 256), self.codes.shape[1]
+        if pitch != Kp // 2 and (padded or self.K % 32 or pitch != self.K // 2):
+            raise ValueError(f"{name}: rows of {pitch} bytes do not hold K={self.K}" +
+                             (" padded to a multiple of 256" if padded else ""))
+        _shape(self.codes, (self.rows, pitch), torch.uint8, name + ".codes")
+        _shape(self.scales, (Kp // 256, 4, _up(self.rows, 16), 2), torch.uint8, name + ".scales")
+
+
+def fp4_quantize(x: torch.Tensor) -> Fp4Matrix:
+    """fp32 or bf16 x [rows, K] in MXFP4, with padded rows."""
+    rows, K = _matrix(x, "x")
+    dev = _same_device(x=x)
+    q = Fp4Matrix.empty(rows, K, dev)
+    _call("mxmoe_fp4_quantize", dev, _p(x), _DTYPES[x.dtype], rows, K, _p(q.codes), _p(q.scales))
+    return q
+
+
+def fp4_matrix(codes: torch.Tensor, scales: torch.Tensor) -> Fp4Matrix:
+    """mxfp4_quantize's codes [rows, K / 2], which stay where they are, and
+    scales [rows, K / 32], copied into the products' order: once for a
+    checkpoint's weights."""
+    if codes.dim() != 2 or codes.shape[1] % 16 or min(codes.shape) < 1:
+        raise ValueError(f"codes must be [rows, K / 2], K a multiple of 32, got {tuple(codes.shape)}")
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    _shape(codes, (rows, K // 2), torch.uint8, "codes")
+    _shape(scales, (rows, K // 32), torch.uint8, "scales")
+    dev = _same_device(codes=codes, scales=scales)
+    ordered = torch.empty((_up(K, 256) // 256, 4, _up(rows, 16), 2), dtype=torch.uint8, device=dev)
+    _call("mxmoe_fp4_scales", dev, _p(scales), rows, K, _p(ordered))
+    return Fp4Matrix(codes, ordered, K)
+
+
+def fp4_matmul(x: Fp4Matrix, w: Fp4Matrix, bias: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """x [M, K] (padded rows, as fp4_quantize makes them) times w [N, K]
+    transposed, plus bias bf16 [N]: [M, N] in dtype."""
+    x.check_shapes("x", padded=True)
+    w.check_shapes("w")
+    if x.K != w.K:
+        raise ValueError(f"x has K={x.K}, w K={w.K}")
+    M, N = x.rows, w.rows
+    _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
+    dev = _same_device(x=x.codes, x_scales=x.scales, w=w.codes, w_scales=w.scales, bias=bias)
+    out = _out(M, N, dtype, dev)
+    ws, nbytes = _workspace("mxmoe_fp4_matmul_workspace_bytes", dev, M, N, x.K, _DTYPES[dtype])
+    _call("mxmoe_fp4_matmul", dev, M, N, x.K, _p(x.codes), _p(x.scales), _p(w.codes), w.codes.shape[1], _p(w.scales),
+          _p(bias), _DTYPES[dtype], _p(out), _p(ws), nbytes)
+    return out
+
+
+def fp4_linear(x: torch.Tensor, w: Fp4Matrix, bias: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """bf16 x [M, K] rounded to MXFP4, times w [N, K] transposed, plus bias:
+    [M, N]."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
+    w.check_shapes("w")
+    M, N, K = x.shape[0], w.rows, w.K
+    _shape(x, (M, K), torch.bfloat16, "x")
+    _shape(bias, (N,), torch.bfloat16, "bias", optional=True)
+    dev = _same_device(x=x, w=w.codes, w_scales=w.scales, bias=bias)
+    out = _out(M, N, dtype, dev)
+    ws, nbytes = _workspace("mxmoe_fp4_linear_workspace_bytes", dev, M, N, K, _DTYPES[dtype])
+    _call("mxmoe_fp4_linear", dev, M, N, K, _p(x), _p(w.codes), w.codes.shape[1], _p(w.scales), _p(bias),
+          _DTYPES[dtype], _p(out), _p(ws), nbytes)
+    return out
+
+
+def fp4_linear_dx(dy: torch.Tensor, w: Fp4Matrix, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The input's gradient of fp4_linear over frozen weights, the rounding of
+    its input passed straight through: bf16 dy [M, N], not rounded, times w
+    [N, K]: [M, K]."""
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be [M, N], got {tuple(dy.shape)}")
+    w.check_shapes("w")
+    M, N, K = dy.shape[0], w.rows, w.K
+    _shape(dy, (M, N), torch.bfloat16, "dy")
+    dev = _same_device(dy=dy, w=w.codes, w_scales=w.scales)
+    out = _out(M, K, dtype, dev)
+    ws, nbytes = _workspace("mxmoe_fp4_linear_dx_workspace_bytes", dev, M, N, K, _DTYPES[dtype])
+    _call("mxmoe_fp4_linear_dx", dev, M, N, K, _p(dy), _p(w.codes), w.codes.shape[1], _p(w.scales), _DTYPES[dtype],
+          _p(out), _p(ws), nbytes)
+    return out
 
 
 # ------------------------------------------------- 8-bit activation checkpoints
