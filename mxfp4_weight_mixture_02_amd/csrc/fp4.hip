@@ -15,6 +15,8 @@
 // feeds row r's elements 64 q .. 64 q + 63 of a block of 256, in two
 // instructions, so [K block][q][row][2] puts the two scales of all rows of a
 // lane side by side.
+#include <type_traits>
+
 #include "common.hpp"
 #include "fp4.hpp"
 #include "ring.hpp"
@@ -22,6 +24,7 @@
 namespace mxmoe {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------- quantizer
 
@@ -191,13 +194,14 @@ __device__ __forceinline__ f32x4 fp4_mfma(const i32x8& a, const i32x8& b, f32x4 
 }
 // 16 bytes of codes as an operand (4-bit formats read its first four registers)
 __device__ __forceinline__ i32x8 fp4_operand(const u32x4& v) {
-  return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+  const i32x4 x = __builtin_bit_cast(i32x4, v);
+  return __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
 // A workgroup's tile: WN x WM waves of (16 FN) x (16 FM), and NST LDS stages.
 // A stage holds one K block, 128 bytes of each of BN rows of W and BM rows of
 // X (256 elements in 4 bits, 64 in bf16), and in 4 bits their scales: 8 bytes
-// a row, [4][rows][2], in copies of 1 KB.
+// a row, [4][rows][2].  Copies bring 1 KB.
 template <int WN_, int WM_, int FN_, int FM_, int NST_, bool FP4_>
 struct Fp4Tile {
   static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, NST = NST_;
@@ -206,16 +210,24 @@ struct Fp4Tile {
   static constexpr int BN = WN * FN * 16, BM = WM * FM * 16;
   static constexpr int CX = FP4 ? (BM + 127) / 128 : 0, CW = FP4 ? (BN + 127) / 128 : 0;   // scale copies
   static constexpr int SX = (BN + BM) * 128, SW = SX + CX * 1024, STAGE = SW + CW * 1024;
-  static constexpr int LOADS = (BN + BM) / 8 / NW;   // 1 KB copies of rows per wave and step
+  static constexpr int LOADS = (BN + BM) / 8 / NW;   // copies of rows per wave and step
   static constexpr int COPIES = LOADS + (FP4 ? 1 : 0);
   static_assert(LOADS <= 8 && LOADS * NW * 8 == BN + BM && CX + CW <= NW, "copies");
-  static_assert(BN <= 256 && BM <= 256 && NST >= 2 && NST * STAGE <= 160 * 1024, "LDS");
-  static_assert((NST - 1) * COPIES < 64, "vector-memory counter");
-  static constexpr bool SPREAD = 2 * NST * STAGE > 160 * 1024;   // one workgroup on a CU
+  static_assert(BN <= 256 && BM <= 256 && NST >= 2 && NST <= 4 && NST * STAGE <= 160 * 1024, "LDS");
+  static_assert(NST * COPIES < 64, "vector-memory counter");
   // words with the scale pairs of a lane's rows: two rows a word, or with odd F one
   static constexpr int XW = FM % 2 ? FM : FM / 2, WW = FN / 2;
-  static_assert(FN % 2 == 0, "pairs of scales");
+  static_assert(FN == 2 || FN == 4 || FN == 8, "pairs of scales, steps");
 };
+
+// The 16-byte slot of a fragment row's chunk c in LDS.  A 16-byte read serves
+// 16 lanes in two cycles, eight rows of one lane quarter (0-3 and 12-15, or
+// 4-11) and the other eight of the next quarter, and there are 16 slots in the
+// 64 banks: these slots differ for all 16.  (With
+// row / 2 alone every read took twice its cycles.)
+__device__ __forceinline__ int fp4_slot(int row, int c) {
+  return c ^ (((row ^ row >> 1) >> 2 & 1) << 2 | (row >> 1 & 1) << 1 | row >> 3);
+}
 
 // A wave's part of a tile's main loop.
 struct Fp4Wave {
@@ -224,28 +236,21 @@ struct Fp4Wave {
   uint32_t soff, sstep;        // its scale copy, and the step to the next K block
   uint32_t sdst;               // where in a stage its scales go
   uint32_t lds;                // LDS address of the stages
-  int wave, lane, woff, xoff, s0;   // fragment addresses in a stage: row, first chunk
+  int wave, woff, xoff, s0;    // fragment addresses in a stage: row, first chunk
   int sxoff, swoff;            // scale addresses in a stage
-  int tail;                    // the K block in which W's rows end early, or -1
-  uint32_t left;               // their bytes in it
 };
 
 // Copies of K block kb into the stage at LDS offset st: this wave's 1 KB
-// pieces (piece p is rows 8 p .. 8 p + 7 of the W tile, then of the X tile)
-// and one of the scales' (several waves write the same bytes, so that every
-// wave has as many copies in flight).  Where W's rows end inside the block, a
-// lane past the end brings bytes of its own row's, which meet zeros of X.
+// pieces (rows of the W tile, then of the X tile) and one of the scales'
+// (several waves may write the same bytes, so that every wave has as many
+// copies in flight).  Where W's rows end inside the last block, the copies go on
+// into the next row, which meets zeros of X; behind the tile's last row the
+// buffer ends, and its bounds check gives zeros.
 template <class T>
 __device__ __forceinline__ void fp4_copy_piece(const Fp4Wave& g, uint32_t st, int kb, int i) {
   if (i < T::LOADS) {
     const int p = g.wave * T::LOADS + i;   // uniform
-    const bool isw = p < T::BN / 8;
-    uint32_t off = g.off[i];
-    if (T::FP4 && isw && kb == g.tail) {   // uniform
-      const uint32_t chunk = ((g.lane & 7) ^ (((8 * (p & 1) + (g.lane >> 3)) >> 1) & 7)) << 4;
-      off -= chunk < g.left ? 0 : chunk;
-    }
-    lds_copy<16>(isw ? g.rw : g.rx, g.lds + st + p * 1024, off, kb * 128);
+    lds_copy<16>(p < T::BN / 8 ? g.rw : g.rx, g.lds + st + p * 1024, g.off[i], kb * 128);
   } else {
     lds_copy<16>(g.rs, g.lds + st + g.sdst, g.soff, kb * g.sstep);
   }
@@ -268,81 +273,88 @@ __device__ __forceinline__ Fp4Scales<T> fp4_scales(const Fp4Wave& g, const uint8
   return s;
 }
 
-// The K loop: wait for the block's copies, meet the others (which ends their
-// reads of the previous block's stage), start the copies of block kb + NST -
-// 1 there, multiply: two instructions for each pair of fragments.
+// The K loop, in steps of one fragment row of W by the wave's FM fragments of X
+// (FM instructions): 2 FN steps a block, of which step s reads the fragment of
+// step s + 3.  So a block's first reads come three steps before the last one
+// ends, and the matrix cores have those steps' work while they wait: there,
+// with all reads of the block behind it, a wave waits for its copies of the
+// next block, meets the others, and starts the copies of block kb + NST into
+// the stage that is free now.
 template <class T>
 __device__ __forceinline__ void fp4_loop(const Fp4Wave& g, int kblocks, const uint8_t* lds,
                                          f32x4 (&acc)[T::FN][T::FM]) {
-  constexpr int FN = T::FN, FM = T::FM, LAST = T::NST * T::STAGE;
+  constexpr int FN = T::FN, FM = T::FM, LAST = T::NST * T::STAGE, S = 2 * FN, AHEAD = FN > 2 ? 3 : 2;
+  constexpr int PER = (T::COPIES + AHEAD - 1) / AHEAD;
 #pragma unroll
-  for (int k = 0; k < T::NST - 1; ++k)
+  for (int k = 0; k < T::NST; ++k)
     if (k < kblocks) {
 #pragma unroll
       for (int i = 0; i < T::COPIES; ++i) fp4_copy_piece<T>(g, k * T::STAGE, k, i);
     }
+  fp8_wait<T>(min(T::NST, kblocks) - 1);
+  barrier_only();
+  u32x4 a[4], b[2][FM];   // fragments of W by step % 4, of X by half of the block
+  auto read_a = [&](const uint8_t* st, int step) {
+    a[step & 3] = *reinterpret_cast<const u32x4*>(st + g.woff + step % FN * 2048 + (step < FN ? g.s0 : g.s0 ^ 16));
+  };
+  auto read_b = [&](const uint8_t* st, int half) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+      b[half][j] = *reinterpret_cast<const u32x4*>(st + g.xoff + j * 2048 + (half ? g.s0 ^ 16 : g.s0));
+  };
+  Fp4Scales<T> c, next{};
+  if (T::FP4) c = fp4_scales<T>(g, lds);
+  read_b(lds, 0);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) read_a(lds, i);
   int st = 0;
-  for (int kb = 0; kb < kblocks; ++kb) {
-    fp8_wait<T>(min(T::NST - 1, kblocks - kb) - 1);
-    barrier_only();
-    const uint32_t prev = st == 0 ? LAST - T::STAGE : st - T::STAGE;
-    const bool more = kb + T::NST - 1 < kblocks;
-    // with one workgroup on a CU the copies are spread over the rows of
-    // products, with two they go first
-    constexpr int PER = T::SPREAD ? (T::COPIES + FN - 1) / FN : T::COPIES;
-    auto copies = [&](int i) {
-      if (more) {
-#pragma unroll
-        for (int c = i * PER; c < (i + 1) * PER && c < T::COPIES; ++c)
-          fp4_copy_piece<T>(g, prev, kb + T::NST - 1, c);
-      }
-    };
+  // One basic block: with branches in it the compiler gathers the products at
+  // its end.  The last blocks read a stage ahead that holds nothing new.
+  auto block = [&](auto copy, int kb) {
+    constexpr bool COPY = decltype(copy)::value;
     const uint8_t* cur = lds + st;
-    if (!T::SPREAD) copies(0);
-    Fp4Scales<T> c;
-    if (T::FP4) c = fp4_scales<T>(g, cur);
-    u32x4 b[FM][2];
+    const int after = st + T::STAGE == LAST ? 0 : st + T::STAGE;
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      b[j][0] = *reinterpret_cast<const u32x4*>(cur + g.xoff + j * 2048 + g.s0);
-      b[j][1] = *reinterpret_cast<const u32x4*>(cur + g.xoff + j * 2048 + (g.s0 ^ 16));
-    }
-    u32x4 a[2][2];
-    auto frag = [&](int i) {
-      a[i & 1][0] = *reinterpret_cast<const u32x4*>(cur + g.woff + i * 2048 + g.s0);
-      a[i & 1][1] = *reinterpret_cast<const u32x4*>(cur + g.woff + i * 2048 + (g.s0 ^ 16));
-    };
-    frag(0);
-#pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      // one workgroup: the next row's fragment is read a row ahead
-      if (T::SPREAD && i + 1 < FN) frag(i + 1);
-      if (!T::SPREAD && i > 0) frag(i);
-      if (T::SPREAD) __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-          if constexpr (T::FP4)
-            acc[i][j] = fp4_mfma(fp4_operand(a[i & 1][t]), fp4_operand(b[j][t]), acc[i][j], 2 * (i & 1) + t,
-                                 (int)c.w[i >> 1], FM % 2 ? t : 2 * (j & 1) + t, (int)c.x[FM % 2 ? j : j >> 1]);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[i & 1][t]), as_bf16x8(b[j][t]),
-                                                                acc[i][j], 0, 0, 0);
+    for (int s = 0; s < S; ++s) {
+      if (s == (FN > AHEAD ? FN - AHEAD : 0)) read_b(cur, 1);
+      if (s + AHEAD < S) {
+        read_a(cur, s + AHEAD);
+      } else {
+        if (s + AHEAD == S) {
+          __builtin_amdgcn_s_waitcnt(waitcnt_imm(COPY ? (T::NST - 2) * T::COPIES : 0, 0));
+          barrier_only();
+          if (T::FP4) next = fp4_scales<T>(g, lds + after);
+          read_b(lds + after, 0);
         }
-      if (T::SPREAD) {
-        __builtin_amdgcn_sched_barrier(0);
-        copies(i);
+        read_a(lds + after, s + AHEAD - S);
+        if (COPY) {
+#pragma unroll
+          for (int i = (s + AHEAD - S) * PER; i < (s + AHEAD - S + 1) * PER && i < T::COPIES; ++i)
+            fp4_copy_piece<T>(g, st, kb + T::NST, i);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
+      const int i = s % FN, t = s / FN;
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        if constexpr (T::FP4)
+          acc[i][j] = fp4_mfma(fp4_operand(a[s & 3]), fp4_operand(b[t][j]), acc[i][j], 2 * (i & 1) + t,
+                               (int)c.w[i >> 1], FM % 2 ? t : 2 * (j & 1) + t, (int)c.x[FM % 2 ? j : j >> 1]);
+        else
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[s & 3]), as_bf16x8(b[t][j]), acc[i][j], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    st = st + T::STAGE == LAST ? 0 : st + T::STAGE;
-  }
+    c = next;
+    st = after;
+  };
+  int kb = 0;
+  for (; kb + T::NST < kblocks; ++kb) block(std::true_type{}, kb);
+  for (; kb < kblocks; ++kb) block(std::false_type{}, kb);
 }
 
 // One BN x BM tile per workgroup.  In LDS an operand's 16-row fragments follow
-// each other, a row is 128 bytes in 16-byte chunks, and chunk c of fragment row
-// r sits at slot c ^ (r / 2 % 8): the rows that a read touches in one cycle
-// spread over all banks.  W is the MFMA's A operand (D rows n), its rows
+// each other, their rows in 16-byte chunks (fp4_slot).  W is the MFMA's A operand (D rows n), its rows
 // interleaved over a wave's fragments so that the values of a lane are
 // consecutive n.
 template <class T, bool F32>
@@ -353,7 +365,6 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
   const int tid = threadIdx.x, lane = tid & 63;
   Fp4Wave v;
   v.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  v.lane = lane;
   // Tiles `first` .. `first + count - 1`: XCD x takes a contiguous range of
   // them (with splits, every tile's parts one after the other).
   int nt, mt, split, tile;
@@ -368,14 +379,11 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
   const int64_t n0 = (int64_t)nt * T::BN, m0 = (int64_t)mt * T::BM;
   const int all = (int)(xp / 128);   // X's rows are whole K blocks
   const int kb0 = (int)((int64_t)all * split / splits), kblocks = (int)((int64_t)all * (split + 1) / splits) - kb0;
-  // copies: lane l brings slot l % 8 of row l / 8 of a piece.  Rows past the
-  // matrix repeat its last row (their results are dropped).
+  // copies: lane l brings slot l % 8 of row l / 8 of a piece.  Rows past the matrix repeat its last row (their results are dropped).
   const int nrows = (int)min((int64_t)T::BN, g.N - n0), mrows = (int)min((int64_t)T::BM, g.M - m0);
   v.rw = buffer_of(g.w + n0 * g.wp, nrows * g.wp);
   v.rx = buffer_of(g.x + m0 * xp, mrows * xp);
   v.lds = (uint32_t)(uintptr_t)(lptr_t)lds;
-  v.tail = g.wp < xp ? all - 1 - kb0 : -1;   // past this part's blocks where it does not have the last one
-  v.left = (uint32_t)(g.wp - (int64_t)(all - 1) * 128);
 #pragma unroll
   for (int i = 0; i < T::LOADS; ++i) {
     const int p = v.wave * T::LOADS + i;
@@ -384,28 +392,29 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
     const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
     const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
     v.off[i] = (uint32_t)min(row, (isw ? nrows : mrows) - 1) * (uint32_t)(isw ? g.wp : xp) + (uint32_t)kb0 * 128 +
-               (((lane & 7) ^ ((fr >> 1) & 7)) << 4);
+               (fp4_slot(fr, lane & 7) << 4);
   }
   if (T::FP4) {
-    // scale copies: 16 bytes a lane, 8 rows' pairs of one q; rows past the
-    // scales repeat their last 16 bytes
+    // scale copies: 16 bytes a lane, 8 rows' pairs; rows past the scales
+    // repeat their last 16 bytes
     const int c = v.wave % (T::CX + T::CW);   // uniform
     const bool isw = c >= T::CX;
     const int rows = isw ? T::BN : T::BM;
     const int64_t srows = fp4_scale_rows(isw ? g.N : g.M), at = isw ? n0 : m0;
     const int chunk = min(64 * (isw ? c - T::CX : c) + lane, rows / 2 - 1);
-    const int q = chunk / (rows / 8), o = 16 * (chunk % (rows / 8));
-    const int left = (int)min((srows - at) * 2, (int64_t)2 * rows);   // bytes of a q, >= 32
-    v.soff = (uint32_t)(q * 2 * srows) + (uint32_t)min(o, left - 16);
+    const int p = chunk / (rows / 8), o = 16 * (chunk % (rows / 8));
+    const int left = (int)min((srows - at) * 2, (int64_t)2 * rows);   // bytes of a pair's rows, >= 32
+    v.soff = (uint32_t)(p * 2 * srows) + (uint32_t)min(o, left - 16);
     v.sstep = (uint32_t)(8 * srows);
     v.sdst = T::SX + c * 1024;
-    v.rs = buffer_of((isw ? g.sw : g.sx) + kb0 * 8 * srows + at * 2, (kblocks - 1) * 8 * srows + 6 * srows + left);
+    v.rs = buffer_of((isw ? g.sw : g.sx) + kb0 * 8 * srows + at * 2,
+                     (kblocks - 1) * 8 * srows + 6 * srows + left);
   }
   const int wn = v.wave / WM, wm = v.wave % WM;
   const int r = lane & 15, q = lane >> 4;
   v.woff = (wn * 16 * FN + r) * 128;
   v.xoff = (T::BN + wm * 16 * FM + r) * 128;
-  v.s0 = ((2 * q) ^ ((r >> 1) & 7)) << 4;
+  v.s0 = fp4_slot(r, 2 * q) << 4;
   v.sxoff = T::SX + q * 2 * T::BM + 2 * (wm * 16 * FM + r * FM);
   v.swoff = T::SW + q * 2 * T::BN + 2 * (wn * 16 * FN + fp8_pi(r) * FN);
   f32x4 acc[FN][FM];
