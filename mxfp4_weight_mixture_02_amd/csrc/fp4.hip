@@ -215,6 +215,8 @@ struct Fp4Tile {
   static_assert(LOADS <= 8 && LOADS * NW * 8 == BN + BM && CX + CW <= NW, "copies");
   static_assert(BN <= 256 && BM <= 256 && NST >= 2 && NST <= 4 && NST * STAGE <= 160 * 1024, "LDS");
   static_assert(NST * COPIES < 64, "vector-memory counter");
+  static constexpr bool SEVERAL = BN * BM >= 128 * 128;   // a workgroup may take several tiles
+  static constexpr int AHEAD = FN > 2 ? 3 : 2;       // steps that fragments are read ahead
   // words with the scale pairs of a lane's rows: two rows a word, or with odd F one
   static constexpr int XW = FM % 2 ? FM : FM / 2, WW = FN / 2;
   static_assert(FN == 2 || FN == 4 || FN == 8, "pairs of scales, steps");
@@ -273,186 +275,272 @@ __device__ __forceinline__ Fp4Scales<T> fp4_scales(const Fp4Wave& g, const uint8
   return s;
 }
 
-// The K loop, in steps of one fragment row of W by the wave's FM fragments of X
-// (FM instructions): 2 FN steps a block, of which step s reads the fragment of
-// step s + 3.  So a block's first reads come three steps before the last one
-// ends, and the matrix cores have those steps' work while they wait: there,
-// with all reads of the block behind it, a wave waits for its copies of the
-// next block, meets the others, and starts the copies of block kb + NST into
-// the stage that is free now.
+// A K block's products, in steps of one fragment row of W by the wave's FM
+// fragments of X (FM instructions): 2 FN steps, of which step s reads the
+// fragment of step s + 3.  So a block's first reads come three steps before the
+// last one ends, and the matrix cores have those steps' work while they wait:
+// there, with all reads of the block behind it, a wave waits for its copies of
+// the next block, meets the others, and starts the copies of the block NST
+// further on into the stage that is free now.  One basic block: with branches
+// in it the compiler gathers the products at its end.
 template <class T>
-__device__ __forceinline__ void fp4_loop(const Fp4Wave& g, int kblocks, const uint8_t* lds,
-                                         f32x4 (&acc)[T::FN][T::FM]) {
-  constexpr int FN = T::FN, FM = T::FM, LAST = T::NST * T::STAGE, S = 2 * FN, AHEAD = FN > 2 ? 3 : 2;
-  constexpr int PER = (T::COPIES + AHEAD - 1) / AHEAD;
+struct Fp4Frags {
+  u32x4 a[4], b[2][T::FM];   // fragments of W by step % 4, of X by half of the block
+  Fp4Scales<T> c;
+};
+template <class T>
+__device__ __forceinline__ void fp4_read_a(const Fp4Wave& g, const uint8_t* st, int step, Fp4Frags<T>& f) {
+  f.a[step & 3] = *reinterpret_cast<const u32x4*>(st + g.woff + step % T::FN * 2048 + (step < T::FN ? g.s0 : g.s0 ^ 16));
+}
+template <class T>
+__device__ __forceinline__ void fp4_read_b(const Fp4Wave& g, const uint8_t* st, int half, Fp4Frags<T>& f) {
 #pragma unroll
-  for (int k = 0; k < T::NST; ++k)
-    if (k < kblocks) {
+  for (int j = 0; j < T::FM; ++j)
+    f.b[half][j] = *reinterpret_cast<const u32x4*>(st + g.xoff + j * 2048 + (half ? g.s0 ^ 16 : g.s0));
+}
+// COPY: with copies of block kb of the tile that g has set out, else all that
+// are under way are waited for.  `there`: the next block's have been waited for
+// already.  Moves st on.
+template <class T, bool COPY>
+__device__ __forceinline__ void fp4_block(const Fp4Wave& g, int kb, int there, const uint8_t* lds, int& st,
+                                          Fp4Frags<T>& f, f32x4 (&acc)[T::FN][T::FM]) {
+  constexpr int FN = T::FN, FM = T::FM, S = 2 * FN, AHEAD = T::AHEAD, PER = (T::COPIES + AHEAD - 1) / AHEAD;
+  const int after = st + T::STAGE == T::NST * T::STAGE ? 0 : st + T::STAGE;
+  Fp4Scales<T> next{};
 #pragma unroll
-      for (int i = 0; i < T::COPIES; ++i) fp4_copy_piece<T>(g, k * T::STAGE, k, i);
-    }
-  fp8_wait<T>(min(T::NST, kblocks) - 1);
-  barrier_only();
-  u32x4 a[4], b[2][FM];   // fragments of W by step % 4, of X by half of the block
-  auto read_a = [&](const uint8_t* st, int step) {
-    a[step & 3] = *reinterpret_cast<const u32x4*>(st + g.woff + step % FN * 2048 + (step < FN ? g.s0 : g.s0 ^ 16));
-  };
-  auto read_b = [&](const uint8_t* st, int half) {
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-      b[half][j] = *reinterpret_cast<const u32x4*>(st + g.xoff + j * 2048 + (half ? g.s0 ^ 16 : g.s0));
-  };
-  Fp4Scales<T> c, next{};
-  if (T::FP4) c = fp4_scales<T>(g, lds);
-  read_b(lds, 0);
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) read_a(lds, i);
-  int st = 0;
-  // One basic block: with branches in it the compiler gathers the products at
-  // its end.  The last blocks read a stage ahead that holds nothing new.
-  auto block = [&](auto copy, int kb) {
-    constexpr bool COPY = decltype(copy)::value;
-    const uint8_t* cur = lds + st;
-    const int after = st + T::STAGE == LAST ? 0 : st + T::STAGE;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (s == (FN > AHEAD ? FN - AHEAD : 0)) read_b(cur, 1);
-      if (s + AHEAD < S) {
-        read_a(cur, s + AHEAD);
-      } else {
-        if (s + AHEAD == S) {
-          __builtin_amdgcn_s_waitcnt(waitcnt_imm(COPY ? (T::NST - 2) * T::COPIES : 0, 0));
-          barrier_only();
-          if (T::FP4) next = fp4_scales<T>(g, lds + after);
-          read_b(lds + after, 0);
-        }
-        read_a(lds + after, s + AHEAD - S);
-        if (COPY) {
-#pragma unroll
-          for (int i = (s + AHEAD - S) * PER; i < (s + AHEAD - S + 1) * PER && i < T::COPIES; ++i)
-            fp4_copy_piece<T>(g, st, kb + T::NST, i);
-        }
+  for (int s = 0; s < S; ++s) {
+    if (s == (FN > AHEAD ? FN - AHEAD : 0)) fp4_read_b<T>(g, lds + st, 1, f);
+    if (s + AHEAD < S) {
+      fp4_read_a<T>(g, lds + st, s + AHEAD, f);
+    } else {
+      if (s + AHEAD == S) {
+        // (a branch of its own inside the assembly leaves the block whole)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(%1)\n1:"
+                     ::"s"(there), "n"(COPY ? (T::NST - 2) * T::COPIES : 0) : "scc", "memory");
+        barrier_only();
+        if (T::FP4) next = fp4_scales<T>(g, lds + after);
+        fp4_read_b<T>(g, lds + after, 0, f);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      const int i = s % FN, t = s / FN;
+      fp4_read_a<T>(g, lds + after, s + AHEAD - S, f);
+      if (COPY) {
 #pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        if constexpr (T::FP4)
-          acc[i][j] = fp4_mfma(fp4_operand(a[s & 3]), fp4_operand(b[t][j]), acc[i][j], 2 * (i & 1) + t,
-                               (int)c.w[i >> 1], FM % 2 ? t : 2 * (j & 1) + t, (int)c.x[FM % 2 ? j : j >> 1]);
-        else
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[s & 3]), as_bf16x8(b[t][j]), acc[i][j], 0, 0, 0);
+        for (int i = (s + AHEAD - S) * PER; i < (s + AHEAD - S + 1) * PER && i < T::COPIES; ++i)
+          fp4_copy_piece<T>(g, st, kb, i);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-    c = next;
-    st = after;
-  };
-  int kb = 0;
-  for (; kb + T::NST < kblocks; ++kb) block(std::true_type{}, kb);
-  for (; kb < kblocks; ++kb) block(std::false_type{}, kb);
+    __builtin_amdgcn_sched_barrier(0);
+    const int i = s % FN, t = s / FN;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      if constexpr (T::FP4)
+        acc[i][j] = fp4_mfma(fp4_operand(f.a[s & 3]), fp4_operand(f.b[t][j]), acc[i][j], 2 * (i & 1) + t,
+                             (int)f.c.w[i >> 1], FM % 2 ? t : 2 * (j & 1) + t, (int)f.c.x[FM % 2 ? j : j >> 1]);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f.a[s & 3]), as_bf16x8(f.b[t][j]), acc[i][j], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  f.c = next;
+  st = after;
 }
 
-// One BN x BM tile per workgroup.  In LDS an operand's 16-row fragments follow
-// each other, their rows in 16-byte chunks (fp4_slot).  W is the MFMA's A operand (D rows n), its rows
-// interleaved over a wave's fragments so that the values of a lane are
-// consecutive n.
-template <class T, bool F32>
+// F values of the bias from n on, zeros past N and without one.
+template <int F>
+__device__ __forceinline__ void fp4_bias(const uint16_t* bias, int64_t n, int64_t N, bool wide, float (&v)[F]) {
+  if (!bias) N = 0;
+  if (wide && (reinterpret_cast<uintptr_t>(bias) & (2 * F - 1)) == 0) {   // uniform
+    uint32_t w[F / 2];
+#pragma unroll
+    for (int i = 0; i < F / 2; ++i) w[i] = n < N ? reinterpret_cast<const uint32_t*>(bias + n)[i] : 0u;
+#pragma unroll
+    for (int i = 0; i < F; ++i) v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < F; ++i) v[i] = n + i < N ? bf16_to_f32(bias[n + i]) : 0.0f;
+  }
+}
+struct Fp4Out {
+  int64_t M, N;
+  const uint16_t* bias;
+  void* out;
+};
+
+// A tile's place: its rows, and its part of K.
+struct Fp4Place {
+  int64_t n0, m0;
+  int nrows, mrows, split, tile, kb0, kblocks;
+};
+
+// BN x BM tiles, one or several after the other for a workgroup: the last
+// blocks of a tile bring the first ones of the next, so that only its stores
+// stand between two tiles' products.  In LDS an operand's 16-row fragments
+// follow each other, their rows in 16-byte chunks (fp4_slot).  W is the MFMA's A
+// operand (D rows n), its rows interleaved over a wave's fragments so that the
+// values of a lane are consecutive n.
+template <class T, bool F32, bool PARTS>
 __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t xp, int ntiles, int mtiles, int first,
                                                               int count, int splits) {
-  constexpr int FN = T::FN, FM = T::FM, WM = T::WM;
-  __shared__ __align__(1024) uint8_t lds[T::NST * T::STAGE];
+  constexpr int FN = T::FN, FM = T::FM, WM = T::WM, NST = T::NST;
+  constexpr bool SEVERAL = T::SEVERAL && !PARTS;
+  __shared__ __align__(1024) uint8_t lds[NST * T::STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
+  const int r = lane & 15, q = lane >> 4;
   Fp4Wave v;
   v.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Tiles `first` .. `first + count - 1`: XCD x takes a contiguous range of
-  // them (with splits, every tile's parts one after the other).
-  int nt, mt, split, tile;
-  {
-    const int L = count * splits, b = blockIdx.x;
-    const int x = b & 7, base = L >> 3, extra = L & 7;
-    const int item = x * base + min(x, extra) + (b >> 3);
-    split = item % splits;
-    tile = item / splits;
-    fp8_tile_at(first + tile, ntiles, mtiles, nt, mt);
-  }
-  const int64_t n0 = (int64_t)nt * T::BN, m0 = (int64_t)mt * T::BM;
-  const int all = (int)(xp / 128);   // X's rows are whole K blocks
-  const int kb0 = (int)((int64_t)all * split / splits), kblocks = (int)((int64_t)all * (split + 1) / splits) - kb0;
-  // copies: lane l brings slot l % 8 of row l / 8 of a piece.  Rows past the matrix repeat its last row (their results are dropped).
-  const int nrows = (int)min((int64_t)T::BN, g.N - n0), mrows = (int)min((int64_t)T::BM, g.M - m0);
-  v.rw = buffer_of(g.w + n0 * g.wp, nrows * g.wp);
-  v.rx = buffer_of(g.x + m0 * xp, mrows * xp);
   v.lds = (uint32_t)(uintptr_t)(lptr_t)lds;
-#pragma unroll
-  for (int i = 0; i < T::LOADS; ++i) {
-    const int p = v.wave * T::LOADS + i;
-    const bool isw = p < T::BN / 8;
-    const int at = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);   // LDS row of the operand
-    const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
-    const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
-    v.off[i] = (uint32_t)min(row, (isw ? nrows : mrows) - 1) * (uint32_t)(isw ? g.wp : xp) + (uint32_t)kb0 * 128 +
-               (fp4_slot(fr, lane & 7) << 4);
-  }
-  if (T::FP4) {
-    // scale copies: 16 bytes a lane, 8 rows' pairs; rows past the scales
-    // repeat their last 16 bytes
-    const int c = v.wave % (T::CX + T::CW);   // uniform
-    const bool isw = c >= T::CX;
-    const int rows = isw ? T::BN : T::BM;
-    const int64_t srows = fp4_scale_rows(isw ? g.N : g.M), at = isw ? n0 : m0;
-    const int chunk = min(64 * (isw ? c - T::CX : c) + lane, rows / 2 - 1);
-    const int p = chunk / (rows / 8), o = 16 * (chunk % (rows / 8));
-    const int left = (int)min((srows - at) * 2, (int64_t)2 * rows);   // bytes of a pair's rows, >= 32
-    v.soff = (uint32_t)(p * 2 * srows) + (uint32_t)min(o, left - 16);
-    v.sstep = (uint32_t)(8 * srows);
-    v.sdst = T::SX + c * 1024;
-    v.rs = buffer_of((isw ? g.sw : g.sx) + kb0 * 8 * srows + at * 2,
-                     (kblocks - 1) * 8 * srows + 6 * srows + left);
-  }
   const int wn = v.wave / WM, wm = v.wave % WM;
-  const int r = lane & 15, q = lane >> 4;
   v.woff = (wn * 16 * FN + r) * 128;
   v.xoff = (T::BN + wm * 16 * FM + r) * 128;
   v.s0 = fp4_slot(r, 2 * q) << 4;
   v.sxoff = T::SX + q * 2 * T::BM + 2 * (wm * 16 * FM + r * FM);
   v.swoff = T::SW + q * 2 * T::BN + 2 * (wn * 16 * FN + fp8_pi(r) * FN);
+  const int all = (int)(xp / 128);   // X's rows are whole K blocks
+  // Sets out the copies of item `item` (with splits, every tile's parts one
+  // after the other).
+  auto place = [&](int item) {
+    Fp4Place w;
+    w.split = PARTS ? item % splits : 0;
+    w.tile = PARTS ? item / splits : item;
+    int nt, mt;
+    fp8_tile_at(first + w.tile, ntiles, mtiles, nt, mt);
+    w.n0 = (int64_t)nt * T::BN;
+    w.m0 = (int64_t)mt * T::BM;
+    w.kb0 = PARTS ? (int)((int64_t)all * w.split / splits) : 0;
+    w.kblocks = PARTS ? (int)((int64_t)all * (w.split + 1) / splits) - w.kb0 : all;
+    // copies: lane l brings slot l % 8 of row l / 8 of a piece.  Rows past the
+    // matrix repeat its last row (their results are dropped).
+    w.nrows = (int)min((int64_t)T::BN, g.N - w.n0);
+    w.mrows = (int)min((int64_t)T::BM, g.M - w.m0);
+    v.rw = buffer_of(g.w + w.n0 * g.wp, w.nrows * g.wp);
+    v.rx = buffer_of(g.x + w.m0 * xp, w.mrows * xp);
+#pragma unroll
+    for (int i = 0; i < T::LOADS; ++i) {
+      const int p = v.wave * T::LOADS + i;
+      const bool isw = p < T::BN / 8;
+      const int at = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);   // LDS row of the operand
+      const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
+      const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
+      v.off[i] = (uint32_t)min(row, (isw ? w.nrows : w.mrows) - 1) * (uint32_t)(isw ? g.wp : xp) +
+                 (uint32_t)w.kb0 * 128 + (fp4_slot(fr, lane & 7) << 4);
+    }
+    if (T::FP4) {
+      // scale copies: 16 bytes a lane, 8 rows' pairs; rows past the scales
+      // repeat their last 16 bytes
+      const int c = v.wave % (T::CX + T::CW);   // uniform
+      const bool isw = c >= T::CX;
+      const int rows = isw ? T::BN : T::BM;
+      const int64_t srows = fp4_scale_rows(isw ? g.N : g.M), at = isw ? w.n0 : w.m0;
+      const int chunk = min(64 * (isw ? c - T::CX : c) + lane, rows / 2 - 1);
+      const int p = chunk / (rows / 8), o = 16 * (chunk % (rows / 8));
+      const int left = (int)min((srows - at) * 2, (int64_t)2 * rows);   // bytes of a pair's rows, >= 32
+      v.soff = (uint32_t)(p * 2 * srows) + (uint32_t)min(o, left - 16);
+      v.sstep = (uint32_t)(8 * srows);
+      v.sdst = T::SX + c * 1024;
+      v.rs = buffer_of((isw ? g.sw : g.sx) + w.kb0 * 8 * srows + at * 2,
+                       (w.kblocks - 1) * 8 * srows + 6 * srows + left);
+    }
+    return w;
+  };
+  // XCD x takes a contiguous range of the items, its workgroups one after the
+  // other of it
+  int item, end, step;
+  {
+    const int L = count * splits, b = blockIdx.x, x = b & 7;
+    const int base = L >> 3, extra = L & 7;
+    item = x * base + min(x, extra) + (b >> 3);
+    end = (x + 1) * base + min(x + 1, extra);
+    step = ((int)gridDim.x - x + 7) >> 3;
+  }
+  Fp4Place w = place(item), ahead = w;   // what is multiplied, what is copied
+  int left = w.kblocks, next = NST;        // blocks of w to come; the next block to copy
+#pragma unroll
+  for (int k = 0; k < NST; ++k)
+    if (SEVERAL || k < left) {
+#pragma unroll
+      for (int i = 0; i < T::COPIES; ++i) fp4_copy_piece<T>(v, k * T::STAGE, min(k, left - 1), i);
+    }
+  fp8_wait<T>((SEVERAL ? NST : min(NST, left)) - 1);
+  barrier_only();
+  Fp4Frags<T> f;
+  if (T::FP4) f.c = fp4_scales<T>(v, lds);
+  fp4_read_b<T>(v, lds, 0, f);
+#pragma unroll
+  for (int i = 0; i < T::AHEAD; ++i) fp4_read_a<T>(v, lds, i, f);
+  int st = 0, there = 0;
   f32x4 acc[FN][FM];
+  auto zero = [&]() {
 #pragma unroll
-  for (int i = 0; i < FN; ++i)
+    for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  fp4_loop<T>(v, kblocks, lds, acc);
-  const int64_t nw0 = n0 + wn * 16 * FN;
-  const bool wide = g.N % FN == 0;
-  if (splits > 1) {   // the tile's part, the rows that exist, as [BM][BN] fp32
-    float* part = g.part + ((int64_t)split * count + tile) * (T::BN * T::BM);
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      if (wm * 16 * FM + r * FM + j >= mrows) break;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        float* d = part + (wm * 16 * FM + r * FM + j) * T::BN + wn * 16 * FN + (4 * t + q) * FN;
-#pragma unroll
-        for (int i = 0; i < FN; i += FN < 4 ? FN : 4) {
-          if constexpr (FN < 4)
-            *reinterpret_cast<f32x2*>(d) = f32x2{acc[0][j][t], acc[1][j][t]};
-          else
-            *reinterpret_cast<f32x4*>(d + i) = f32x4{acc[i][j][t], acc[i + 1][j][t], acc[i + 2][j][t], acc[i + 3][j][t]};
-        }
+      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  zero();
+  if constexpr (!SEVERAL) {
+    // the last blocks read a stage ahead that holds nothing new
+    for (; left > NST; --left) fp4_block<T, true>(v, next++, 0, lds, st, f, acc);
+    for (; left > 1; --left) fp4_block<T, false>(v, 0, 0, lds, st, f, acc);
+  }
+  for (;;) {
+    if (SEVERAL && next >= ahead.kblocks) {   // the copies go on with the next tile
+      item += step;
+      next = 0;
+      if (item < end) {
+        ahead = place(item);
+      } else {   // or with nothing: all of an empty buffer is past its end, and no memory is read
+        ahead.kblocks = 1 << 30;
+        v.rw[2] = v.rx[2] = v.rs[2] = 0;
       }
     }
-    return;
-  }
+    fp4_block<T, SEVERAL>(v, next++, there, lds, st, f, acc);
+    there = 0;
+    if (--left) continue;
+    const Fp4Place done = w;
+    const bool more = SEVERAL && item < end;   // whole tiles: the host gives several only K of more blocks than stages
+    const int64_t nw0 = done.n0 + wn * 16 * FN;
+    if constexpr (PARTS) {   // the tile's part, the rows that exist, as [BM][BN] fp32
+      float* part = g.part + ((int64_t)done.split * count + done.tile) * (T::BN * T::BM);
 #pragma unroll
-  for (int j = 0; j < FM; ++j)
+      for (int j = 0; j < FM; ++j) {
+        if (wm * 16 * FM + r * FM + j >= done.mrows) break;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float* d = part + (wm * 16 * FM + r * FM + j) * T::BN + wn * 16 * FN + (4 * t + q) * FN;
+#pragma unroll
+          for (int i = 0; i < FN; i += FN < 4 ? FN : 4) {
+            if constexpr (FN < 4)
+              *reinterpret_cast<f32x2*>(d) = f32x2{acc[0][j][t], acc[1][j][t]};
+            else
+              *reinterpret_cast<f32x4*>(d + i) = f32x4{acc[i][j][t], acc[i + 1][j][t], acc[i + 2][j][t], acc[i + 3][j][t]};
+          }
+        }
+      }
+      break;
+    }
+    // The copies of the next tile's second block come before the stores: a
+    // wait for them later would be one for the stores.
+    if (more) __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+    const bool wide = g.N % FN == 0;
+    const Fp4Out to{g.M, g.N, nullptr, g.out};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      float o[FN];
+      const int64_t n = nw0 + (4 * t + q) * FN;
+      float bias[FN];   // once for the lane's FM columns
+      fp4_bias<FN>(g.bias, n, g.N, wide, bias);
 #pragma unroll
-      for (int i = 0; i < FN; ++i) o[i] = acc[i][j][t];
-      fp8_store<FN, F32>(g, m0 + wm * 16 * FM + r * FM + j, nw0 + (4 * t + q) * FN, o, wide);
+      for (int j = 0; j < FM; ++j) {
+        float o[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) o[i] = acc[i][j][t] + bias[i];
+        fp8_store<FN, F32>(to, done.m0 + wm * 16 * FM + r * FM + j, n, o, wide);
+      }
     }
+    if (!more) break;
+    zero();
+    w = ahead;
+    left = w.kblocks;
+    there = 1;
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));   // no copy outlives the workgroup
 }
 
 // Few rows: a workgroup takes 16 rows of W and its waves split K in units of
@@ -692,11 +780,17 @@ size_t bf16_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
 template <class T>
 static hipError_t gemm_tiles(const Fp4Gemm& g, int64_t xp, int first, int count, int splits, hipStream_t s) {
   const int nt = (int)((g.N + T::BN - 1) / T::BN), mt = (int)((g.M + T::BM - 1) / T::BM);
-  const dim3 grid((unsigned)((int64_t)count * splits)), block(64 * T::NW);
-  if (g.out_f32)
-    hipLaunchKernelGGL((fp4_gemm_kernel<T, true>), grid, block, 0, s, g, xp, nt, mt, first, count, splits);
+  // As many workgroups as the CUs hold take several tiles each, where a tile has
+  // blocks of its own beside those that its neighbours' copies touch.
+  const int64_t items = (int64_t)count * splits, held = 256 * (160 * 1024 / (T::NST * T::STAGE));
+  const bool several = T::SEVERAL && splits == 1 && items > held && xp / 128 > T::NST;
+  const dim3 grid((unsigned)(several ? held : items)), block(64 * T::NW);
+  if (splits > 1)
+    hipLaunchKernelGGL((fp4_gemm_kernel<T, true, true>), grid, block, 0, s, g, xp, nt, mt, first, count, splits);
+  else if (g.out_f32)
+    hipLaunchKernelGGL((fp4_gemm_kernel<T, true, false>), grid, block, 0, s, g, xp, nt, mt, first, count, splits);
   else
-    hipLaunchKernelGGL((fp4_gemm_kernel<T, false>), grid, block, 0, s, g, xp, nt, mt, first, count, splits);
+    hipLaunchKernelGGL((fp4_gemm_kernel<T, false, false>), grid, block, 0, s, g, xp, nt, mt, first, count, splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   Fp8Gemm j{};
@@ -723,7 +817,7 @@ static hipError_t gemm_of(const Fp4Gemm& g, int64_t xp, const GemmPlan& p, hipSt
   switch (p.tile) {
     case 0: return gemm<Fp4Tile<2, 4, 8, 4, 2, FP4>>(g, xp, p, s);
     case 1: return gemm<Fp4Tile<2, 4, 8, 3, 2, FP4>>(g, xp, p, s);
-    case 2: return gemm<Fp4Tile<2, 4, 4, 3, 3, FP4>>(g, xp, p, s);
+    case 2: return gemm<Fp4Tile<2, 4, 4, 3, FP4 ? 3 : 4, FP4>>(g, xp, p, s);
     case 3: return gemm<Fp4Tile<2, 2, 4, 4, 2, FP4>>(g, xp, p, s);
     case 4: return gemm<Fp4Tile<2, 2, 4, 4, 3, FP4>>(g, xp, p, s);
     case 5: return gemm<Fp4Tile<1, 4, 4, 2, 3, FP4>>(g, xp, p, s);
