@@ -15,7 +15,6 @@
 // feeds row r's elements 64 q .. 64 q + 63 of a block of 256, in two
 // instructions, so [K block][q][row][2] puts the two scales of all rows of a
 // lane side by side.
-#include <type_traits>
 
 #include "common.hpp"
 #include "fp4.hpp"
@@ -606,7 +605,7 @@ __global__ __launch_bounds__(64 * FK_NW) void fp4_skinny_kernel(Fp4Gemm g) {
 // bf16 X of up to 16 rows, rounded here: every workgroup rounds all of X into
 // LDS (4 lanes a block) while its first W loads are under way.  LDS unit u of
 // row m is 64 bytes at (u M + m) * 64, its four scales at (u M + m) * 4.
-constexpr int FUSED4_BYTES = 24576, FUSED4_ROUNDS = FUSED4_BYTES / 4 / (64 * FK_NW);
+constexpr int FUSED4_BYTES = 20480, FUSED4_ROUNDS = FUSED4_BYTES / 4 / (64 * FK_NW);
 
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(64 * FK_NW) void fp4_fused_kernel(Fp4Gemm g, const uint16_t* __restrict__ xb) {
@@ -749,25 +748,51 @@ hipError_t launch_bf16_pad(const uint16_t* x, int64_t rows, int64_t K, uint16_t*
   return hipGetLastError();
 }
 
+// The tiles' times (GemmShape), for bf16 and for fp32 results, fitted to launches
+// of 32 to 16384 rows by 5760 x 2880, 2880 x 5760, 8192 x 1024, 1024 x 8192, 4096
+// x 4096, 512 x 512 and 700 x 512 whose W comes from HBM.  The choice is 1% slower
+// on average than the best tile, at most 12%.  In 4 bits (us; 5760 x 2880):
+//   rows       64    256    512   1024   2047   4096  16384
+//   256 x 256  23.6  25.8  26.2   27.0   28.0   52.0    189
+//   256 x 192  21.6  23.0  23.4   24.2   26.7   49.0    183
+//   128 x 192  15.6  17.4  17.9   30.8   32.7   60.5    226
+//   128 x 128  13.6  14.7  15.2   20.0   31.6   53.6    242   two stages, two workgroups on a CU
+//   128 x 128  11.6  12.8  13.2   22.8   33.2   61.1    266   three stages, one
+//   64 x 128    8.4   9.2  13.4   20.0   34.8   64.4    268
+//   64 x 64     7.0   9.8  14.4   24.6   44.1   79.6    331
+//   32 x 64     6.3  10.2  16.8   30.5   56.2    107    450
+//   32 x 32     6.4  13.3  20.9   37.0   68.0    130    522
 static constexpr GemmShape FP4_SHAPE[] = {
-    {256, 256, 1, {1.40f, 1.40f}, {1.40f, 1.40f}, {7.5f, 10.3f}},
-    {256, 192, 1, {1.33f, 1.33f}, {1.33f, 1.33f}, {7.2f, 9.3f}},
-    {128, 192, 1, {0.73f, 0.73f}, {0.73f, 0.73f}, {7.0f, 7.4f}},
-    {128, 128, 2, {0.90f, 0.90f}, {0.59f, 0.59f}, {4.9f, 5.8f}},
-    {128, 128, 1, {0.60f, 0.60f}, {0.60f, 0.60f}, {5.7f, 5.8f}},
-    {64, 128, 2, {0.46f, 0.46f}, {0.38f, 0.38f}, {4.4f, 4.6f}},
-    {64, 64, 2, {0.37f, 0.37f}, {0.27f, 0.27f}, {3.9f, 4.0f}},
-    {32, 64, 3, {0.28f, 0.28f}, {0.22f, 0.22f}, {3.7f, 3.8f}},
-    {32, 32, 4, {0.24f, 0.24f}, {0.13f, 0.13f}, {3.5f, 3.5f}},
+    {256, 256, 1, {1.23f, 1.05f}, {1.47f, 1.38f}, {10.8f, 17.5f}},
+    {256, 192, 1, {1.26f, 1.10f}, {1.26f, 1.12f}, {7.5f, 13.0f}},
+    {128, 192, 1, {0.85f, 0.82f}, {0.75f, 0.79f}, {6.2f, 7.0f}},
+    {128, 128, 2, {0.62f, 0.58f}, {0.51f, 0.63f}, {6.6f, 7.3f}},
+    {128, 128, 1, {0.54f, 0.50f}, {0.46f, 0.55f}, {5.4f, 6.4f}},
+    {64, 128, 2, {0.33f, 0.33f}, {0.29f, 0.36f}, {4.7f, 4.9f}},
+    {64, 64, 2, {0.28f, 0.27f}, {0.20f, 0.23f}, {3.2f, 3.3f}},
+    {32, 64, 3, {0.25f, 0.26f}, {0.14f, 0.16f}, {2.9f, 2.8f}},
+    {32, 32, 3, {0.28f, 0.25f}, {0.08f, 0.09f}, {2.1f, 2.1f}},
 };
-constexpr int FP4_SHAPES = (int)(sizeof(FP4_SHAPE) / sizeof(FP4_SHAPE[0]));
+// The same in bf16, the input's gradient's product.
+static constexpr GemmShape BF16_SHAPE[] = {
+    {256, 256, 1, {1.14f, 1.14f}, {1.21f, 1.21f}, {13.1f, 16.0f}},
+    {256, 192, 1, {0.92f, 0.92f}, {0.94f, 0.94f}, {12.3f, 15.0f}},
+    {128, 192, 1, {0.55f, 0.55f}, {0.55f, 0.55f}, {10.3f, 11.0f}},
+    {128, 128, 2, {0.52f, 0.52f}, {0.36f, 0.36f}, {12.0f, 13.0f}},
+    {128, 128, 1, {0.41f, 0.41f}, {0.37f, 0.37f}, {9.3f, 10.0f}},
+    {64, 128, 2, {0.24f, 0.24f}, {0.23f, 0.23f}, {9.3f, 9.5f}},
+    {64, 64, 2, {0.18f, 0.18f}, {0.14f, 0.14f}, {6.7f, 6.8f}},
+    {32, 64, 3, {0.15f, 0.15f}, {0.11f, 0.11f}, {4.8f, 4.9f}},
+    {32, 32, 4, {0.16f, 0.16f}, {0.07f, 0.07f}, {2.9f, 2.9f}},
+};
+constexpr int GEMM_SHAPES = (int)(sizeof(FP4_SHAPE) / sizeof(FP4_SHAPE[0]));
 
 static GemmPlan fp4_plan(int64_t M, int64_t N, int64_t K, bool f32) {
   if (M <= 16 && N >= 1024) return {-1, 0, 0, 1, 0, 0};
-  return gemm_plan(FP4_SHAPE, FP4_SHAPES, M, N, fp4_kblocks(K), f32);
+  return gemm_plan(FP4_SHAPE, GEMM_SHAPES, M, N, fp4_kblocks(K), f32);
 }
 static GemmPlan bf16_plan(int64_t M, int64_t N, int64_t K, bool f32) {
-  return gemm_plan(FP4_SHAPE, FP4_SHAPES, M, N, K / 64, f32);
+  return gemm_plan(BF16_SHAPE, GEMM_SHAPES, M, N, K / 64, f32);
 }
 size_t fp4_part_bytes(int64_t M, int64_t N, int64_t K, int out_f32) {
   return gemm_part_bytes(fp4_plan(M, N, K, out_f32 != 0));
@@ -845,8 +870,12 @@ hipError_t launch_bf16_gemm(const Fp4Gemm& g, hipStream_t s) {
   return gemm_of<false>(b, 2 * g.K, bf16_plan(g.M, g.N, g.K, g.out_f32 != 0), s);
 }
 
+// The one-launch form: X's codes fit its LDS, and rounding them in every
+// workgroup costs less than a launch of its own (from HBM, us: 5760 x 2880, 4
+// rows 6.1 against 7.3, 8 rows 7.9, 7.4; 2880 x 5760, 4 rows 7.0, 7.5; with few
+// columns, 512 x 2880, 16 rows 7.8, 7.3).
 bool fp4_fused_fits(int64_t M, int64_t N, int64_t K) {
-  return M <= 16 && M * ((K + 127) / 128 * 64) <= FUSED4_BYTES;
+  return M <= 16 && M * ((K + 127) / 128 * 64) <= (N < 1024 ? FUSED4_BYTES : FUSED4_BYTES / 2);
 }
 
 hipError_t launch_fp4_fused(const Fp4Gemm& g, const uint16_t* x, hipStream_t s) {

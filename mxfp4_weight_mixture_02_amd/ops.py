@@ -790,7 +790,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     if not (bf16 or fp8):
         raise ValueError("one of bf16 and fp8 is needed")
     dev = _same_device(x=x, weight=weight, residual=residual)
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None
+    y = (torch.empty_like(x) if x.dtype == torch.bfloat16 else
+         torch.empty((T, H), dtype=torch.bfloat16, device=dev)) if bf16 else None
     q = Fp8Matrix.empty(T, H, 1, dev) if fp8 else None
     n = Normed(y, q, x if residual is None else torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=dev))
     _call("mxmoe_rms_norm", dev, _p(x), _p(residual), _DTYPES[x.dtype], _p(weight), _DTYPES[weight.dtype], T, H, eps,
