@@ -15,7 +15,6 @@
 // feeds row r's elements 64 q .. 64 q + 63 of a block of 256, in two
 // instructions, so [K block][q][row][2] puts the two scales of all rows of a
 // lane side by side.
-
 #include "common.hpp"
 #include "fp4.hpp"
 #include "ring.hpp"
@@ -94,7 +93,11 @@ __device__ __forceinline__ u32x4 bf16x8_at(const uint16_t* x, int64_t at, int64_
 }
 
 // One K block of 256 of 16 rows per workgroup: 32 lanes a row, 8 elements
-// each, two rounds of 8 rows; the scales leave by LDS in their order.
+// each, two rounds of 8 rows; the scales leave by LDS in their order.  bf16
+// pairs are rounded as they are stored: the maximum as 16-bit integers, the
+// conversion by the hardware's, whose ties go to even.  Bound by HBM: 16384 x
+// 2880 bf16 in 22 to 29 us (with X in the last-level cache, or not), 4.2 TB/s;
+// 2047 x 2880 in 4.8.
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(256) void fp4_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t K,
                                                        int64_t pitch, int64_t srows, int kblocks,
@@ -376,6 +379,20 @@ struct Fp4Place {
 // follow each other, their rows in 16-byte chunks (fp4_slot).  W is the MFMA's A
 // operand (D rows n), its rows interleaved over a wave's fragments so that the
 // values of a lane are consecutive n.
+//
+// Bound by power: the matrix instructions alone, on random codes, reach 6.7
+// PFLOP/s on the card (8.8 on zeros), and with the copies and the LDS reads
+// that feed them 4.6 (8192^3, 239 us).  16384 x 5760 x 2880: 167 us, 3.3
+// PFLOP/s, with K padded by 7%, six rounds of tiles that are 5.75, and 189 MB of
+// results; a tile after another on its own (188 us) took 142 without its
+// stores, 120 without its copies, 101 without the matrix instructions, 66
+// without any of the three: their times add up, a slower clock behind them.
+// 2047 x 5760 x 2880: 28 us, 2.4 PFLOP/s, one round.  The larger a wave's part of
+// a tile the fewer LDS reads for a product, so 256 x 256 wins where there are
+// rounds of it.  Tried without gain: stages of 64 bytes a row, four waves with
+// 128 x 128 each, 96-column waves, rows of X at an odd pitch, stores of whole
+// KB or past the caches, workgroups that start one after the other.  In bf16:
+// 2048 x 2880 x 5760, 62 us, 1.1 PFLOP/s (the library's 8192^3: 1.35).
 template <class T, bool F32, bool PARTS>
 __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t xp, int ntiles, int mtiles, int first,
                                                               int count, int splits) {
@@ -545,6 +562,8 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
 // Few rows: a workgroup takes 16 rows of W and its waves split K in units of
 // 128; every wave streams its part of W straight into fragments (lane (r, q):
 // block 4 u + q of row r), and the partial sums meet in LDS in wave order.
+// Bound by the latency of a launch with a trip to HBM in it: 16 x 5760 x 2880
+// in 6.8 us (one row 5.6, of them an empty launch 2).
 constexpr int FK_NW = 8, FK_CH = 3;   // waves; units in flight per wave
 
 struct SkinnyW4 {
@@ -604,7 +623,8 @@ __global__ __launch_bounds__(64 * FK_NW) void fp4_skinny_kernel(Fp4Gemm g) {
 
 // bf16 X of up to 16 rows, rounded here: every workgroup rounds all of X into
 // LDS (4 lanes a block) while its first W loads are under way.  LDS unit u of
-// row m is 64 bytes at (u M + m) * 64, its four scales at (u M + m) * 4.
+// row m is 64 bytes at (u M + m) * 64, its four scales at (u M + m) * 4.  One
+// row, 5760 x 2880: 4.7 us (1.9 TB/s of W), an empty launch 2.
 constexpr int FUSED4_BYTES = 20480, FUSED4_ROUNDS = FUSED4_BYTES / 4 / (64 * FK_NW);
 
 template <bool F32, bool VEC>
@@ -665,7 +685,9 @@ __global__ __launch_bounds__(64 * FK_NW) void fp4_fused_kernel(Fp4Gemm g, const 
 // ------------------------------------------------------------- input's gradient
 
 // W [N, K] decoded and transposed: 64 rows x 128 elements a workgroup, a thread
-// two rows x 8 elements, pairs of rows through LDS as words.
+// two rows x 8 elements, pairs of rows through LDS as words.  Bound by HBM: 5760
+// x 2880 in 12 us (3.5 TB/s; with 256 elements a workgroup, whole lines both
+// ways, 15).
 __global__ __launch_bounds__(256) void fp4_dequant_t_kernel(const uint8_t* __restrict__ w, int64_t wp,
                                                             const uint8_t* __restrict__ sw, int64_t N, int64_t K,
                                                             int ktiles, int64_t np, uint16_t* __restrict__ wt) {
@@ -703,6 +725,8 @@ __global__ __launch_bounds__(256) void fp4_dequant_t_kernel(const uint8_t* __res
   }
 }
 
+// Rows of dY at a pitch of whole K blocks and 16-byte alignment, which the
+// product's copies need; left out where dY has them.
 __global__ __launch_bounds__(256) void bf16_pad_kernel(const uint16_t* __restrict__ x, int64_t K, int64_t kp,
                                                        int64_t total, uint16_t* __restrict__ out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // 8 elements of the result
