@@ -22,7 +22,7 @@ struct BalanceArgs {
 };
 size_t balance_ws_bytes(int64_t T, int E, int S);
 // all launches of a forward: balance_launches of them, numbered from 0
-int balance_launches(int64_t T, int S);
+int balance_launches(int64_t T, int E, int S);
 hipError_t launch_balance(const BalanceArgs& a, int which, void* ws, hipStream_t s);
 // dlogits [T, E] from counts, tokens and dlosses [2], plus add [T, E] or nullptr
 hipError_t launch_balance_bwd(const BalanceArgs& a, const float* dlosses, const float* add, float* dlogits,

@@ -364,7 +364,7 @@ int mxmoe_balance(int score, int64_t T, int32_t E, int32_t k, int32_t S, const f
   a.prob = prob;
   hipStream_t s = static_cast<hipStream_t>(stream);
   static const char* const NAMES[] = {"balance_part", "balance_seq"};
-  for (int i = 0; i < mxmoe::balance_launches(T, S); ++i) LAUNCH(mxmoe::launch_balance(a, i, workspace, s), NAMES[i]);
+  for (int i = 0; i < mxmoe::balance_launches(T, E, S); ++i) LAUNCH(mxmoe::launch_balance(a, i, workspace, s), NAMES[i]);
   return ok();
 }
 
