@@ -7,9 +7,9 @@
 //   dx = rstd (w dy - xhat mean(w dy xhat)) + ds,  dw = sum over rows of dy xhat,
 //   xhat = s rstd
 //
-// One pass over the data: a row lives in the registers of NW waves, C chunks
-// of 8 elements a lane, so that 16 lanes side by side hold one 128-element
-// block of the 8-bit result.  Squares, means and the weight's gradient are
+// One pass over the data: a row lives in the registers of LR lanes (16 to 1024),
+// C chunks of 8 elements each, so that 16 lanes side by side hold one
+// 128-element block of the 8-bit result.  Squares, means and the weight's gradient are
 // summed in fp32; everything is rounded once, when it is stored.
 #include "common.hpp"
 #include "fp8.hpp"
@@ -17,23 +17,24 @@
 
 namespace mxmoe {
 
-// Eight consecutive elements as they are stored, zeros from `left` on.
+// Eight consecutive elements as they are stored, zeros from `left` on.  Rows of
+// any length begin at any element, and the memory takes 16-byte accesses at any:
+// WHOLE (H % 8 == 0) leaves out the rows' ends, which go element by element.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 template <bool F32>
 struct Raw8 {
   u32x4 q[F32 ? 2 : 1];
 };
-template <bool F32, bool VEC>
+template <bool F32, bool WHOLE>
 __device__ __forceinline__ Raw8<F32> raw8(const void* x, int64_t at, int64_t left) {
   Raw8<F32> r;
 #pragma unroll
   for (int i = 0; i < (F32 ? 2 : 1); ++i) r.q[i] = u32x4{0u, 0u, 0u, 0u};
-  if (VEC) {
-    if (left > 0) {
-      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2));
+  if (WHOLE ? left > 0 : left >= 8) {
+    const u32x4_any* p = reinterpret_cast<const u32x4_any*>(static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2));
 #pragma unroll
-      for (int i = 0; i < (F32 ? 2 : 1); ++i) r.q[i] = p[i];
-    }
-  } else {
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) r.q[i] = p[i];
+  } else if (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < left) {
@@ -53,66 +54,61 @@ __device__ __forceinline__ float value(const Raw8<F32>& r, int i) {
 }
 // The weight's eight elements: its type is an argument, not a template's (the
 // branch is uniform).
-template <bool VEC>
+template <bool WHOLE>
 __device__ __forceinline__ void weight8(const NormArgs& a, int64_t k0, float (&w)[8]) {
   if (a.w_f32) {
-    const Raw8<true> r = raw8<true, VEC>(a.w, k0, a.H - k0);
+    const Raw8<true> r = raw8<true, WHOLE>(a.w, k0, a.H - k0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = value<true>(r, i);
   } else {
-    const Raw8<false> r = raw8<false, VEC>(a.w, k0, a.H - k0);
+    const Raw8<false> r = raw8<false, WHOLE>(a.w, k0, a.H - k0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = value<false>(r, i);
   }
 }
 // Eight values rounded to fp32 or bf16, those before `left`.
-template <bool F32, bool VEC>
+template <bool F32, bool WHOLE>
 __device__ __forceinline__ void store8(void* p, int64_t at, int64_t left, const float (&v)[8]) {
-  if (VEC) {
-    if (left <= 0) return;
-    u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p) + at * (F32 ? 4 : 2));
+  if (WHOLE ? left > 0 : left >= 8) {
+    u32x4_any* d = reinterpret_cast<u32x4_any*>(static_cast<uint8_t*>(p) + at * (F32 ? 4 : 2));
     if (F32) {
       d[0] = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
       d[1] = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
     } else {
       d[0] = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
     }
-    return;
-  }
+  } else if (!WHOLE) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < left) {
-      if (F32)
-        static_cast<float*>(p)[at + i] = v[i];
-      else
-        static_cast<uint16_t*>(p)[at + i] = (uint16_t)f32_to_bf16(v[i]);
-    }
+    for (int i = 0; i < 8; ++i)
+      if (i < left) {
+        if (F32)
+          static_cast<float*>(p)[at + i] = v[i];
+        else
+          static_cast<uint16_t*>(p)[at + i] = (uint16_t)f32_to_bf16(v[i]);
+      }
+  }
 }
 
-template <class V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
-}
-// The sum over a row's NW waves, in their order.  Called by all of them.
-template <int NW, class V>
+// The sum over a row's LR lanes: of a part of a wave, or of whole ones in their
+// order, which all call it.
+template <int LR, class V>
 __device__ __forceinline__ V row_sum(V v, V* slots, int wave, int lane) {
-  v = wave_sum(v);
-  if (NW == 1) return v;
+#pragma unroll
+  for (int d = 1; d < (LR < 64 ? LR : 64); d <<= 1) v += __shfl_xor(v, d);
+  if (LR <= 64) return v;
   __syncthreads();   // the slots' last readers are done
   if (lane == 0) slots[wave] = v;
   __syncthreads();
   v = slots[0];
 #pragma unroll
-  for (int i = 1; i < NW; ++i) v += slots[i];
+  for (int i = 1; i < LR / 64; ++i) v += slots[i];
   return v;
 }
 
 // 1 / sqrt(mean of the squares + eps).  A sum of squares that fp32 cannot
 // hold (elements from about 1e18 on, or a tiny eps under tiny elements) is
 // formed again in fp64; a NaN or an infinity in the row stays one.
-template <int NW, int C>
+template <int LR, int C>
 __device__ __forceinline__ float row_rstd(const float (&v)[C][8], int64_t H, float eps, double* slots, int wave,
                                           int lane) {
   // sums of 8, of the chunks, then in fp64 over the lanes: the reciprocal's
@@ -125,38 +121,41 @@ __device__ __forceinline__ float row_rstd(const float (&v)[C][8], int64_t H, flo
     for (int i = 0; i < 8; ++i) t = fmaf(v[c][i], v[c][i], t);
     ss += t;
   }
-  const double m = row_sum<NW>((double)ss, slots, wave, lane) / (double)H + (double)eps;
+  const double m = row_sum<LR>((double)ss, slots, wave, lane) / (double)H + (double)eps;
   if (m > 1e-30 && m < 3e38) return (float)(1.0 / sqrt(m));
   double sd = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) sd += (double)v[c][i] * (double)v[c][i];
-  sd = row_sum<NW>(sd, slots, wave, lane);
+  sd = row_sum<LR>(sd, slots, wave, lane);
   return (float)(1.0 / sqrt(sd / (double)H + (double)eps));
 }
 
-// A row for NW waves; four waves a workgroup, or NW where that is more.  Bound
+// The threads of a workgroup whose rows have LR lanes each.
+constexpr int norm_block(int lr) { return lr < 256 ? 256 : lr; }
+
+// A row for LR lanes; 256 threads a workgroup, or LR where that is more.  Bound
 // by HBM: 16381 x 2880 bf16 with the residual, both results: 85 us, 5.0 TB/s;
-// 2047 x 2880 fp32, bf16 result: 15.6 us, 5.3 TB/s.  One row: 3.7 us.
-template <bool F32, bool VEC, int NW, int C>
-__global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_kernel(NormArgs a) {
-  __shared__ double slots[NW];
-  const int lane = threadIdx.x & 63, all = threadIdx.x >> 6, wave = all % NW;
-  const int64_t row = (int64_t)blockIdx.x * (NW < 4 ? 4 / NW : 1) + all / NW;
-  if (row >= a.T) return;   // whole waves, and with NW >= 4 none
+// 2047 x 2880 fp32, bf16 result: 15.5 us, 5.3 TB/s.  One row: 3.6 us.
+template <bool F32, bool WHOLE, int LR, int C>
+__global__ __launch_bounds__(norm_block(LR)) void norm_kernel(NormArgs a) {
+  __shared__ double slots[LR < 64 ? 1 : LR / 64];
+  const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % (LR < 64 ? 1 : LR / 64), l = threadIdx.x % LR;
+  const int64_t row = (int64_t)blockIdx.x * (norm_block(LR) / LR) + threadIdx.x / LR;
+  if (row >= a.T) return;   // all of a row's lanes, and with several waves none
   Raw8<F32> x[C], r[C];
   const int64_t at = row * a.H;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
-    x[c] = raw8<F32, VEC>(a.x, at + k0, a.H - k0);
+    const int64_t k0 = (c * LR + l) * 8;
+    x[c] = raw8<F32, WHOLE>(a.x, at + k0, a.H - k0);
   }
   if (a.residual) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
-      r[c] = raw8<F32, VEC>(a.residual, at + k0, a.H - k0);
+      const int64_t k0 = (c * LR + l) * 8;
+      r[c] = raw8<F32, WHOLE>(a.residual, at + k0, a.H - k0);
     }
   }
   float v[C][8];
@@ -165,26 +164,26 @@ __global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_kernel(NormArgs a
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[c][i] = value<F32>(x[c], i);
     if (a.residual) {
-      const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
+      const int64_t k0 = (c * LR + l) * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[c][i] += value<F32>(r[c], i);
         if (!F32) v[c][i] = bf16_to_f32((uint16_t)f32_to_bf16(v[c][i]));   // the stream as it is stored
       }
-      store8<F32, VEC>(a.sum, at + k0, a.H - k0, v[c]);
+      store8<F32, WHOLE>(a.sum, at + k0, a.H - k0, v[c]);
     }
   }
-  const float rstd = row_rstd<NW, C>(v, a.H, a.eps, slots, wave, lane);
-  if (wave == 0 && lane == 0) a.rstd[row] = rstd;
+  const float rstd = row_rstd<LR, C>(v, a.H, a.eps, slots, wave, lane);
+  if (l == 0) a.rstd[row] = rstd;
   const int64_t pitch = fp8_pitch(a.H), spitch = fp8_scale_pitch(a.T);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
+    const int64_t k0 = (c * LR + l) * 8;
     float w[8];
-    weight8<VEC>(a, k0, w);
+    weight8<WHOLE>(a, k0, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * rstd * w[i];
-    if (a.y) store8<false, VEC>(a.y, at + k0, a.H - k0, v[c]);
+    if (a.y) store8<false, WHOLE>(a.y, at + k0, a.H - k0, v[c]);
     if (a.codes) {
       uint32_t m = 0;
 #pragma unroll
@@ -213,12 +212,14 @@ __global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_kernel(NormArgs a
 // in order through LDS, and the parts [workgroups][H] are joined by another
 // launch (one workgroup writes dw itself).  Bound by HBM: 16384 x 2880 bf16
 // with the sum's own gradient in 77.8 us (4.8 TB/s), the join 5.5.
-template <bool F32, bool VEC, int NW, int C>
-__global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_bwd_kernel(NormArgs a) {
-  constexpr int ROWS = NW < 4 ? 4 / NW : 1;   // rows at a time
-  __shared__ double slots[NW];
-  __shared__ float add[ROWS == 1 ? 1 : C * NW * 512];
-  const int lane = threadIdx.x & 63, all = threadIdx.x >> 6, wave = all % NW;
+template <bool F32, bool WHOLE, int LR, int C>
+__global__ __launch_bounds__(norm_block(LR)) void norm_bwd_kernel(NormArgs a) {
+  constexpr int ROWS = norm_block(LR) / LR;   // rows at a time
+  constexpr bool LATE = C > 2;   // a row is read twice, chunk by chunk: 1024 threads have 128 registers each
+  __shared__ double slots[LR < 64 ? 1 : LR / 64];
+  __shared__ float add[ROWS == 1 ? 1 : C * LR * 8];
+  const int lane = threadIdx.x & 63, all = threadIdx.x >> 6, wave = all % (LR < 64 ? 1 : LR / 64);
+  const int l = threadIdx.x % LR;
   float dw[C][8];
 #pragma unroll
   for (int c = 0; c < C; ++c)
@@ -226,77 +227,92 @@ __global__ __launch_bounds__(64 * (NW < 4 ? 4 : NW)) void norm_bwd_kernel(NormAr
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
   const int64_t groups = (a.T + ROWS - 1) / ROWS;
   for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-    const int64_t row = g * ROWS + all / NW;
-    if (row >= a.T) break;   // whole waves, and with NW >= 4 none: no barrier is missed
+    const int64_t row = g * ROWS + threadIdx.x / LR;
+    if (row >= a.T) break;   // all of a row's lanes, and with several waves none: no barrier is missed
     const int64_t at = row * a.H;
     Raw8<F32> x[C], ds[C];
     Raw8<false> dy[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
-      x[c] = raw8<F32, VEC>(a.x, at + k0, a.H - k0);
-      dy[c] = raw8<false, VEC>(a.dy, at + k0, a.H - k0);
+      const int64_t k0 = (c * LR + l) * 8;
+      if (LATE) continue;
+      x[c] = raw8<F32, WHOLE>(a.x, at + k0, a.H - k0);
+      dy[c] = raw8<false, WHOLE>(a.dy, at + k0, a.H - k0);
     }
-    if (a.residual) {
+    if (a.residual && !LATE) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
-        ds[c] = raw8<F32, VEC>(a.residual, at + k0, a.H - k0);
+        const int64_t k0 = (c * LR + l) * 8;
+        ds[c] = raw8<F32, WHOLE>(a.residual, at + k0, a.H - k0);
       }
     }
     const float rstd = a.rstd[row];
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
+      const int64_t k0 = (c * LR + l) * 8;
+      if (LATE) {
+        x[c] = raw8<F32, WHOLE>(a.x, at + k0, a.H - k0);
+        dy[c] = raw8<false, WHOLE>(a.dy, at + k0, a.H - k0);
+      }
       float w[8];
-      weight8<VEC>(a, k0, w);
+      weight8<WHOLE>(a, k0, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float p = value<false>(dy[c], i) * (value<F32>(x[c], i) * rstd);
         dw[c][i] += p;
         dot = fmaf(w[i], p, dot);
       }
+      if (LATE) asm volatile("" : "+v"(dot)::"memory");   // no load is kept or moved ahead
     }
-    dot = row_sum<NW>(dot, reinterpret_cast<float*>(slots), wave, lane) / (float)a.H;
+    dot = row_sum<LR>(dot, reinterpret_cast<float*>(slots), wave, lane) / (float)a.H;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
+      const int64_t k0 = (c * LR + l) * 8;
       float w[8], d[8];
-      weight8<VEC>(a, k0, w);
+      weight8<WHOLE>(a, k0, w);
+      if (LATE) {
+        x[c] = raw8<F32, WHOLE>(a.x, at + k0, a.H - k0);
+        dy[c] = raw8<false, WHOLE>(a.dy, at + k0, a.H - k0);
+        if (a.residual) ds[c] = raw8<F32, WHOLE>(a.residual, at + k0, a.H - k0);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         d[i] = rstd * (w[i] * value<false>(dy[c], i) - value<F32>(x[c], i) * rstd * dot);
         if (a.residual) d[i] += value<F32>(ds[c], i);
       }
-      store8<F32, VEC>(a.sum, at + k0, a.H - k0, d);
+      store8<F32, WHOLE>(a.sum, at + k0, a.H - k0, d);
+      if (LATE) asm volatile("" : "+v"(dot)::"memory");
     }
   }
-  if (ROWS > 1) {   // the waves' sums, one wave after the other
+  if (ROWS > 1) {   // the rows of a wave, then the waves' sums, one wave after the other
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int d = LR; d < 64; d <<= 1) dw[c][i] += __shfl_xor(dw[c][i], d);
 #pragma unroll 1
-    for (int u = 0; u < ROWS; ++u) {
-      if (all / NW == u) {
+    for (int u = 0; u < 4; ++u) {
+      if (all == u && lane < LR) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float* p = &add[((c * NW + wave) * 8 + i) * 64 + lane];
+            float* p = &add[(c * 8 + i) * LR + l];
             dw[c][i] = u ? *p + dw[c][i] : dw[c][i];
             *p = dw[c][i];
           }
       }
       __syncthreads();
     }
-    if (all / NW != ROWS - 1) return;   // the last one has the sum
+    if (all != 3 || lane >= LR) return;   // the last wave has the sum
   }
   float* out = gridDim.x == 1 ? a.dw : a.part + (int64_t)blockIdx.x * a.H;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int64_t k0 = ((int64_t)(c * NW + wave) * 64 + lane) * 8;
-    if (VEC && gridDim.x > 1)
-      store8<true, true>(out, k0, a.H - k0, dw[c]);
-    else
-      store8<true, false>(out, k0, a.H - k0, dw[c]);   // dw may have any alignment
+    const int64_t k0 = (c * LR + l) * 8;
+    store8<true, WHOLE>(out, k0, a.H - k0, dw[c]);
   }
 }
 
@@ -322,21 +338,18 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict
 
 // ------------------------------------------------------------------ launchers
 
-static bool norm_vec(const NormArgs& a) {
-  auto ok = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  return a.H % 8 == 0 && ok(a.x) && ok(a.residual) && ok(a.w) && ok(a.sum) && ok(a.y) && ok(a.dy);
-}
-
-// Waves of a row and chunks of a lane, forward.  One wave a row moves most
-// bytes while rows fill the card; fewer rows, or longer ones, take more waves.
+// Lanes of a row and chunks of 8 a lane, forward.  A wave a row, or a part of one,
+// moves most bytes while rows fill the card; fewer rows of over 512, or longer
+// ones, take more waves.
 struct NormShape {
-  int nw, c;
+  int lr, c;
 };
 static NormShape norm_shape(int64_t T, int64_t H) {
   const int w = (int)((H + 511) / 512);   // chunks of one wave
-  if (w <= 6 && T >= 1024) return {1, w <= 2 ? 2 : w <= 4 ? 4 : 6};
-  if (w <= 16) return {4, w <= 4 ? 1 : w <= 8 ? 2 : 4};
-  return {16, w <= 32 ? 2 : 4};
+  if (w == 1) return {H <= 128 ? 16 : H <= 256 ? 32 : 64, 1};
+  if (w <= 6 && T >= 1024) return {64, w <= 2 ? 2 : w <= 4 ? 4 : 6};
+  if (w <= 16) return {256, w <= 4 ? 1 : w <= 8 ? 2 : 4};
+  return {1024, w <= 32 ? 2 : 4};
 }
 // Backward: a lane also holds the weight and its part of dw, so rows are split
 // wider, to 16 waves on a CU (16384 x 2880: one wave a row, 4 on a CU, 138 us;
@@ -344,42 +357,48 @@ static NormShape norm_shape(int64_t T, int64_t H) {
 // workgroups and parts 91).
 static NormShape norm_bwd_shape(int64_t H) {
   const int w = (int)((H + 511) / 512);
-  if (w <= 2) return {1, w};
-  if (w <= 8) return {4, w <= 4 ? 1 : 2};
-  if (w <= 16) return {8, 2};
-  return {16, w <= 32 ? 2 : 4};
+  if (w <= 2) return {H <= 128 ? 16 : H <= 256 ? 32 : 64, w};
+  if (w <= 8) return {256, w <= 4 ? 1 : 2};
+  if (w <= 16) return {512, 2};
+  return {1024, w <= 32 ? 2 : 4};
 }
-int64_t norm_blocks(int64_t T, int64_t H) { return norm_shape(T, H).nw == 1 ? (T + 3) / 4 : T; }
-int norm_threads(int64_t T, int64_t H) { return norm_shape(T, H).nw == 16 ? 1024 : 256; }
+int norm_threads(int64_t T, int64_t H) { return norm_block(norm_shape(T, H).lr); }
+int64_t norm_blocks(int64_t T, int64_t H) {
+  const int64_t rows = norm_threads(T, H) / norm_shape(T, H).lr;
+  return (T + rows - 1) / rows;
+}
 static unsigned norm_bwd_grid(int64_t T, int64_t H) {
-  const int nw = norm_bwd_shape(H).nw;
-  const int64_t groups = nw == 1 ? (T + 3) / 4 : T, most = nw <= 4 ? 1024 : 4096 / nw;
+  const int lr = norm_bwd_shape(H).lr, block = norm_block(lr);
+  const int64_t groups = (T + block / lr - 1) / (block / lr), most = 4 * 65536 / block;
   return (unsigned)(groups < most ? groups : most);
 }
 
-#define NORM_LAUNCH(kernel, grid, NW, C)                                                  \
-  do {                                                                                    \
-    const dim3 g_((unsigned)(grid)), b_(64 * (NW < 4 ? 4 : NW));                          \
-    const bool vec_ = norm_vec(a);                                                        \
-    if (a.f32 && vec_) hipLaunchKernelGGL((kernel<true, true, NW, C>), g_, b_, 0, s, a);  \
-    else if (a.f32) hipLaunchKernelGGL((kernel<true, false, NW, C>), g_, b_, 0, s, a);    \
-    else if (vec_) hipLaunchKernelGGL((kernel<false, true, NW, C>), g_, b_, 0, s, a);     \
-    else hipLaunchKernelGGL((kernel<false, false, NW, C>), g_, b_, 0, s, a);              \
-    return hipGetLastError();                                                             \
+#define NORM_LAUNCH(kernel, grid, LR, C)                                                    \
+  do {                                                                                      \
+    const dim3 g_((unsigned)(grid)), b_(norm_block(LR));                                    \
+    const bool whole_ = a.H % 8 == 0;                                                       \
+    if (a.f32 && whole_) hipLaunchKernelGGL((kernel<true, true, LR, C>), g_, b_, 0, s, a);  \
+    else if (a.f32) hipLaunchKernelGGL((kernel<true, false, LR, C>), g_, b_, 0, s, a);      \
+    else if (whole_) hipLaunchKernelGGL((kernel<false, true, LR, C>), g_, b_, 0, s, a);     \
+    else hipLaunchKernelGGL((kernel<false, false, LR, C>), g_, b_, 0, s, a);                \
+    return hipGetLastError();                                                               \
   } while (0)
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   const int64_t grid = norm_blocks(a.T, a.H);
   const NormShape n = norm_shape(a.T, a.H);
-  switch (100 * n.nw + n.c) {
-    case 102: NORM_LAUNCH(norm_kernel, grid, 1, 2);
-    case 104: NORM_LAUNCH(norm_kernel, grid, 1, 4);
-    case 106: NORM_LAUNCH(norm_kernel, grid, 1, 6);
-    case 401: NORM_LAUNCH(norm_kernel, grid, 4, 1);
-    case 402: NORM_LAUNCH(norm_kernel, grid, 4, 2);
-    case 404: NORM_LAUNCH(norm_kernel, grid, 4, 4);
-    case 1602: NORM_LAUNCH(norm_kernel, grid, 16, 2);
-    default: NORM_LAUNCH(norm_kernel, grid, 16, 4);
+  switch (10 * n.lr + n.c) {
+    case 161: NORM_LAUNCH(norm_kernel, grid, 16, 1);
+    case 321: NORM_LAUNCH(norm_kernel, grid, 32, 1);
+    case 641: NORM_LAUNCH(norm_kernel, grid, 64, 1);
+    case 642: NORM_LAUNCH(norm_kernel, grid, 64, 2);
+    case 644: NORM_LAUNCH(norm_kernel, grid, 64, 4);
+    case 646: NORM_LAUNCH(norm_kernel, grid, 64, 6);
+    case 2561: NORM_LAUNCH(norm_kernel, grid, 256, 1);
+    case 2562: NORM_LAUNCH(norm_kernel, grid, 256, 2);
+    case 2564: NORM_LAUNCH(norm_kernel, grid, 256, 4);
+    case 10242: NORM_LAUNCH(norm_kernel, grid, 1024, 2);
+    default: NORM_LAUNCH(norm_kernel, grid, 1024, 4);
   }
 }
 
@@ -392,14 +411,16 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
   if (norm_part_bytes(a.T, a.H) && !a.part) return hipErrorInvalidValue;
   const unsigned grid = norm_bwd_grid(a.T, a.H);
   const NormShape n = norm_bwd_shape(a.H);
-  switch (100 * n.nw + n.c) {
-    case 101: NORM_LAUNCH(norm_bwd_kernel, grid, 1, 1);
-    case 102: NORM_LAUNCH(norm_bwd_kernel, grid, 1, 2);
-    case 401: NORM_LAUNCH(norm_bwd_kernel, grid, 4, 1);
-    case 402: NORM_LAUNCH(norm_bwd_kernel, grid, 4, 2);
-    case 802: NORM_LAUNCH(norm_bwd_kernel, grid, 8, 2);
-    case 1602: NORM_LAUNCH(norm_bwd_kernel, grid, 16, 2);
-    default: NORM_LAUNCH(norm_bwd_kernel, grid, 16, 4);
+  switch (10 * n.lr + n.c) {
+    case 161: NORM_LAUNCH(norm_bwd_kernel, grid, 16, 1);
+    case 321: NORM_LAUNCH(norm_bwd_kernel, grid, 32, 1);
+    case 641: NORM_LAUNCH(norm_bwd_kernel, grid, 64, 1);
+    case 642: NORM_LAUNCH(norm_bwd_kernel, grid, 64, 2);
+    case 2561: NORM_LAUNCH(norm_bwd_kernel, grid, 256, 1);
+    case 2562: NORM_LAUNCH(norm_bwd_kernel, grid, 256, 2);
+    case 5122: NORM_LAUNCH(norm_bwd_kernel, grid, 512, 2);
+    case 10242: NORM_LAUNCH(norm_bwd_kernel, grid, 1024, 2);
+    default: NORM_LAUNCH(norm_bwd_kernel, grid, 1024, 4);
   }
 }
 
