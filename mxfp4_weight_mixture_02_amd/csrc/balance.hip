@@ -11,9 +11,8 @@
 //     c_e = a E f_se / (N_s S+),  q = p (softmax) or p (1 - sigmoid)
 //
 // A token is a row of 16 lanes, four tokens a wave: lane l has the experts 64 j
-// + 4 l + i (i = 0 .. 3), or 64 j + 16 i + l where rows are not 16-byte aligned,
-// so a row's sums are four DPP rotations and its loads whole 256- or 64-byte
-// pieces.  Scores are formed in fp32 relative to the largest of the
+// + 4 l .. + 3, so a row's sums are four DPP rotations and its loads whole
+// 256-byte pieces (16 bytes a lane, at any element).  Scores are formed in fp32 relative to the largest of the
 // token (of the sigmoids too: logits below -88 keep their ratios), with the
 // hardware's base-2 exponential and reciprocal (1 ulp each; the argument's
 // rounding is 2^-24 of it, which the largest scores do not see): the library's
@@ -41,24 +40,17 @@ __device__ __forceinline__ float row16_max(float v) {
   return fmaxf(v, row_ror<1>(v));
 }
 
-// The expert of lane l's element (j, i).
-template <bool WIDE>
-__device__ __forceinline__ int expert(int j, int i, int l) {
-  return 64 * j + (WIDE ? 4 * l + i : 16 * i + l);
-}
-// Lane l's elements (j, 0 .. 3) of a token; `fill` past E.
-template <bool WIDE>
-__device__ __forceinline__ f32x4 four(const float* row, int j, int l, int E, float fill) {
+// Four elements of a token from expert e on; `fill` past E.  WHOLE: E % 4 == 0.
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+template <bool WHOLE>
+__device__ __forceinline__ f32x4 four(const float* row, int e, int E, float fill) {
   f32x4 v = {fill, fill, fill, fill};
-  if (WIDE) {
-    const int e = expert<true>(j, 0, l);
-    if (e < E) v = *reinterpret_cast<const f32x4*>(row + e);
-  } else {
+  if (WHOLE ? e < E : e + 4 <= E) {
+    v = *reinterpret_cast<const f32x4_any*>(row + e);
+  } else if (!WHOLE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = expert<false>(j, i, l);
-      if (e < E) v[i] = row[e];
-    }
+    for (int i = 0; i < 3; ++i)
+      if (e + i < E) v[i] = row[e + i];
   }
   return v;
 }
@@ -68,10 +60,10 @@ template <int J>
 struct Logits {
   f32x4 x[J];
 };
-template <int J, bool WIDE>
+template <int J, bool WHOLE>
 __device__ __forceinline__ void logits16(const float* row, int E, int l, Logits<J>& v) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) v.x[j] = four<WIDE>(row, j, l, E, -__builtin_inff());
+  for (int j = 0; j < J; ++j) v.x[j] = four<WHOLE>(row, 64 * j + 4 * l, E, -__builtin_inff());
 }
 __device__ __forceinline__ float exp_hw(float v) { return __builtin_amdgcn_exp2f(v * 1.4426950408889634f); }
 
@@ -175,7 +167,7 @@ struct BalanceWs {
 //
 // Partial sums of a slot's tokens.  ONE: all tokens are one sequence and this
 // workgroup's, which also finishes.
-template <int J, bool SIG, bool WIDE, bool ONE>
+template <int J, bool SIG, bool WHOLE, bool ONE>
 __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArgs a, BalanceWs ws, int per) {
   __shared__ float part[BAL_WAVES][256];
   __shared__ int hist[256];
@@ -197,7 +189,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
   Logits<J> x;
   int live = 1, pick = -1;
   auto fetch = [&](int64_t t, Logits<J>& y, int& on, int& e) {
-    logits16<J, WIDE>(a.logits + t * a.E, a.E, l, y);
+    logits16<J, WHOLE>(a.logits + t * a.E, a.E, l, y);
     on = a.mask ? a.mask[t] : 1;
     e = l < a.k ? a.topk_idx[t * a.k + l] : -1;
   };
@@ -233,7 +225,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
     for (int i = 0; i < 4; ++i) {
       acc[j][i] += __shfl_xor(acc[j][i], 16);
       acc[j][i] += __shfl_xor(acc[j][i], 32);
-      if (lane < 16) part[wave][expert<WIDE>(j, i, l)] = acc[j][i];
+      if (lane < 16) part[wave][64 * j + 4 * l + i] = acc[j][i];
     }
   z += __shfl_xor(z, 16);
   z += __shfl_xor(z, 32);
@@ -402,7 +394,7 @@ __global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceArgs a, Balanc
 //
 // dlogits: 16 tokens at a time in a workgroup, `per` in all.  A wave looks its
 // first token's sequence up, and those of the rows whose tokens lie behind it.
-template <int J, bool SIG, bool WIDE>
+template <int J, bool SIG, bool WHOLE>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const float* __restrict__ dlosses,
                                                           const float* __restrict__ add,
                                                           float* __restrict__ dlogits, int per) {
@@ -411,7 +403,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const f
   const int64_t first = (int64_t)blockIdx.x * per, t1 = min(first + per, a.T);
   // the first token's logits are under way while the sequences are counted
   Logits<J> x;
-  if (first + row < t1) logits16<J, WIDE>(a.logits + (first + row) * a.E, a.E, l, x);
+  if (first + row < t1) logits16<J, WHOLE>(a.logits + (first + row) * a.E, a.E, l, x);
   int n_ = 0, some_ = 0;   // N <= T < 2^26
   for (int s = tid; s < a.S; s += 256) {
     const int n = a.tokens[s];
@@ -445,7 +437,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const f
       }
     }
     if (t >= t1) continue;
-    if (base > first) logits16<J, WIDE>(a.logits + t * a.E, a.E, l, x);
+    if (base > first) logits16<J, WHOLE>(a.logits + t * a.E, a.E, l, x);
     const bool live = s < a.S && seq_begin(a, s) <= t && !(a.mask && !a.mask[t]);
     float d[J][4] = {};
     if (live) {
@@ -458,7 +450,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const f
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int e = expert<WIDE>(j, i, l);
+          const int e = 64 * j + 4 * l + i;
           c[j][i] = e < a.E ? f * (float)counts[e] : 0.0f;
           dot = fmaf(c[j][i], q.p[j][i], dot);
         }
@@ -474,18 +466,17 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const f
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
+      const int e = 64 * j + 4 * l;
+      if (e >= a.E) continue;
       f32x4 v = {d[j][0], d[j][1], d[j][2], d[j][3]};
-      if (add) v += four<WIDE>(add + t * a.E, j, l, a.E, 0.0f);
-      float* o = dlogits + t * a.E;
-      if (WIDE) {
-        const int e = expert<true>(j, 0, l);
-        if (e < a.E) *reinterpret_cast<f32x4*>(o + e) = v;
+      if (add) v += four<WHOLE>(add + t * a.E, e, a.E, 0.0f);
+      float* o = dlogits + t * a.E + e;
+      if (WHOLE || e + 4 <= a.E) {
+        *reinterpret_cast<f32x4_any*>(o) = v;
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = expert<false>(j, i, l);
-          if (e < a.E) o[e] = v[i];
-        }
+        for (int i = 0; i < 3; ++i)
+          if (e + i < a.E) o[i] = v[i];
       }
     }
   }
@@ -536,12 +527,12 @@ static void part(const BalanceArgs& a, const BalanceWs& ws, int per, hipStream_t
   // one sequence of all tokens has a slot for each block
   const dim3 grid(ONE ? 1 : (unsigned)((a.T + per - 1) / per + (a.offsets ? a.S : 0))), block(64 * BAL_WAVES);
   if (a.sigmoid) {
-    if (a.wide)
+    if (a.E % 4 == 0)
       hipLaunchKernelGGL((balance_part_kernel<J, true, true, ONE>), grid, block, 0, s, a, ws, per);
     else
       hipLaunchKernelGGL((balance_part_kernel<J, true, false, ONE>), grid, block, 0, s, a, ws, per);
   } else {
-    if (a.wide)
+    if (a.E % 4 == 0)
       hipLaunchKernelGGL((balance_part_kernel<J, false, true, ONE>), grid, block, 0, s, a, ws, per);
     else
       hipLaunchKernelGGL((balance_part_kernel<J, false, false, ONE>), grid, block, 0, s, a, ws, per);
@@ -584,12 +575,12 @@ template <int J>
 static void bwd(const BalanceArgs& a, const float* dlosses, const float* add, float* dlogits, int per, hipStream_t s) {
   const dim3 grid((unsigned)((a.T + per - 1) / per)), block(256);
   if (a.sigmoid) {
-    if (a.wide)
+    if (a.E % 4 == 0)
       hipLaunchKernelGGL((balance_bwd_kernel<J, true, true>), grid, block, 0, s, a, dlosses, add, dlogits, per);
     else
       hipLaunchKernelGGL((balance_bwd_kernel<J, true, false>), grid, block, 0, s, a, dlosses, add, dlogits, per);
   } else {
-    if (a.wide)
+    if (a.E % 4 == 0)
       hipLaunchKernelGGL((balance_bwd_kernel<J, false, true>), grid, block, 0, s, a, dlosses, add, dlogits, per);
     else
       hipLaunchKernelGGL((balance_bwd_kernel<J, false, false>), grid, block, 0, s, a, dlosses, add, dlogits, per);

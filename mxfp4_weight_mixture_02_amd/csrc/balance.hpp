@@ -10,7 +10,6 @@ struct BalanceArgs {
   int64_t T;
   int E, k, S;
   int sigmoid;
-  int wide;                 // E % 4 == 0, logits (and dlogits, add) 16-byte aligned
   const float* logits;      // [T, E]
   const int32_t* topk_idx;  // [T, k]
   const uint8_t* mask;      // [T] or nullptr: nonzero counts

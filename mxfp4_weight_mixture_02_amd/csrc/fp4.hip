@@ -78,13 +78,22 @@ __device__ __forceinline__ uint32_t fp4_codes(const u32x4& x, uint32_t& scale) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x3), f, 3);
 }
 
+// The memory takes 16-byte accesses at any element, so rows of any length are
+// read and written so, but for their ends.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+typedef uint32_t __attribute__((aligned(2))) u32_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+typedef f32x2 __attribute__((aligned(4))) f32x2_any;
+
 // Eight consecutive elements of a row as bf16 pairs, zeros from `left` on.
-template <bool VEC>
+// WHOLE: rows have no ends.
+template <bool WHOLE>
 __device__ __forceinline__ u32x4 bf16x8_at(const uint16_t* x, int64_t at, int64_t left) {
   u32x4 r = {0u, 0u, 0u, 0u};
-  if (VEC) {
-    if (left > 0) r = *reinterpret_cast<const u32x4*>(x + at);
-  } else {
+  if (WHOLE ? left > 0 : left >= 8) {
+    r = *reinterpret_cast<const u32x4_any*>(x + at);
+  } else if (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < left) r[i >> 1] |= (uint32_t)x[at + i] << (16 * (i & 1));
@@ -98,7 +107,7 @@ __device__ __forceinline__ u32x4 bf16x8_at(const uint16_t* x, int64_t at, int64_
 // conversion by the hardware's, whose ties go to even.  Bound by HBM: 16384 x
 // 2880 bf16 in 22 to 29 us (with X in the last-level cache, or not), 4.2 TB/s;
 // 2047 x 2880 in 4.8.
-template <bool F32, bool VEC>
+template <bool F32, bool WHOLE>
 __global__ __launch_bounds__(256) void fp4_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t K,
                                                        int64_t pitch, int64_t srows, int kblocks,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -111,10 +120,10 @@ __global__ __launch_bounds__(256) void fp4_rows_kernel(const void* __restrict__ 
     for (int p = 0; p < 2; ++p) {
       const int64_t row = r0 + 8 * p + (tid >> 5), left = row < rows ? K - k0 : 0;
       float v[8];
-      if (VEC) {
+      if (WHOLE || left >= 8) {
         f32x4 a = {0, 0, 0, 0}, b = a;
         if (left > 0) {
-          const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(x) + row * K + k0);
+          const f32x4_any* q = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(x) + row * K + k0);
           a = q[0];
           b = q[1];
         }
@@ -134,7 +143,7 @@ __global__ __launch_bounds__(256) void fp4_rows_kernel(const void* __restrict__ 
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int64_t row = r0 + 8 * p + (tid >> 5);
-      v[p] = bf16x8_at<VEC>(static_cast<const uint16_t*>(x), row * K + k0, row < rows ? K - k0 : 0);
+      v[p] = bf16x8_at<WHOLE>(static_cast<const uint16_t*>(x), row * K + k0, row < rows ? K - k0 : 0);
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) c[p] = fp4_codes(v[p], s[p]);
@@ -348,24 +357,56 @@ __device__ __forceinline__ void fp4_block(const Fp4Wave& g, int kb, int there, c
 
 // F values of the bias from n on, zeros past N and without one.
 template <int F>
-__device__ __forceinline__ void fp4_bias(const uint16_t* bias, int64_t n, int64_t N, bool wide, float (&v)[F]) {
+__device__ __forceinline__ void fp4_bias(const uint16_t* bias, int64_t n, int64_t N, float (&v)[F]) {
   if (!bias) N = 0;
-  if (wide && (reinterpret_cast<uintptr_t>(bias) & (2 * F - 1)) == 0) {   // uniform
-    uint32_t w[F / 2];
+  if (n + F <= N) {
 #pragma unroll
-    for (int i = 0; i < F / 2; ++i) w[i] = n < N ? reinterpret_cast<const uint32_t*>(bias + n)[i] : 0u;
-#pragma unroll
-    for (int i = 0; i < F; ++i) v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    for (int i = 0; i < F; i += 2) {
+      const uint32_t w = *reinterpret_cast<const u32_any*>(bias + n + i);
+      v[i] = __uint_as_float(w << 16);
+      v[i + 1] = __uint_as_float(w & 0xFFFF0000u);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < F; ++i) v[i] = n + i < N ? bf16_to_f32(bias[n + i]) : 0.0f;
   }
 }
-struct Fp4Out {
-  int64_t M, N;
-  const uint16_t* bias;
-  void* out;
-};
+// F consecutive results out[m][n ..].
+template <int F, bool F32>
+__device__ __forceinline__ void fp4_store(void* out, int64_t M, int64_t N, int64_t m, int64_t n, const float (&v)[F]) {
+  if (m >= M) return;
+  const int64_t at = m * N + n;
+  if (n + F <= N) {
+    if constexpr (F32) {
+      float* d = static_cast<float*>(out) + at;
+      if constexpr (F == 2) {
+        *reinterpret_cast<f32x2_any*>(d) = f32x2{v[0], v[1]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < F; i += 4)
+          *reinterpret_cast<f32x4_any*>(d + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      }
+    } else {
+      uint16_t* d = static_cast<uint16_t*>(out) + at;
+      if constexpr (F == 2)
+        *reinterpret_cast<u32_any*>(d) = pack_bf16x2(v[0], v[1]);
+      else if constexpr (F == 4)
+        *reinterpret_cast<u32x2_any*>(d) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      else
+        *reinterpret_cast<u32x4_any*>(d) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+    if (n + i < N) {
+      if (F32)
+        static_cast<float*>(out)[at + i] = v[i];
+      else
+        static_cast<uint16_t*>(out)[at + i] = (uint16_t)f32_to_bf16(v[i]);
+    }
+}
 
 // A tile's place: its rows, and its part of K.
 struct Fp4Place {
@@ -535,19 +576,17 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
     // The copies of the next tile's second block come before the stores: a
     // wait for them later would be one for the stores.
     if (more) __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-    const bool wide = g.N % FN == 0;
-    const Fp4Out to{g.M, g.N, nullptr, g.out};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int64_t n = nw0 + (4 * t + q) * FN;
       float bias[FN];   // once for the lane's FM columns
-      fp4_bias<FN>(g.bias, n, g.N, wide, bias);
+      fp4_bias<FN>(g.bias, n, g.N, bias);
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
         float o[FN];
 #pragma unroll
         for (int i = 0; i < FN; ++i) o[i] = acc[i][j][t] + bias[i];
-        fp8_store<FN, F32>(to, done.m0 + wm * 16 * FM + r * FM + j, n, o, wide);
+        fp4_store<FN, F32>(g.out, g.M, g.N, done.m0 + wm * 16 * FM + r * FM + j, n, o);
       }
     }
     if (!more) break;
@@ -589,8 +628,11 @@ __device__ __forceinline__ void skinny4_store(const Fp4Gemm& g, f32x4 (*part)[64
   f32x4 sum = part[0][lane];
 #pragma unroll
   for (int u = 1; u < FK_NW; ++u) sum += part[u][lane];
-  float o[4] = {sum[0], sum[1], sum[2], sum[3]};
-  fp8_store<4, F32>(g, lane & 15, n0 + 4 * (lane >> 4), o, g.N % 4 == 0);
+  const int64_t n = n0 + 4 * (lane >> 4);
+  float bias[4];
+  fp4_bias<4>(g.bias, n, g.N, bias);
+  const float o[4] = {sum[0] + bias[0], sum[1] + bias[1], sum[2] + bias[2], sum[3] + bias[3]};
+  fp4_store<4, F32>(g.out, g.M, g.N, lane & 15, n, o);
 }
 
 // 4-bit X, up to 16 rows.
@@ -627,7 +669,7 @@ __global__ __launch_bounds__(64 * FK_NW) void fp4_skinny_kernel(Fp4Gemm g) {
 // row, 5760 x 2880: 4.7 us (1.9 TB/s of W), an empty launch 2.
 constexpr int FUSED4_BYTES = 20480, FUSED4_ROUNDS = FUSED4_BYTES / 4 / (64 * FK_NW);
 
-template <bool F32, bool VEC>
+template <bool F32, bool WHOLE>
 __global__ __launch_bounds__(64 * FK_NW) void fp4_fused_kernel(Fp4Gemm g, const uint16_t* __restrict__ xb) {
   __shared__ __align__(16) uint8_t xs[FUSED4_BYTES];
   __shared__ uint8_t sxs[FUSED4_BYTES / 16];
@@ -647,7 +689,7 @@ __global__ __launch_bounds__(64 * FK_NW) void fp4_fused_kernel(Fp4Gemm g, const 
   for (int i = 0; i < FUSED4_ROUNDS; ++i) {
     if (i < turns) {
       const int id = min(tid + i * 64 * FK_NW, groups - 1), m = id / (units * 16), k0 = 8 * (id % (units * 16));
-      xv[i] = bf16x8_at<VEC>(xb, m * g.K + k0, g.K - k0);
+      xv[i] = bf16x8_at<WHOLE>(xb, m * g.K + k0, g.K - k0);
     }
   }
   SkinnyW4 f;
@@ -741,14 +783,14 @@ hipError_t launch_fp4_quantize(const void* x, int x_f32, int64_t rows, int64_t K
                                hipStream_t s) {
   const int64_t kb = fp4_kblocks(K);
   const dim3 grid((unsigned)(kb * ((rows + 15) / 16)));
-  const bool vec = K % 8 == 0 && (reinterpret_cast<uintptr_t>(x) % 16) == 0;
+  const bool whole = K % 8 == 0;
   auto launch = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, rows, K, fp4_pitch(K), fp4_scale_rows(rows), (int)kb, codes,
                        scales);
     return hipGetLastError();
   };
-  if (x_f32) return vec ? launch(fp4_rows_kernel<true, true>) : launch(fp4_rows_kernel<true, false>);
-  return vec ? launch(fp4_rows_kernel<false, true>) : launch(fp4_rows_kernel<false, false>);
+  if (x_f32) return whole ? launch(fp4_rows_kernel<true, true>) : launch(fp4_rows_kernel<true, false>);
+  return whole ? launch(fp4_rows_kernel<false, true>) : launch(fp4_rows_kernel<false, false>);
 }
 
 hipError_t launch_fp4_scales(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* ordered, hipStream_t s) {
@@ -905,14 +947,14 @@ bool fp4_fused_fits(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_fp4_fused(const Fp4Gemm& g, const uint16_t* x, hipStream_t s) {
   if (!fp4_fused_fits(g.M, g.N, g.K)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * FK_NW);
-  const bool vec = g.K % 8 == 0 && (reinterpret_cast<uintptr_t>(x) % 16) == 0;
+  const bool whole = g.K % 8 == 0;
   if (g.out_f32) {
-    if (vec)
+    if (whole)
       hipLaunchKernelGGL((fp4_fused_kernel<true, true>), grid, block, 0, s, g, x);
     else
       hipLaunchKernelGGL((fp4_fused_kernel<true, false>), grid, block, 0, s, g, x);
   } else {
-    if (vec)
+    if (whole)
       hipLaunchKernelGGL((fp4_fused_kernel<false, true>), grid, block, 0, s, g, x);
     else
       hipLaunchKernelGGL((fp4_fused_kernel<false, false>), grid, block, 0, s, g, x);

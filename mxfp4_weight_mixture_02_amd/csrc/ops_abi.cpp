@@ -115,7 +115,6 @@ int balance_args(int score, int64_t T, int32_t E, int32_t k, int32_t S, const fl
   a->k = k;
   a->S = S;
   a->sigmoid = score == MXMOE_SCORE_SIGMOID;
-  a->wide = E % 4 == 0 && aligned(logits, 16);
   a->logits = logits;
   a->mask = mask;
   a->offsets = offsets;
@@ -378,7 +377,6 @@ int mxmoe_balance_backward(int score, int64_t T, int32_t E, int32_t k, int32_t S
   if (!dlosses || !dlogits) return fail(MXFP4_EINVAL, "dlosses and dlogits are required");
   if (!aligned(dlosses, 4) || !aligned(add, 4) || !aligned(dlogits, 4))
     return fail(MXFP4_EINVAL, "tensors must be 4-byte aligned");
-  a.wide = a.wide && aligned(add, 16) && aligned(dlogits, 16);
   hipStream_t s = static_cast<hipStream_t>(stream);
   LAUNCH(mxmoe::launch_balance_bwd(a, dlosses, add, dlogits, s), "balance_bwd");
   return ok();
