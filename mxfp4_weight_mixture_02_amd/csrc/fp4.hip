@@ -767,6 +767,131 @@ __global__ __launch_bounds__(256) void fp4_dequant_t_kernel(const uint8_t* __res
   }
 }
 
+// Few rows of dY: W's codes straight into fragments, with no copy in between.
+// The sum over n may take its terms in any order and columns of the result may
+// be in any: lane (r, q) reads a word of codes, columns 8 r .. + 7, of each of
+// the eight rows of W at 8 q, and the values of column 8 r + t of those rows are its
+// part of fragment t; dY's rows are the other operand.  A workgroup has 128 columns,
+// 16 rows of dY and a part of n, which its waves share in units of 32; their sums
+// meet in LDS and those of the parts in another launch, in their order.  Bound
+// by latency, HBM's and of the second launch (us, W 5760 x 2880 from HBM; by way
+// of the copy): 1 row 9.3 (24), 16 rows 10.4 (27), 64 rows 20 (28), 128 rows 30
+// (39), 192 rows 42 (47; 8192 x 1024: 23, 20).  32 or 64 rows a workgroup: 13 at
+// 16 of them, 21 at 64.
+struct DxUnit {
+  uint32_t w[8];
+  u32x4 s, y;
+};
+constexpr int DX_WAVES = 8;
+
+template <bool WHOLE>
+__global__ __launch_bounds__(64 * DX_WAVES) void fp4_dx_few_kernel(Fp4Gemm g, const uint16_t* __restrict__ dy,
+                                                                   int ktiles, int splits) {
+  __shared__ f32x4 red[DX_WAVES / 2][8][64];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // XCD x takes a contiguous range of the items: neighbours of 128 columns share
+  // lines of W
+  int item;
+  {
+    const int L = (int)gridDim.x, x = blockIdx.x & 7;
+    item = x * (L >> 3) + min(x, L & 7) + (blockIdx.x >> 3);
+  }
+  const int split = item / ktiles;
+  const int64_t k = (int64_t)(item % ktiles) * 128 + 8 * r, m0 = (int64_t)blockIdx.y * 16;
+  const int64_t N = g.N, srows = fp4_scale_rows(N), units = (N + 31) / 32;
+  const int u1 = (int)(units * (split + 1) / splits);
+  const int b = (int)(k >> 5);
+  // columns past K are computed as the first ones and not stored
+  const uint8_t* w = g.w + (k < g.K ? k / 2 : 0);
+  const uint8_t* sw = g.sw + (k < g.K ? ((int64_t)(b >> 3) * 4 + ((b >> 1) & 3)) * srows * 2 : 0);
+  const int par = 8 * (b & 1);   // the block's byte of a pair
+  auto load = [&](int u, DxUnit& f) {
+    const int64_t n = 32 * (int64_t)u + 8 * q;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f.w[j] = 0;   // rows past N have no codes
+      if (n + j < N) f.w[j] = *reinterpret_cast<const uint32_t*>(w + (n + j) * g.wp);
+    }
+    f.s = u32x4{0u, 0u, 0u, 0u};
+    if (n < N) f.s = *reinterpret_cast<const u32x4*>(sw + 2 * n);
+    f.y = bf16x8_at<WHOLE>(dy, min(m0 + r, g.M - 1) * N + n, N - n);
+  };
+  f32x4 acc[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  DxUnit f;
+  int u = (int)(units * split / splits) + wave;
+  if (u < u1) load(u, f);
+  for (; u < u1; u += DX_WAVES) {
+    DxUnit next;
+    if (u + DX_WAVES < u1) load(u + DX_WAVES, next);
+    u32x4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = dequant8_bf16(f.w[j], scale_operand(f.s[j >> 1] >> (16 * (j & 1) + par) & 255));
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      u32x4 c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = v[2 * j][t >> 1], hi = v[2 * j + 1][t >> 1];
+        c[j] = t & 1 ? lo >> 16 | (hi & 0xFFFF0000u) : (lo & 0xFFFFu) | hi << 16;
+      }
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f.y), as_bf16x8(c), acc[t], 0, 0, 0);
+    }
+    f = next;
+  }
+#pragma unroll
+  for (int h = DX_WAVES / 2; h >= 1; h /= 2) {
+    if (wave >= h && wave < 2 * h) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) red[wave - h][t][lane] = acc[t];
+    }
+    __syncthreads();
+    if (wave < h) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[t] += red[wave][t][lane];
+    }
+    __syncthreads();
+  }
+  if (wave) return;
+  void* out = splits > 1 ? static_cast<void*>(g.part + (int64_t)split * g.M * g.K) : g.out;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {   // D row 4 q + e: a row of dY
+    float o[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) o[t] = acc[t][e];
+    if (splits > 1 || g.out_f32)
+      fp4_store<8, true>(out, g.M, g.K, m0 + 4 * q + e, k, o);
+    else
+      fp4_store<8, false>(out, g.M, g.K, m0 + 4 * q + e, k, o);
+  }
+}
+
+// The parts' sum: four elements a thread.
+__global__ __launch_bounds__(256) void dx_join_kernel(const float* __restrict__ part, int64_t count, int splits,
+                                                      void* __restrict__ out, int out_f32) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (i + 4 <= count) {
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const f32x4 p = *reinterpret_cast<const f32x4_any*>(part + s * count + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += p[e];
+    }
+  } else {
+    for (int s = 0; s < splits; ++s)
+      for (int e = 0; e < 3; ++e)
+        if (i + e < count) v[e] += part[s * count + i + e];
+  }
+  if (out_f32)
+    fp4_store<4, true>(out, 1, count, 0, i, v);
+  else
+    fp4_store<4, false>(out, 1, count, 0, i, v);
+}
+
 // Rows of dY at a pitch of whole K blocks and 16-byte alignment, which the
 // product's copies need; left out where dY has them.
 __global__ __launch_bounds__(256) void bf16_pad_kernel(const uint16_t* __restrict__ x, int64_t K, int64_t kp,
@@ -934,6 +1059,33 @@ hipError_t launch_bf16_gemm(const Fp4Gemm& g, hipStream_t s) {
   Fp4Gemm b = g;
   b.wp = 2 * g.K;
   return gemm_of<false>(b, 2 * g.K, bf16_plan(g.M, g.N, g.K, g.out_f32 != 0), s);
+}
+
+// The gradient of few rows (above), in parts of n for a workgroup on every CU.
+bool fp4_dx_few(int64_t M) { return M <= 128; }
+static int dx_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t fill = 256 / (((K + 127) / 128) * ((M + 15) / 16)), units = (N + 31) / 32;
+  const int64_t most = (units + DX_WAVES - 1) / DX_WAVES;
+  return (int)(fill < 1 ? 1 : fill < most ? fill : most);
+}
+size_t fp4_dx_few_bytes(int64_t M, int64_t N, int64_t K) {
+  const int s = dx_splits(M, N, K);
+  return s > 1 ? (size_t)s * M * K * sizeof(float) : 0;
+}
+hipError_t launch_fp4_dx_few(const Fp4Gemm& g, const uint16_t* dy, hipStream_t s) {
+  const int splits = dx_splits(g.M, g.N, g.K), ktiles = (int)((g.K + 127) / 128);
+  if (splits > 1 && !g.part) return hipErrorInvalidValue;
+  const dim3 grid(ktiles * splits, (unsigned)((g.M + 15) / 16)), block(64 * DX_WAVES);
+  if (g.N % 8 == 0)
+    hipLaunchKernelGGL(fp4_dx_few_kernel<true>, grid, block, 0, s, g, dy, ktiles, splits);
+  else
+    hipLaunchKernelGGL(fp4_dx_few_kernel<false>, grid, block, 0, s, g, dy, ktiles, splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t count = g.M * g.K;
+  hipLaunchKernelGGL(dx_join_kernel, dim3((unsigned)((count + 1023) / 1024)), dim3(256), 0, s, g.part, count, splits,
+                     g.out, g.out_f32);
+  return hipGetLastError();
 }
 
 // The one-launch form: X's codes fit its LDS, and rounding them in every

@@ -247,6 +247,10 @@ Fp4Layout fp4_layout(int64_t M, int64_t N, int64_t K, int out_f32) {
 Fp4Layout dx4_layout(int64_t M, int64_t N, int64_t K, int out_f32) {
   const size_t np = (size_t)mxmoe::fp8_up(N, 64);
   Fp4Layout L{};
+  if (mxmoe::fp4_dx_few(M)) {   // W is read as it is
+    L.total = up(mxmoe::fp4_dx_few_bytes(M, N, K), ALIGN) + ALIGN;
+    return L;
+  }
   L.second = up((size_t)K * np * 2, ALIGN);
   L.part = L.second + up((size_t)M * np * 2, ALIGN);
   L.total = L.part + up(mxmoe::bf16_part_bytes(M, K, (int64_t)np, out_f32), ALIGN);
@@ -635,6 +639,20 @@ int mxmoe_fp4_linear_dx(int64_t M, int64_t N, int64_t K, const uint16_t* dy, con
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int64_t np = mxmoe::fp8_up(N, 64);
+  mxmoe::Fp4Gemm g{};
+  g.M = M;
+  g.out = dx;
+  g.out_f32 = out_dtype == MXMOE_F32;
+  g.part = reinterpret_cast<float*>(ws + L.part);
+  if (mxmoe::fp4_dx_few(M)) {
+    g.N = N;
+    g.K = K;
+    g.w = w_codes;
+    g.wp = w_pitch;
+    g.sw = w_scales;
+    LAUNCH(mxmoe::launch_fp4_dx_few(g, dy, s), "fp4_dx_few");
+    return ok();
+  }
   LAUNCH(mxmoe::launch_fp4_dequant_t(w_codes, w_pitch, w_scales, N, K, reinterpret_cast<uint16_t*>(ws), s),
          "fp4_dequant_t");
   const uint16_t* rows = dy;
@@ -643,15 +661,10 @@ int mxmoe_fp4_linear_dx(int64_t M, int64_t N, int64_t K, const uint16_t* dy, con
     LAUNCH(mxmoe::launch_bf16_pad(dy, M, N, pad, s), "bf16_pad");
     rows = pad;
   }
-  mxmoe::Fp4Gemm g{};
-  g.M = M;
   g.N = K;
   g.K = np;
   g.x = reinterpret_cast<const uint8_t*>(rows);
   g.w = ws;
-  g.out = dx;
-  g.out_f32 = out_dtype == MXMOE_F32;
-  g.part = reinterpret_cast<float*>(ws + L.part);
   LAUNCH(mxmoe::launch_bf16_gemm(g, s), "bf16_matmul");
   return ok();
 }

@@ -131,7 +131,10 @@ def test_products_are_exact(M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 64, 32), (2, 33, 96), (16, 100, 260), (65, 129, 100), (130, 64, 257),
                                    (70, 1000, 640), (300, 777, 1312), (2049, 1001, 288), (2050, 2881, 1001),
-                                   (4099, 320, 2881), (33, 5760, 2880), (5000, 130, 64), (1030, 100, 8200)])
+                                   (4099, 320, 2881), (33, 5760, 2880), (5000, 130, 64), (1030, 100, 8200),
+                                   # up to 128 rows: one part of n and several, units and columns past the edges
+                                   (1, 5760, 2880), (3, 70, 33000), (128, 333, 4064), (127, 8191, 160), (17, 1001, 8200),
+                                   (100, 40001, 96), (129, 333, 4064), (64, 31, 2883), (8, 257, 31), (113, 256, 129)])
 def test_input_gradients_are_exact(M, N, K):
     """dy of integers up to 8: sums of 5760 products below 2^24 steps of 1/4."""
     print("dx", M, N, K, flush=True)

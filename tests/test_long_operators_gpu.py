@@ -88,7 +88,7 @@ def test_rows_of_a_product():
         assert torch.all((y[a:b].double() - u @ v.t()).abs() <= (u.abs() @ v.abs().t()) * K * 2.0 ** -23)
 
 
-@pytest.mark.parametrize("M", [3, 40])
+@pytest.mark.parametrize("M", [3, 40, 130])
 def test_rows_of_weights(M):
     """And the weights' transpose, 17 GB in bf16, of the gradient."""
     N, K = ROWS, 8400
