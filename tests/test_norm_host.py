@@ -39,7 +39,7 @@ def _refused(code, rc):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(T=0), -1), (dict(H=0), -1), (dict(H=32769), -2), (dict(T=1 << 28, H=128), -2), (dict(T=1 << 40), -2),
-    (dict(T=(1 << 26) + 4, H=1), -2), (dict(x=None), -1), (dict(w=None), -1), (dict(rstd=None), -1),
+    (dict(T=(1 << 28) - 15, H=1), -2), (dict(T=(1 << 26) + 4, H=300), -2), (dict(x=None), -1), (dict(w=None), -1), (dict(rstd=None), -1),
     (dict(y=None, codes=None, scales=None), -1), (dict(scales=None), -1), (dict(codes=None), -1), (dict(sum=None), -1),
     (dict(res=None), -1), (dict(dtype=2), -1), (dict(wt=7), -1), (dict(x=FAKE + 1), -1), (dict(dtype=0, res=FAKE + 2), -1),
     (dict(sum=FAKE + 1), -1), (dict(wt=0, w=FAKE + 2), -1), (dict(y=FAKE + 1), -1), (dict(codes=FAKE + 8), -1),
