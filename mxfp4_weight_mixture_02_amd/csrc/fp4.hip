@@ -774,20 +774,20 @@ __global__ __launch_bounds__(256) void fp4_dequant_t_kernel(const uint8_t* __res
 // part of fragment t; dY's rows are the other operand.  A workgroup has 128 columns,
 // 16 rows of dY and a part of n, which its waves share in units of 32; their sums
 // meet in LDS and those of the parts in another launch, in their order.  Bound
-// by latency, HBM's and of the second launch (us, W 5760 x 2880 from HBM; by way
-// of the copy): 1 row 9.3 (24), 16 rows 10.4 (27), 64 rows 20 (28), 128 rows 30
-// (39), 192 rows 42 (47; 8192 x 1024: 23, 20).  32 or 64 rows a workgroup: 13 at
-// 16 of them, 21 at 64.
+// by the arithmetic that decodes W (32 conversions and 32 permutations for 8
+// MT products), by HBM and the second launch for few rows (us, W 5760 x 2880 from
+// HBM; by way of the copy): 1 row 9.0 (24), 16 rows 10 (28), 64 rows 15 (28), 256
+// rows 33 (48), 512 rows 49 (59).  Units read two and more ahead: no gain.
+template <int MT>
 struct DxUnit {
   uint32_t w[8];
-  u32x4 s, y;
+  u32x4 s, y[MT];
 };
 constexpr int DX_WAVES = 8;
-
-template <bool WHOLE>
+template <int MT, bool WHOLE>
 __global__ __launch_bounds__(64 * DX_WAVES) void fp4_dx_few_kernel(Fp4Gemm g, const uint16_t* __restrict__ dy,
                                                                    int ktiles, int splits) {
-  __shared__ f32x4 red[DX_WAVES / 2][8][64];
+  __shared__ f32x4 red[DX_WAVES / 2][8 * MT][64];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // XCD x takes a contiguous range of the items: neighbours of 128 columns share
@@ -798,7 +798,7 @@ __global__ __launch_bounds__(64 * DX_WAVES) void fp4_dx_few_kernel(Fp4Gemm g, co
     item = x * (L >> 3) + min(x, L & 7) + (blockIdx.x >> 3);
   }
   const int split = item / ktiles;
-  const int64_t k = (int64_t)(item % ktiles) * 128 + 8 * r, m0 = (int64_t)blockIdx.y * 16;
+  const int64_t k = (int64_t)(item % ktiles) * 128 + 8 * r, m0 = (int64_t)blockIdx.y * 16 * MT;
   const int64_t N = g.N, srows = fp4_scale_rows(N), units = (N + 31) / 32;
   const int u1 = (int)(units * (split + 1) / splits);
   const int b = (int)(k >> 5);
@@ -806,7 +806,7 @@ __global__ __launch_bounds__(64 * DX_WAVES) void fp4_dx_few_kernel(Fp4Gemm g, co
   const uint8_t* w = g.w + (k < g.K ? k / 2 : 0);
   const uint8_t* sw = g.sw + (k < g.K ? ((int64_t)(b >> 3) * 4 + ((b >> 1) & 3)) * srows * 2 : 0);
   const int par = 8 * (b & 1);   // the block's byte of a pair
-  auto load = [&](int u, DxUnit& f) {
+  auto load = [&](int u, DxUnit<MT>& f) {
     const int64_t n = 32 * (int64_t)u + 8 * q;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -815,17 +815,18 @@ __global__ __launch_bounds__(64 * DX_WAVES) void fp4_dx_few_kernel(Fp4Gemm g, co
     }
     f.s = u32x4{0u, 0u, 0u, 0u};
     if (n < N) f.s = *reinterpret_cast<const u32x4*>(sw + 2 * n);
-    f.y = bf16x8_at<WHOLE>(dy, min(m0 + r, g.M - 1) * N + n, N - n);
-  };
-  f32x4 acc[8];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  DxUnit f;
+    for (int i = 0; i < MT; ++i) f.y[i] = bf16x8_at<WHOLE>(dy, min(m0 + 16 * i + r, g.M - 1) * N + n, N - n);
+  };
+  f32x4 acc[MT][8];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  DxUnit<MT> f;
   int u = (int)(units * split / splits) + wave;
   if (u < u1) load(u, f);
-  for (; u < u1; u += DX_WAVES) {
-    DxUnit next;
-    if (u + DX_WAVES < u1) load(u + DX_WAVES, next);
+  while (u < u1) {
     u32x4 v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = dequant8_bf16(f.w[j], scale_operand(f.s[j >> 1] >> (16 * (j & 1) + par) & 255));
@@ -837,35 +838,45 @@ __global__ __launch_bounds__(64 * DX_WAVES) void fp4_dx_few_kernel(Fp4Gemm g, co
         const uint32_t lo = v[2 * j][t >> 1], hi = v[2 * j + 1][t >> 1];
         c[j] = t & 1 ? lo >> 16 | (hi & 0xFFFF0000u) : (lo & 0xFFFFu) | hi << 16;
       }
-      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f.y), as_bf16x8(c), acc[t], 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f.y[i]), as_bf16x8(c), acc[i][t], 0, 0, 0);
     }
-    f = next;
+    u += DX_WAVES;
+    if (u < u1) load(u, f);
   }
 #pragma unroll
   for (int h = DX_WAVES / 2; h >= 1; h /= 2) {
     if (wave >= h && wave < 2 * h) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t) red[wave - h][t][lane] = acc[t];
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) red[wave - h][8 * i + t][lane] = acc[i][t];
     }
     __syncthreads();
     if (wave < h) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t) acc[t] += red[wave][t][lane];
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) acc[i][t] += red[wave][8 * i + t][lane];
     }
     __syncthreads();
   }
   if (wave) return;
   void* out = splits > 1 ? static_cast<void*>(g.part + (int64_t)split * g.M * g.K) : g.out;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {   // D row 4 q + e: a row of dY
-    float o[8];
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int t = 0; t < 8; ++t) o[t] = acc[t][e];
-    if (splits > 1 || g.out_f32)
-      fp4_store<8, true>(out, g.M, g.K, m0 + 4 * q + e, k, o);
-    else
-      fp4_store<8, false>(out, g.M, g.K, m0 + 4 * q + e, k, o);
-  }
+    for (int e = 0; e < 4; ++e) {   // D row 4 q + e: a row of dY
+      float o[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) o[t] = acc[i][t][e];
+      const int64_t m = m0 + 16 * i + 4 * q + e;
+      if (splits > 1 || g.out_f32)
+        fp4_store<8, true>(out, g.M, g.K, m, k, o);
+      else
+        fp4_store<8, false>(out, g.M, g.K, m, k, o);
+    }
 }
 
 // The parts' sum: four elements a thread.
@@ -1061,25 +1072,56 @@ hipError_t launch_bf16_gemm(const Fp4Gemm& g, hipStream_t s) {
   return gemm_of<false>(b, 2 * g.K, bf16_plan(g.M, g.N, g.K, g.out_f32 != 0), s);
 }
 
-// The gradient of few rows (above), in parts of n for a workgroup on every CU.
-bool fp4_dx_few(int64_t M) { return M <= 128; }
-static int dx_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t fill = 256 / (((K + 127) / 128) * ((M + 15) / 16)), units = (N + 31) / 32;
-  const int64_t most = (units + DX_WAVES - 1) / DX_WAVES;
-  return (int)(fill < 1 ? 1 : fill < most ? fill : most);
+// The gradient of few rows (above): rows of dY of a workgroup, parts of n and
+// time, fitted to the launches listed there, 2880 x 2880, 1000 x 8192, 8192 x 1024,
+// 336 x 4064, 8192 x 160, 512 x 512 and 4096 x 4096 with 1 to 1024 rows.
+struct DxPlan {
+  int mt, splits;
+  float us;
+};
+static DxPlan dx_plan(int64_t M, int64_t N, int64_t K) {
+  static constexpr struct {
+    int mt;
+    float unit, c;
+  } SHAPE[] = {{1, 1.12f, 3.4f}, {2, 1.35f, 4.5f}, {4, 1.89f, 6.4f}};
+  const int64_t units = (N + 31) / 32, most = (units + DX_WAVES - 1) / DX_WAVES;
+  DxPlan best{0, 0, 0.0f};
+  for (const auto& t : SHAPE) {
+    const int64_t items = ((K + 127) / 128) * ((M + 16 * t.mt - 1) / (16 * t.mt));
+    const int64_t fill = 256 / items < 1 ? 1 : 256 / items, splits = fill < most ? fill : most;
+    float us = (float)((items * splits + 255) / 256) * (t.unit * (float)((most + splits - 1) / splits) + t.c);
+    if (splits > 1) us += 3.0f + (float)(splits * M * K) * 8.0f / 4.0e6f;
+    if (best.mt == 0 || us < best.us) best = {t.mt, (int)splits, us};
+  }
+  return best;
+}
+// Or by way of the copy, whose launch moves 2.5 N K bytes at 3.5 TB/s: over 80
+// random sizes of 48 to 1024 rows the choice is at most 4% slower than the better
+// way, but for two (15% and 47%).  Beyond 1024 rows the copy is a small part.
+bool fp4_dx_few(int64_t M, int64_t N, int64_t K, int out_f32) {
+  if (M > 1024) return false;
+  const int64_t np = fp8_up(N, 64);
+  return dx_plan(M, N, K).us < bf16_plan(M, K, np, out_f32 != 0).us + 6.0f + (float)(np * K) * 2.5f / 3.5e6f;
 }
 size_t fp4_dx_few_bytes(int64_t M, int64_t N, int64_t K) {
-  const int s = dx_splits(M, N, K);
+  const int s = dx_plan(M, N, K).splits;
   return s > 1 ? (size_t)s * M * K * sizeof(float) : 0;
 }
 hipError_t launch_fp4_dx_few(const Fp4Gemm& g, const uint16_t* dy, hipStream_t s) {
-  const int splits = dx_splits(g.M, g.N, g.K), ktiles = (int)((g.K + 127) / 128);
+  const DxPlan p = dx_plan(g.M, g.N, g.K);
+  const int splits = p.splits, ktiles = (int)((g.K + 127) / 128);
   if (splits > 1 && !g.part) return hipErrorInvalidValue;
-  const dim3 grid(ktiles * splits, (unsigned)((g.M + 15) / 16)), block(64 * DX_WAVES);
-  if (g.N % 8 == 0)
-    hipLaunchKernelGGL(fp4_dx_few_kernel<true>, grid, block, 0, s, g, dy, ktiles, splits);
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(ktiles * splits, (unsigned)((g.M + 16 * p.mt - 1) / (16 * p.mt))),
+                       dim3(64 * DX_WAVES), 0, s, g, dy, ktiles, splits);
+  };
+  const bool whole = g.N % 8 == 0;
+  if (p.mt == 1)
+    whole ? launch(fp4_dx_few_kernel<1, true>) : launch(fp4_dx_few_kernel<1, false>);
+  else if (p.mt == 2)
+    whole ? launch(fp4_dx_few_kernel<2, true>) : launch(fp4_dx_few_kernel<2, false>);
   else
-    hipLaunchKernelGGL(fp4_dx_few_kernel<false>, grid, block, 0, s, g, dy, ktiles, splits);
+    whole ? launch(fp4_dx_few_kernel<4, true>) : launch(fp4_dx_few_kernel<4, false>);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   const int64_t count = g.M * g.K;

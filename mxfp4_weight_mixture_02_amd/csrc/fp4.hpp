@@ -40,8 +40,8 @@ bool fp4_fused_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_fp4_fused(const Fp4Gemm& g, const uint16_t* x, hipStream_t s);
 
 // out [M, K] = X W for bf16 rows x [M, N] (of g: N and K of W, w, wp, sw, out,
-// out_f32, part of fp4_dx_few_bytes), for few rows
-bool fp4_dx_few(int64_t M);
+// out_f32, part of fp4_dx_few_bytes), where that is the faster way
+bool fp4_dx_few(int64_t M, int64_t N, int64_t K, int out_f32);
 size_t fp4_dx_few_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_fp4_dx_few(const Fp4Gemm& g, const uint16_t* x, hipStream_t s);
 // W [N, K] -> its transpose in bf16 [K, N rounded up to 64], zeros past N

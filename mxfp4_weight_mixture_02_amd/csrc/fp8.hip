@@ -923,6 +923,7 @@ GemmPlan gemm_plan(const GemmShape* shapes, int count, int64_t M, int64_t N, int
   }
   best.bn = shapes[best.tile].bn;
   best.bm = shapes[best.tile].bm;
+  best.us = least;
   return best;
 }
 

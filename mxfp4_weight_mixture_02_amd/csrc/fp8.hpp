@@ -53,6 +53,7 @@ struct GemmShape {
 // whole, and the parts of K in which the others are.
 struct GemmPlan {
   int tile, whole, rest, splits, bn, bm;
+  float us;   // the launches' estimate
 };
 GemmPlan gemm_plan(const GemmShape* shapes, int count, int64_t M, int64_t N, int64_t kblocks, bool f32);
 inline size_t gemm_part_bytes(const GemmPlan& p) {

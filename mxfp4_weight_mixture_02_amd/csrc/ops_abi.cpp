@@ -247,7 +247,7 @@ Fp4Layout fp4_layout(int64_t M, int64_t N, int64_t K, int out_f32) {
 Fp4Layout dx4_layout(int64_t M, int64_t N, int64_t K, int out_f32) {
   const size_t np = (size_t)mxmoe::fp8_up(N, 64);
   Fp4Layout L{};
-  if (mxmoe::fp4_dx_few(M)) {   // W is read as it is
+  if (mxmoe::fp4_dx_few(M, N, K, out_f32)) {   // W is read as it is
     L.total = up(mxmoe::fp4_dx_few_bytes(M, N, K), ALIGN) + ALIGN;
     return L;
   }
@@ -644,7 +644,7 @@ int mxmoe_fp4_linear_dx(int64_t M, int64_t N, int64_t K, const uint16_t* dy, con
   g.out = dx;
   g.out_f32 = out_dtype == MXMOE_F32;
   g.part = reinterpret_cast<float*>(ws + L.part);
-  if (mxmoe::fp4_dx_few(M)) {
+  if (mxmoe::fp4_dx_few(M, N, K, g.out_f32)) {
     g.N = N;
     g.K = K;
     g.w = w_codes;

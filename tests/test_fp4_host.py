@@ -81,7 +81,7 @@ def test_linear_refuses(kw, code):
 
 @pytest.mark.parametrize("kw,code", SIZES + [
     (dict(K=(1 << 22) + 1), -2), (dict(N=(1 << 22) + 1), -2), (dict(dy=None), -1), (dict(dy=FAKE + 1), -1),
-    (dict(n=128), -3), (dict(M=129, n=1024), -3), (dict(M=1 << 26, N=1024), -2)])
+    (dict(n=128), -3), (dict(M=2000, n=1024), -3), (dict(M=1 << 26, N=1024), -2)])
 def test_linear_dx_refuses(kw, code):
     d = dict(M=4, N=4, K=64, dy=FAKE, w=FAKE, wp=128, sw=FAKE, od=1, out=FAKE, ws=FAKE, n=BIG)
     d.update(kw)
