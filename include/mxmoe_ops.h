@@ -221,8 +221,8 @@ size_t mxmoe_fp8_linear_dw_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * product's M * N < 2^37 (both rounded up to 128), and N <= 2^27 - 16 where
  * M <= 16. */
 
-/* x [rows, K], dtype MXMOE_F32 or MXMOE_BF16 (any alignment of the dtype's; 16
- * bytes and K % 8 == 0 run faster), any K: codes [rows, Kp / 2] and scales. */
+/* x [rows, K], dtype MXMOE_F32 or MXMOE_BF16 (aligned to its elements), any K
+ * (multiples of 8 run faster): codes [rows, Kp / 2] and scales. */
 int mxmoe_fp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
                        void* stream);
 /* The scales [rows, K / 32] of mxfp4_quantize in the order above; K % 32 == 0. */
@@ -232,7 +232,7 @@ int mxmoe_fp4_scales(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* or
  * pitch); bias bf16 [N] or NULL; out bf16 or fp32 (out_dtype), 16-byte aligned,
  * rounded once.  Products are exact and summed in fp32 (values below 2^-126 may
  * count as 0).  The order of the sums, and so the result's last bits, depend on
- * M, N and K alone. */
+ * M, N, K and out_dtype alone. */
 int mxmoe_fp4_matmul(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
                      const uint8_t* w_codes, int64_t w_pitch, const uint8_t* w_scales, const uint16_t* bias,
                      int out_dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
@@ -291,8 +291,8 @@ int mxmoe_swiglu8_restore(const uint8_t* codes, const uint8_t* scales, int64_t R
  *  matrix with block_rows 1 (codes [T, Hp], scales [Hp / 128, T rounded up to
  *  16]), or both, each rounded once; what is not wanted is NULL.
  * weight [H] in w_dtype.  sum may be x or residual.  1 <= H <= 32768, T >= 1,
- * (T + 15) * Hp < 2^35, eps > 0 and finite; tensors aligned to their elements
- * (16 bytes and H % 8 == 0 run faster), codes 16-byte aligned. */
+ * (T + 15) * Hp < 2^35 (and T <= 2^26 - 4 with H in 257 .. 384), eps > 0 and
+ * finite; tensors aligned to their elements, codes 16-byte aligned. */
 int mxmoe_rms_norm(const void* x, const void* residual, int dtype, const void* weight, int w_dtype, int64_t T,
                    int64_t H, float eps, void* sum, uint16_t* y, uint8_t* codes, uint8_t* scales, float* rstd,
                    void* stream);

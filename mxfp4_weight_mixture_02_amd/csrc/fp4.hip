@@ -7,7 +7,8 @@
 // nothing is dropped: sums of blocks 2^24 apart came out as in fp32).  The
 // input's gradient dX = dY W sums along W's rows, where a block of 32 has as
 // many scales: no scaled product.  dY stays in bf16 and W is decoded, exactly,
-// to a transposed bf16 copy that the bf16 matrix core reads.
+// for the bf16 matrix core: as its codes are read for few rows of dY, else once
+// into a transposed copy.
 //
 // Storage: W's codes stay where they are ([N, K / 2]); X's rows are padded
 // with zeros to 256, so whatever a row of W is followed by is multiplied by 0.
@@ -815,6 +816,11 @@ __global__ __launch_bounds__(64 * DX_WAVES) void fp4_dx_few_kernel(Fp4Gemm g, co
     }
     f.s = u32x4{0u, 0u, 0u, 0u};
     if (n < N) f.s = *reinterpret_cast<const u32x4*>(sw + 2 * n);
+    if (!WHOLE) {   // past the rows any bytes may stand, NaN too
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j >= N) f.s[j >> 1] &= j & 1 ? 0xFFFFu : 0u;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) f.y[i] = bf16x8_at<WHOLE>(dy, min(m0 + 16 * i + r, g.M - 1) * N + n, N - n);
   };

@@ -206,6 +206,19 @@ def test_a_nan_block_stays_in_its_row(M, N):
     assert torch.equal(torch.isnan(dx), cols.expand(M, K))
 
 
+@pytest.mark.parametrize("M", [1, 20, 40, 1100])
+@pytest.mark.parametrize("N,K", [(1, 40), (257, 352), (1001, 96), (1030, 288)])
+def test_scales_past_the_rows_are_not_used(M, N, K):
+    g = gen(M, N)
+    x, w = ref.whole(M, K, g, DEV), ref.whole(N, K, g, DEV)
+    dy = torch.randint(-8, 9, (M, N), generator=g, device=DEV).bfloat16()
+    X, W = fp4_quantize(x), fp4_quantize(w)
+    X.scales[:, :, M:], W.scales[:, :, N:] = 255, 255
+    assert torch.equal(fp4_matmul(X, W, dtype=F32), (x.double() @ w.double().t()).float())
+    assert torch.equal(fp4_linear(x.bfloat16(), W, dtype=F32), (x.double() @ w.double().t()).float())
+    assert torch.equal(fp4_linear_dx(dy, W, dtype=F32), (dy.double() @ w.double()).float())
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 1030, 96), (33, 257, 352), (300, 130, 2880), (2050, 1001, 288)])
 def test_nothing_else_is_written(M, N, K):
     G = 4096
