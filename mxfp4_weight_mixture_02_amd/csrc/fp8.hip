@@ -18,7 +18,6 @@
 
 namespace mxmoe {
 
-
 // ---------------------------------------------------------------- quantizers
 
 // Eight consecutive elements of a row, zeros from `limit` on.  VEC: the row
@@ -300,6 +299,48 @@ __device__ __forceinline__ void fp8_to_bf16(const i32x8& c, uint32_t scale, bf16
 }
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
 
+// F consecutive outputs out[m][n ..], plus the bias; whole vectors where
+// the row allows it.
+template <int F, bool F32>
+__device__ __forceinline__ void fp8_store(const Fp8Gemm& g, int64_t m, int64_t n, float (&v)[F],
+                                          bool wide) {
+  if (m >= g.M || n >= g.N) return;
+  if (g.bias) {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+      if (n + i < g.N) v[i] += bf16_to_f32(g.bias[n + i]);
+  }
+  const int64_t at = m * g.N + n;
+  if (wide) {   // N % F == 0: the F values exist and are aligned
+    if constexpr (F == 2) {
+      if (F32)
+        *reinterpret_cast<f32x2*>(static_cast<float*>(g.out) + at) = f32x2{v[0], v[1]};
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + at) = pack_bf16x2(v[0], v[1]);
+    } else if constexpr (F32) {
+      f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
+#pragma unroll
+      for (int i = 0; i < F / 4; ++i) d[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    } else {
+      u32x2* d = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + at);
+      if (F == 8)
+        *reinterpret_cast<u32x4*>(d) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                             pack_bf16x2(v[F - 4], v[F - 3]), pack_bf16x2(v[F - 2], v[F - 1])};
+      else
+        d[0] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+    if (n + i < g.N) {
+      if (F32)
+        static_cast<float*>(g.out)[at + i] = v[i];
+      else
+        static_cast<uint16_t*>(g.out)[at + i] = (uint16_t)f32_to_bf16(v[i]);
+    }
+}
+
 // A workgroup's tile: WN x WM waves of (16 FN) x (16 FM), and NST LDS stages.
 // A stage holds one K block: BN rows of W and BM rows of X (128 bytes each),
 // X's BM scale bytes (room for 256) and W's scales (256 bytes).
@@ -350,6 +391,12 @@ template <class T, bool WROWS>
 __device__ __forceinline__ void fp8_copy(const Fp8Wave& g, uint32_t st, int kb) {
 #pragma unroll
   for (int i = 0; i <= T::LOADS; ++i) fp8_copy_piece<T, WROWS>(g, st, kb, i);
+}
+
+__device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p, int s0) {
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(p + s0);
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(p + (s0 ^ 16));
+  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
 // A K block's scales of this lane's rows: words of four bytes, or bytes.

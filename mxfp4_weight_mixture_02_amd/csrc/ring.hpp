@@ -1,5 +1,5 @@
 // What the tiled products share (fp8.hip, fp4.hip): direct-to-LDS copies and
-// the wait for them, fragments of 128-byte rows, the order of tiles, stores.
+// the wait for them, the order of rows in fragments and of tiles.
 #pragma once
 
 #include "common.hpp"
@@ -10,48 +10,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // MFMA row r of a wave's W fragments is matrix row fp8_pi(r) * F_N + fragment.
 __device__ __forceinline__ int fp8_pi(int r) { return 4 * (r & 3) + (r >> 2); }
-
-// F consecutive outputs out[m][n ..], plus the bias; whole vectors where
-// the row allows it.
-template <int F, bool F32, class G>
-__device__ __forceinline__ void fp8_store(const G& g, int64_t m, int64_t n, float (&v)[F],
-                                          bool wide) {
-  if (m >= g.M || n >= g.N) return;
-  if (g.bias) {
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-      if (n + i < g.N) v[i] += bf16_to_f32(g.bias[n + i]);
-  }
-  const int64_t at = m * g.N + n;
-  if (wide) {   // N % F == 0: the F values exist and are aligned
-    if constexpr (F == 2) {
-      if (F32)
-        *reinterpret_cast<f32x2*>(static_cast<float*>(g.out) + at) = f32x2{v[0], v[1]};
-      else
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + at) = pack_bf16x2(v[0], v[1]);
-    } else if constexpr (F32) {
-      f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
-#pragma unroll
-      for (int i = 0; i < F / 4; ++i) d[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-    } else {
-      u32x2* d = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + at);
-      if (F == 8)
-        *reinterpret_cast<u32x4*>(d) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                             pack_bf16x2(v[F - 4], v[F - 3]), pack_bf16x2(v[F - 2], v[F - 1])};
-      else
-        d[0] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < F; ++i)
-    if (n + i < g.N) {
-      if (F32)
-        static_cast<float*>(g.out)[at + i] = v[i];
-      else
-        static_cast<uint16_t*>(g.out)[at + i] = (uint16_t)f32_to_bf16(v[i]);
-    }
-}
 
 constexpr int FP8_RSRC_W3 = 0x00020000;   // raw buffer, untyped
 
@@ -100,14 +58,6 @@ __device__ __forceinline__ void fp8_wait(int blocks) {
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::COPIES, 0));
   else
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * T::COPIES, 0));
-}
-
-// A lane's two 16-byte chunks of a fragment's row: chunk s0 / 16 and the one
-// beside it.
-__device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p, int s0) {
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(p + s0);
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(p + (s0 ^ 16));
-  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
 // Tile `item` of the order in which bands of 8 m-tiles run through all
