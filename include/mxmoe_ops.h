@@ -290,6 +290,7 @@ int mxmoe_swiglu8_restore(const uint8_t* codes, const uint8_t* scales, int64_t R
  *  s^2 + eps); y = s rstd weight, formed in fp32: bf16 [T, H], or an 8-bit
  *  matrix with block_rows 1 (codes [T, Hp], scales [Hp / 128, T rounded up to
  *  16]), or both, each rounded once; what is not wanted is NULL.
+ * A row's bits depend on its values, on H and on whether T >= 1024.
  * weight [H] in w_dtype.  sum may be x or residual.  1 <= H <= 32768, T >= 1,
  * (T + 15) * Hp < 2^35 (and T <= 2^26 - 4 with H in 257 .. 384), eps > 0 and
  * finite; tensors aligned to their elements, codes 16-byte aligned. */

@@ -206,6 +206,19 @@ def test_a_nan_block_stays_in_its_row(M, N):
     assert torch.equal(torch.isnan(dx), cols.expand(M, K))
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 333, 352), (40, 1000, 96), (300, 130, 640), (2100, 320, 1100), (2100, 321, 1100)])
+def test_a_nan_gradient_stays_in_its_row(M, N, K):
+    g = gen(M, N, K)
+    w = ref.whole(N, K, g, DEV)
+    dy = torch.randint(-8, 9, (M, N), generator=g, device=DEV).bfloat16()
+    want = (dy.double() @ w.double()).float()
+    dy[1, 0], dy[3, N - 1], dy[M - 1, N - 1] = torch.nan, torch.nan, torch.nan
+    got = fp4_linear_dx(dy, fp4_quantize(w), dtype=F32)
+    bad = torch.zeros(M, dtype=torch.bool, device=DEV)
+    bad[[1, 3, M - 1]] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+
+
 @pytest.mark.parametrize("M", [1, 20, 40, 1100])
 @pytest.mark.parametrize("N,K", [(1, 40), (257, 352), (1001, 96), (1030, 288)])
 def test_scales_past_the_rows_are_not_used(M, N, K):
