@@ -1079,8 +1079,11 @@ hipError_t launch_bf16_gemm(const Fp4Gemm& g, hipStream_t s) {
 }
 
 // The gradient of few rows (above): rows of dY of a workgroup, parts of n and
-// time, fitted to the launches listed there, 2880 x 2880, 1000 x 8192, 8192 x 1024,
-// 336 x 4064, 8192 x 160, 512 x 512 and 4096 x 4096 with 1 to 1024 rows.
+// time, which is `c` us, `round` for each round of 256 workgroups, and in it `unit` for
+// each of a wave's units of n one after the other (`even` or `odd` more where dY's
+// rows are at such elements, not at eighths); the join of the parts has its own launch.
+// Fitted, like the copy's way below, to both ways' times at 806 sizes of 16 to 1024
+// rows, W from HBM of 64 to 12000 rows and columns, every kind of alignment.
 struct DxPlan {
   int mt, splits;
   float us;
@@ -1088,26 +1091,37 @@ struct DxPlan {
 static DxPlan dx_plan(int64_t M, int64_t N, int64_t K) {
   static constexpr struct {
     int mt;
-    float unit, c;
-  } SHAPE[] = {{1, 1.12f, 3.4f}, {2, 1.35f, 4.5f}, {4, 1.89f, 6.4f}};
+    float unit, even, odd, round, c;
+  } SHAPE[] = {{1, 0.81f, 0.09f, 0.19f, 0.42f, 3.3f},
+               {2, 1.125f, 0.20f, 0.54f, 2.5f, 2.35f},
+               {4, 1.43f, 0.32f, 1.41f, 5.9f, 1.45f}};
   const int64_t units = (N + 31) / 32, most = (units + DX_WAVES - 1) / DX_WAVES;
   DxPlan best{0, 0, 0.0f};
   for (const auto& t : SHAPE) {
     const int64_t items = ((K + 127) / 128) * ((M + 16 * t.mt - 1) / (16 * t.mt));
     const int64_t fill = 256 / items < 1 ? 1 : 256 / items, splits = fill < most ? fill : most;
-    float us = (float)((items * splits + 255) / 256) * (t.unit * (float)((most + splits - 1) / splits) + t.c);
-    if (splits > 1) us += 3.0f + (float)(splits * M * K) * 8.0f / 4.0e6f;
+    const float unit = t.unit + (N % 2 ? t.odd : N % 8 ? t.even : 0.0f);
+    float us = t.c + (float)((items * splits + 255) / 256) * (unit * (float)((most + splits - 1) / splits) + t.round);
+    if (splits > 1) us += 2.3f + 0.105f * (float)splits + (float)(splits * M * K) * 1.8e-6f;
     if (best.mt == 0 || us < best.us) best = {t.mt, (int)splits, us};
   }
   return best;
 }
-// Or by way of the copy, whose launch moves 2.5 N K bytes at 3.5 TB/s: over 80
-// random sizes of 48 to 1024 rows the choice is at most 4% slower than the better
-// way, but for two (15% and 47%).  Beyond 1024 rows the copy is a small part.
-bool fp4_dx_few(int64_t M, int64_t N, int64_t K, int out_f32) {
-  if (M > 1024) return false;
+// By way of the copy: its product, the copy, and dY's padding where it is needed.
+static float dx_copy_us(int64_t M, int64_t N, int64_t K, bool f32) {
   const int64_t np = fp8_up(N, 64);
-  return dx_plan(M, N, K).us < bf16_plan(M, K, np, out_f32 != 0).us + 6.0f + (float)(np * K) * 2.5f / 3.5e6f;
+  float us = 0.97f * bf16_plan(M, K, np, f32).us + 3.1f + (float)(np * K) * 0.86e-6f;
+  if (N != np) us += 1.95f + (float)(M * np) * 1.9e-6f;
+  return us;
+}
+// At 544 sizes beside the fitted ones the choice of way and workgroup is 0.9%
+// slower on average than the best of the four, over 5% slower at 39 of them and 38%
+// at the worst (986 x 256 x 5664, 23 us for 17).  5760 x 2880, from the codes and by way
+// of the copy: 512 rows 48 and 59 us, 768 rows 77 and 66.  Beyond 1024 rows the copy is
+// always made: at 2048 rows of 5760 x 2880 84 us for 120, but up to twice as slow
+// while W is small (1405 rows, 3104 x 96: 23.5 for 11.7).
+bool fp4_dx_few(int64_t M, int64_t N, int64_t K, int out_f32) {
+  return M <= 1024 && dx_plan(M, N, K).us < dx_copy_us(M, N, K, out_f32 != 0);
 }
 size_t fp4_dx_few_bytes(int64_t M, int64_t N, int64_t K) {
   const int s = dx_plan(M, N, K).splits;
