@@ -16,8 +16,12 @@
 // token (of the sigmoids too: logits below -88 keep their ratios), with the
 // hardware's base-2 exponential and reciprocal (1 ulp each; the argument's
 // rounding is 2^-24 of it, which the largest scores do not see): the library's
-// exponential and division took three quarters of the time.  Sums over a
-// workgroup's tokens are fp32, over workgroups fp64, in a fixed order.
+// exponential and division took three quarters of the time.  Squares of the
+// logsumexp, which fp32 may not hold though their mean is one, are formed and
+// summed in fp64.  Probabilities are summed in fp32 over a wave's tokens (up to 32 a
+// lane, then four lanes), in fp64 over waves, rounded to fp32 as a part and
+// summed in fp64 over the parts: 35 roundings of 2^-24 at most (in fp64 from a lane
+// on, 16384 x 256 took 4% longer).  The order of all sums is fixed.
 #include "balance.hpp"
 #include "common.hpp"
 
@@ -151,9 +155,9 @@ constexpr int BAL_WAVES = 8;               // waves of a workgroup: 32 tokens at
 // side.  Slot u has a workgroup of its own, which finds s: the last sequence
 // whose first slot is not behind u.
 struct BalanceWs {
-  float* p;         // [slots, E] sums of p
+  float* p;         // [slots, E] sums of p, rounded
   int32_t* c;       // [slots, E] choices
-  float* z;         // [slots] sums of lse^2
+  double* z;        // [slots] sums of lse^2
   int32_t* n;       // [slots] tokens
   double* seq;      // [S, 2] balance of a sequence, sum of lse^2
   int32_t* done;    // sequences that are finished: 0 from the parts' launch
@@ -171,7 +175,7 @@ template <int J, bool SIG, bool WHOLE, bool ONE>
 __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArgs a, BalanceWs ws, int per) {
   __shared__ float part[BAL_WAVES][256];
   __shared__ int hist[256];
-  __shared__ float zpart[BAL_WAVES];
+  __shared__ double zpart[BAL_WAVES];
   __shared__ int npart[BAL_WAVES];
   __shared__ double fin[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, row = tid >> 4;
@@ -197,7 +201,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
   for (int e = tid; e < 256; e += 64 * BAL_WAVES) hist[e] = 0;
   __syncthreads();
   float acc[J][4] = {};
-  float z = 0.0f;
+  double z = 0.0;
   int n = 0;
   for (int64_t t = lo + row; t < hi; t += 4 * BAL_WAVES) {   // a row's 16 lanes go together
     Logits<J> next;
@@ -211,7 +215,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][i] += q.p[j][i];
       if (pick >= 0 && pick < a.E) atomicAdd(&hist[pick], 1);
-      z = fmaf(q.lse, q.lse, z);
+      z += (double)q.lse * (double)q.lse;
       ++n;
     }
     x = next;
@@ -236,7 +240,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
     npart[wave] = n;
   }
   __syncthreads();
-  float pe = 0.0f, ze = 0.0f;
+  double pe = 0.0, ze = 0.0;
   int ne = 0;
 #pragma unroll
   for (int u = 0; u < BAL_WAVES; ++u) {
@@ -246,7 +250,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
   }
   if constexpr (!ONE) {
     if (tid < a.E) {
-      ws.p[(int64_t)slot * a.E + tid] = pe;
+      ws.p[(int64_t)slot * a.E + tid] = (float)pe;
       ws.c[(int64_t)slot * a.E + tid] = hist[tid];
     }
     if (tid == 0) {
@@ -256,7 +260,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_part_kernel(BalanceArg
   } else {
     double w = 0.0;
     if (tid < a.E) {
-      const double mean = ne ? (double)pe / ne : 0.0;
+      const double mean = ne ? pe / ne : 0.0;
       a.counts[tid] = hist[tid];
       a.prob[tid] = (float)mean;
       w = hist[tid] * mean;
@@ -300,7 +304,7 @@ __global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceArgs a, Balanc
   double p = 0.0, z = 0.0;
   int c = 0, n = 0;
   for (int64_t b = b0 + tid; b < b1; b += 1024) {
-    z += (double)ws.z[b + s];
+    z += ws.z[b + s];
     n += ws.n[b + s];
   }
   if (e < a.E) {
@@ -512,7 +516,7 @@ static size_t balance_layout(int64_t T, int E, int S, void* base, BalanceWs* ws)
   w.done = reinterpret_cast<int32_t*>(take(4));
   w.p = reinterpret_cast<float*>(take(slots * E * 4));
   w.c = reinterpret_cast<int32_t*>(take(slots * E * 4));
-  w.z = reinterpret_cast<float*>(take(slots * 4));
+  w.z = reinterpret_cast<double*>(take(slots * 8));
   w.n = reinterpret_cast<int32_t*>(take(slots * 4));
   if (ws) *ws = w;
   return at;
