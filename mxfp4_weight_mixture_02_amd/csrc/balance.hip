@@ -398,10 +398,10 @@ __global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceArgs a, Balanc
 //
 // dlogits: 16 tokens at a time in a workgroup, `per` in all.  A wave looks its
 // first token's sequence up, and those of the rows whose tokens lie behind it.
+// add may be dlogits: a lane reads its elements before it writes them.
 template <int J, bool SIG, bool WHOLE>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a, const float* __restrict__ dlosses,
-                                                          const float* __restrict__ add,
-                                                          float* __restrict__ dlogits, int per) {
+                                                          const float* add, float* dlogits, int per) {
   __shared__ int all[4], some[4];
   const int tid = threadIdx.x, l = tid & 15, row = tid >> 4;
   const int64_t first = (int64_t)blockIdx.x * per, t1 = min(first + per, a.T);
