@@ -451,7 +451,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
   v.xoff = (T::BN + wm * 16 * FM + r) * 128;
   v.s0 = fp4_slot(r, 2 * q) << 4;
   v.sxoff = T::SX + q * 2 * T::BM + 2 * (wm * 16 * FM + r * FM);
-  v.swoff = T::SW + q * 2 * T::BN + 2 * (wn * 16 * FN + fp8_pi(r) * FN);
+  v.swoff = T::SW + q * 2 * T::BN + 2 * (wn * 16 * FN + w_row(r) * FN);
   const int all = (int)(xp / 128);   // X's rows are whole K blocks
   // Sets out the copies of item `item` (with splits, every tile's parts one
   // after the other).
@@ -460,7 +460,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
     w.split = PARTS ? item % splits : 0;
     w.tile = PARTS ? item / splits : item;
     int nt, mt;
-    fp8_tile_at(first + w.tile, ntiles, mtiles, nt, mt);
+    tile_at(first + w.tile, ntiles, mtiles, nt, mt);
     w.n0 = (int64_t)nt * T::BN;
     w.m0 = (int64_t)mt * T::BM;
     w.kb0 = PARTS ? (int)((int64_t)all * w.split / splits) : 0;
@@ -477,7 +477,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
       const bool isw = p < T::BN / 8;
       const int at = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);   // LDS row of the operand
       const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
-      const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
+      const int row = isw ? f / FN * 16 * FN + w_row(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
       v.off[i] = (uint32_t)min(row, (isw ? w.nrows : w.mrows) - 1) * (uint32_t)(isw ? g.wp : xp) +
                  (uint32_t)w.kb0 * 128 + (fp4_slot(fr, lane & 7) << 4);
     }
@@ -517,7 +517,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp4_gemm_kernel(Fp4Gemm g, int64_t
 #pragma unroll
       for (int i = 0; i < T::COPIES; ++i) fp4_copy_piece<T>(v, k * T::STAGE, min(k, left - 1), i);
     }
-  fp8_wait<T>((SEVERAL ? NST : min(NST, left)) - 1);
+  ring_wait<T>((SEVERAL ? NST : min(NST, left)) - 1);
   barrier_only();
   Fp4Frags<T> f;
   if (T::FP4) f.c = fp4_scales<T>(v, lds);

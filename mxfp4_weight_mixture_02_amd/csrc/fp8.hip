@@ -429,7 +429,7 @@ __device__ __forceinline__ void fp8_loop(const Fp8Wave& g, int kblocks, const ui
     if (k < kblocks) fp8_copy<T, WROWS>(g, k * T::STAGE, k);
   int st = 0;
   for (int kb = 0; kb < kblocks; ++kb) {
-    fp8_wait<T>(min(T::NST - 1, kblocks - kb) - 1);
+    ring_wait<T>(min(T::NST - 1, kblocks - kb) - 1);
     barrier_only();
     const uint32_t prev = st == 0 ? LAST - T::STAGE : st - T::STAGE;
     const bool more = kb + T::NST - 1 < kblocks;
@@ -525,7 +525,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
     const int item = x * base + min(x, extra) + (b >> 3);
     split = item % splits;
     tile = item / splits;
-    fp8_tile_at(first + tile, ntiles, mtiles, nt, mt);
+    tile_at(first + tile, ntiles, mtiles, nt, mt);
   }
   const int64_t n0 = (int64_t)nt * T::BN, m0 = (int64_t)mt * T::BM;
   const int64_t pitch = fp8_pitch(g.K);
@@ -543,7 +543,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
     const bool isw = p < T::BN / 8;
     const int at = 8 * (isw ? p : p - T::BN / 8) + (lane >> 3);   // LDS row of the operand
     const int fr = at & 15, f = at >> 4;                          // its fragment row and fragment
-    const int row = isw ? f / FN * 16 * FN + fp8_pi(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
+    const int row = isw ? f / FN * 16 * FN + w_row(fr) * FN + f % FN : f / FM * 16 * FM + fr * FM + f % FM;
     v.off[i] = (uint32_t)min(row, (isw ? nrows : mrows) - 1) * (uint32_t)pitch + (uint32_t)kb0 * 128 +
                (((lane & 7) ^ ((fr >> 1) & 7)) << 4);
   }
@@ -565,7 +565,7 @@ __global__ __launch_bounds__(64 * T::NW) void fp8_gemm_kernel(Fp8Gemm g, int nti
   v.xoff = (T::BN + wm * 16 * FM + r) * 128;
   v.s0 = ((2 * q) ^ ((r >> 1) & 7)) << 4;
   v.sxoff = T::SX + wm * 16 * FM + r * FM;
-  v.swoff = T::SW + (WROWS ? wn * 16 * FN + fp8_pi(r) * FN : wn * 16 * FN / 128 * 4);
+  v.swoff = T::SW + (WROWS ? wn * 16 * FN + w_row(r) * FN : wn * 16 * FN / 128 * 4);
   f32x4 acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
@@ -613,7 +613,7 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm g, int ntiles, in
   const int per = bn * bm / 1024, tile = blockIdx.x / per;
   const int i = (blockIdx.x % per * 256 + threadIdx.x) * 4;   // in the tile
   int nt, mt;
-  fp8_tile_at(first + tile, ntiles, mtiles, nt, mt);
+  tile_at(first + tile, ntiles, mtiles, nt, mt);
   const int64_t m = (int64_t)mt * bm + i / bn, n = (int64_t)nt * bn + i % bn;
   if (m >= g.M || n >= g.N) return;
   const float* p = g.part + (int64_t)tile * bn * bm + i;

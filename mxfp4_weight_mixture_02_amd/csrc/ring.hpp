@@ -8,16 +8,16 @@ namespace mxmoe {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// MFMA row r of a wave's W fragments is matrix row fp8_pi(r) * F_N + fragment.
-__device__ __forceinline__ int fp8_pi(int r) { return 4 * (r & 3) + (r >> 2); }
+// MFMA row r of a wave's W fragments is matrix row w_row(r) * F_N + fragment.
+__device__ __forceinline__ int w_row(int r) { return 4 * (r & 3) + (r >> 2); }
 
-constexpr int FP8_RSRC_W3 = 0x00020000;   // raw buffer, untyped
+constexpr int RAW_BUFFER_W3 = 0x00020000;   // raw buffer, untyped
 
 // Copy from global memory to LDS: 16, 4 or 1 bytes a lane from base + off +
 // soff to LDS address lds + (16, 4, 4) * lane.  As assembly, because the
 // compiler makes every later LDS read wait for every such copy in flight
 // that it cannot prove to go elsewhere, and with a ring of stages it can
-// prove nothing.  The kernel waits itself (fp8_wait) before it reads a
+// prove nothing.  The kernel waits itself (ring_wait) before it reads a
 // stage.  A copy has no output register; its address is read at issue.  m0
 // is a reserved register, which the compiler writes right before each use of
 // its own: the clobber keeps such a pair on one side of a copy (none of these
@@ -42,13 +42,13 @@ __device__ __forceinline__ u32x4 buffer_of(const uint8_t* p, int64_t bytes) {
   const uint64_t a = (uint64_t)(uintptr_t)p;
   return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)FP8_RSRC_W3};
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)RAW_BUFFER_W3};
 }
 
 // Wait until at most `blocks` K blocks' copies of this wave are under way,
 // and for all its LDS reads.
 template <class T>
-__device__ __forceinline__ void fp8_wait(int blocks) {
+__device__ __forceinline__ void ring_wait(int blocks) {
   // a constant for every count that a ring of up to 4 stages has
   if (blocks <= 0)
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
@@ -62,7 +62,7 @@ __device__ __forceinline__ void fp8_wait(int blocks) {
 
 // Tile `item` of the order in which bands of 8 m-tiles run through all
 // n-tiles, m fastest.
-__device__ __forceinline__ void fp8_tile_at(int item, int ntiles, int mtiles, int& nt, int& mt) {
+__device__ __forceinline__ void tile_at(int item, int ntiles, int mtiles, int& nt, int& mt) {
   const int band = item / (8 * ntiles), rows = min(8, mtiles - 8 * band);
   const int local = item - band * 8 * ntiles;
   mt = band * 8 + local % rows;
