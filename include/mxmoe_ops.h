@@ -100,7 +100,8 @@ int mxmoe_router_logits(int64_t T, int64_t H, int32_t E, const uint16_t* x, cons
  *  losses    fp32 [2]: the mean over the S+ sequences of E sum_e counts / (k
  *            N_s) prob (1 when all is even), and the mean over the N tokens of
  *            logsumexp(logits)^2 (0 for a token of -inf alone)
- * Without tokens all are 0.  Counts are exact, sums in a fixed order.
+ * Without tokens all are 0.  Counts are exact, sums in a fixed order.  p is formed
+ * in fp32: of a logit d below the token's largest to (3 d + 32) 2^-24 of itself.
  * workspace: mxmoe_balance_workspace_bytes. */
 int mxmoe_balance(int score, int64_t T, int32_t E, int32_t k, int32_t S, const float* logits,
                   const int32_t* topk_idx, const uint8_t* mask, const int32_t* offsets, float* losses,

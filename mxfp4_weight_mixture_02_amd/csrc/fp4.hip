@@ -775,10 +775,13 @@ __global__ __launch_bounds__(256) void fp4_dequant_t_kernel(const uint8_t* __res
 // part of fragment t; dY's rows are the other operand.  A workgroup has 128 columns,
 // 16 rows of dY and a part of n, which its waves share in units of 32; their sums
 // meet in LDS and those of the parts in another launch, in their order.  Bound
-// by the arithmetic that decodes W (32 conversions and 32 permutations for 8
-// MT products), by HBM and the second launch for few rows (us, W 5760 x 2880 from
-// HBM; by way of the copy): 1 row 9.0 (24), 16 rows 10 (28), 64 rows 15 (28), 256
-// rows 33 (48), 512 rows 49 (59).  Units read two and more ahead: no gain.
+// by the loads' round trips: a wave asks for its next unit behind a unit's
+// products and decodes it at once, and a CU has one workgroup, two waves a SIMD.
+// By counters (W 5760 x 2880, 256 rows, 26.6 us) a wave waits for 53% of its time and
+// issues vector instructions in 23%, the matrix cores are busy 17%, and HBM gives 1.0
+// TB/s (16 rows: 61%, 19%, 4%, 0.7 TB/s).  Both launches, us (by way of the
+// copy): 1 row 9.0 (24), 16 rows 10 (28), 64 rows 15 (28), 256 rows 33 (48), 512
+// rows 48 (59).  Units read two and more ahead brought no gain.
 template <int MT>
 struct DxUnit {
   uint32_t w[8];

@@ -7,9 +7,9 @@
 //   dx = rstd (w dy - xhat mean(w dy xhat)) + ds,  dw = sum over rows of dy xhat,
 //   xhat = s rstd
 //
-// One pass over the data: a row lives in the registers of LR lanes (16 to 1024),
-// C chunks of 8 elements each, so that 16 lanes side by side hold one
-// 128-element block of the 8-bit result.  Squares, means and the weight's gradient are
+// One pass over the data (but for the gradient of more than 16384 columns): a row
+// lives in the registers of LR lanes (16 to 1024), C chunks of 8 elements each, so
+// that 16 lanes side by side hold one 128-element block of the 8-bit result.  Squares, means and the weight's gradient are
 // summed in fp32; everything is rounded once, when it is stored.
 #include "common.hpp"
 #include "fp8.hpp"
@@ -137,7 +137,9 @@ constexpr int norm_block(int lr) { return lr < 256 ? 256 : lr; }
 
 // A row for LR lanes; 256 threads a workgroup, or LR where that is more.  Bound
 // by HBM: 16381 x 2880 bf16 with the residual, both results: 85 us, 5.0 TB/s;
-// 2047 x 2880 fp32, bf16 result: 15.5 us, 5.3 TB/s.  One row: 3.6 us.
+// 2047 x 2880 fp32, bf16 result: 15.5 us, 5.3 TB/s; 4096 x 16384 bf16 121 us and
+// 4096 x 32768 238, 5.0 TB/s; below some 4000 rows of 2880 by the launch and its
+// one round of loads (1024 rows 11 us, 2.4 TB/s).  One row: 3.6 us.
 template <bool F32, bool WHOLE, int LR, int C>
 __global__ __launch_bounds__(norm_block(LR)) void norm_kernel(NormArgs a) {
   __shared__ double slots[LR < 64 ? 1 : LR / 64];
@@ -211,11 +213,14 @@ __global__ __launch_bounds__(norm_block(LR)) void norm_kernel(NormArgs a) {
 // sums its columns' part of dw over its rows, the workgroup's waves add theirs
 // in order through LDS, and the parts [workgroups][H] are joined by another
 // launch (one workgroup writes dw itself).  Bound by HBM: 16384 x 2880 bf16
-// with the sum's own gradient in 77.8 us (4.8 TB/s), the join 5.5.
+// with the sum's own gradient in 77.8 us (4.8 TB/s), the join 5.5; both together
+// 4096 x 16384 118 us (4.6 TB/s).  Of more than 16384 columns a row is read twice, for
+// a workgroup's 1024 threads have 128 registers each, and of these 28 to 53 still
+// go to scratch memory: 4096 x 32768 bf16 300 us, 3.6 TB/s (fp32 510, 3.7).
 template <bool F32, bool WHOLE, int LR, int C>
 __global__ __launch_bounds__(norm_block(LR)) void norm_bwd_kernel(NormArgs a) {
   constexpr int ROWS = norm_block(LR) / LR;   // rows at a time
-  constexpr bool LATE = C > 2;   // a row is read twice, chunk by chunk: 1024 threads have 128 registers each
+  constexpr bool LATE = C > 2;   // a row is read twice, chunk by chunk
   __shared__ double slots[LR < 64 ? 1 : LR / 64];
   __shared__ float add[ROWS == 1 ? 1 : C * LR * 8];
   const int lane = threadIdx.x & 63, all = threadIdx.x >> 6, wave = all % (LR < 64 ? 1 : LR / 64);
@@ -369,8 +374,9 @@ int64_t norm_blocks(int64_t T, int64_t H) {
 }
 // Workgroups: all that the card holds for many rows; a third as many as groups
 // of rows, but one for each CU, while their parts of dw weigh as much as the rows
-// (2880 columns, us: 700 rows, 256 workgroups 11.6, 700 14.4; 2047 rows, 1024
-// workgroups 18.4, 256 23.4).
+// (2880 columns, both launches, us: 700 rows, 256 workgroups 11.5, 700 14.0; 1024
+// rows, the rule's 341 14.4, 256 13.3, 1024 16.2; 2047 rows, the rule's 682 20.2, 256
+// 23.9, 1024 19.1).
 static unsigned norm_bwd_grid(int64_t T, int64_t H) {
   const int lr = norm_bwd_shape(H).lr, block = norm_block(lr);
   const int64_t groups = (T + block / lr - 1) / (block / lr), most = 4 * 65536 / block;

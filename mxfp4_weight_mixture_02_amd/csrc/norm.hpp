@@ -24,7 +24,8 @@ struct NormArgs {
   float* dw;                // backward: fp32 [H]
   float* part;              // norm_part_bytes of scratch
 };
-// workgroups of a forward launch (no backward one has more) and their threads
+// workgroups of a forward launch and their threads (a backward one has at most
+// 1024 workgroups)
 int64_t norm_blocks(int64_t T, int64_t H);
 int norm_threads(int64_t T, int64_t H);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
